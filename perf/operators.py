@@ -88,7 +88,8 @@ def _grid(gen, shape, sigma, most):
 
 def _float_inputs(case, seed):
     """W and h on the grid; each hidden row leans, by a random amount, to the
-    token it is scored with, as a trained head's rows do."""
+    token it is scored with, as a trained head's rows do (its probability
+    ranges from that of any other token to about a third)."""
     B, V, d = case["B"], case["V"], case["d"]
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
@@ -96,7 +97,8 @@ def _float_inputs(case, seed):
     w_step = 2.0 ** -round(math.log2(math.sqrt(d) * 16 / 2.5))   # logits of deviation about 2.5
     W = _grid(gen, (V, d), 16.0, 63.0)
     targets = torch.randint(V, (B,), generator=gen, device="cuda", dtype=torch.int32)
-    lean = torch.rand((B, 1), generator=gen, device="cuda") * (4.0 / math.sqrt(d))
+    most = (math.log(V) + 1.0) * case["T"] / (H_STEP * w_step * d * 16.0 ** 2)
+    lean = torch.rand((B, 1), generator=gen, device="cuda") * most
     h = torch.randn((B, d), generator=gen, device="cuda") * 8.0 + lean * W[targets.long()]
     h = h.round_().clamp_(-31.0, 31.0)
     gone = torch.rand((B,), generator=gen, device="cuda") < case["masked"]
@@ -142,7 +144,7 @@ def prepare(case, seed):
         if case["op"] == "gradient":
             # what the scoring call of the same step left behind
             dlogp, dentropy = _loss_gradients(case, gen)
-            stats = _plain_stats(_plain_logits(h, W) / case["T"])
+            stats = _plain_stats(_plain_logits(h, W) / case["T"])[0]
             state.update(dlogp=dlogp, dentropy=dentropy, lse=stats["lse"],
                          entropy=stats["entropy"])
     if own:
@@ -173,7 +175,8 @@ def _plain_stats(z):
     e = torch.exp(t)
     s = e.sum(dim=1)
     u = (e * t).sum(dim=1)
-    return {"lse": m[:, 0] + torch.log(s), "entropy": torch.log(s) - u / s}
+    log_s = torch.log(s)
+    return {"lse": m[:, 0] + log_s, "entropy": log_s - u / s}, m, log_s[:, None]
 
 
 def _plain_top(z, K):
@@ -190,14 +193,14 @@ def _plain_score(s):
     case = s["case"]
     raw = _plain_logits(s["h"], s["W"])
     z = raw / case["T"]
-    out = _plain_stats(z)
+    out, m, log_s = _plain_stats(z)
     t = s["targets"].long()
-    zt = z.gather(1, t.clamp_min(0)[:, None])[:, 0]
-    out["logp"] = torch.where(t >= 0, zt - out["lse"], torch.zeros_like(zt))
+    logp = (z.gather(1, t.clamp_min(0)[:, None]) - m - log_s)[:, 0]
+    out["logp"] = torch.where(t >= 0, logp, torch.zeros_like(logp))
     if case["K"]:
         top = _plain_top(raw, case["K"])
         out["top_token"] = top.int()
-        out["top_logp"] = z.gather(1, top) - out["lse"][:, None]
+        out["top_logp"] = z.gather(1, top) - m - log_s
     return out
 
 
