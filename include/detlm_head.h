@@ -54,7 +54,7 @@ typedef enum {
   DETLM_BF16 = 0,   /* bf16 W and h, fp32 accumulation, fp32 logits        */
   DETLM_FP16 = 1,   /* IEEE fp16 W and h, fp32 accumulation, fp32 logits   */
   DETLM_INT8 = 2,   /* int8 W and h, exact int32 accumulation and logits   */
-  DETLM_FP32 = 3    /* fp32 rows: input of the integer front end only      */
+  DETLM_FP32 = 3    /* fp32 rows into the integer front end, scaled logits */
 } detlm_dtype_t;
 
 typedef enum {
@@ -259,6 +259,101 @@ int detlm_head_greedy_host_async(detlm_head_t* head, const void* h_host,
 int detlm_head_logprob_host_async(detlm_head_t* head, const void* h_host,
                                   const int32_t* targets_host, int64_t B,
                                   float* logp_host, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Scores: log-probabilities of given tokens with the entropy of the row's
+ * distribution and its most likely tokens; their gradient; and the scaled
+ * logits of an int8 head.
+ * ------------------------------------------------------------------------ */
+
+#define DETLM_NO_TARGET (-1)   /* a row with no token to score (padding)      */
+#define DETLM_MAX_TOP 32       /* most likely tokens a row can return         */
+
+/* Score B hidden rows h_dev [B, d] (BF16/FP16 heads; INT8:
+ * DETLM_EUNSUPPORTED). With z = h . W^T, p = softmax(z / T):
+ *
+ * logp_dev float [B]:    log p of targets_dev[n]; 0 where the target is
+ *                        DETLM_NO_TARGET; NaN, with DETLM_ETARGET in the
+ *                        error word, where it is outside [0, V) otherwise.
+ *                        Both pointers NULL: no token is scored.
+ * entropy_dev float [B]: -sum_v p_v log p_v (natural logarithm); may be NULL.
+ * lse_dev float [B]:     log sum_v exp(z_v / T); may be NULL.
+ * top_token_dev int32 [B, top_k], top_logp_dev float [B, top_k]: the top_k
+ *                        most likely tokens and their log-probabilities, the
+ *                        most likely first, the lowest index first among
+ *                        equal logits. top_k = 0: not written. A row with
+ *                        fewer logits that are numbers: -1 and NaN behind them.
+ *
+ * temperature T: finite and > 0. 0 <= top_k <= min(DETLM_MAX_TOP, V).
+ * A row of NaN or infinite logits gives NaN.
+ * The logits are those of the other calls, and every sum runs in an order set
+ * by V alone, so a row's outputs are the same bits for any B and any co-rows.
+ * "batch-logprob-gap": the trainer's per-token log-probability; "Inference
+ * and Decoding", section 3, Temperature. B == 0 is a no-op; h_dev 16-byte
+ * aligned, the other arrays 4-byte aligned. */
+int detlm_head_score(detlm_head_t* head, const void* h_dev,
+                     const int32_t* targets_dev, int64_t B, int top_k,
+                     float temperature, float* logp_dev, float* entropy_dev,
+                     float* lse_dev, int32_t* top_token_dev,
+                     float* top_logp_dev, cudaStream_t stream);
+
+/* Workspace for score calls of up to max_B rows and top_k alternatives
+ * (these then allocate nothing). Optional, like detlm_head_reserve. */
+int detlm_head_reserve_score(detlm_head_t* head, int64_t max_B, int top_k);
+
+/* Gradient of detlm_head_score's logp and entropy (BF16/FP16 heads). With
+ * lse_dev and entropy_dev of the score call on the same h, W, targets and T,
+ * and dlogp_dev, dentropy_dev float [B] the loss's gradients with respect to
+ * logp and entropy:
+ *
+ *   dz[n, v] = (dlogp[n] ([v = target n] - p) - dentropy[n] p (log p + H)) / T
+ *   dh_dev [B, d] = dz . W,   dW_dev [V, d] = dz^T . h
+ *
+ * in the head's type, overwritten. dentropy_dev NULL: no entropy term
+ * (entropy_dev is then not read). A row whose target is DETLM_NO_TARGET, or
+ * outside [0, V), has no dlogp term. dh_dev or dW_dev may be NULL; both
+ * 16-byte aligned device memory. B == 0 sets dW_dev to zero.
+ * dz is held in the head's type between the products (for FP16 heads times a
+ * power of two set by the largest |dlogp| and |dentropy| of the call), sums
+ * run in fp32 in a fixed order without atomics; dh of a row is the same bits
+ * for any B and any co-rows (FP16 heads: up to that power of two's effect on
+ * terms 2^24 times smaller than the call's largest). */
+int detlm_head_score_backward(detlm_head_t* head, const void* h_dev,
+                              const int32_t* targets_dev, int64_t B,
+                              float temperature, const float* lse_dev,
+                              const float* entropy_dev, const float* dlogp_dev,
+                              const float* dentropy_dev, void* dh_dev,
+                              void* dW_dev, cudaStream_t stream);
+
+/* Workspace for gradient calls of up to max_B rows: dz, 2 B bytes per
+ * vocabulary entry (in passes over the vocabulary above about 8 GB), and the
+ * fp32 partial sums of dh. */
+int detlm_head_reserve_backward(detlm_head_t* head, int64_t max_B);
+
+/* To be called after W was changed in place on `stream` (by an optimizer,
+ * say), before the next call of this head: the calls request parts of W before
+ * the stream's earlier kernels have finished, and an INT8 head keeps a
+ * converted copy. Score calls of more than 128 rows and gradient calls of
+ * BF16/FP16 heads read W in stream order and do not need it. */
+int detlm_head_weights_changed(detlm_head_t* head, cudaStream_t stream);
+
+/* Scaled logits of an INT8 head ("Eliminating Nondeterminism in LLM Inference
+ * with Integer-Only Arithmetic", section DetLLM: each token is quantized from
+ * its own values): one scale for each token and each channel,
+ *
+ *   out[n, v] = (sum_k q[n, k] W[v, k]) * (x_scale[n] * w_scale[v])
+ *
+ * q_dev int8 [B, d]; x_scale_dev float [B]; w_scale_dev float [V]; out_dev
+ * [B, V] of out_dtype (DETLM_FP32, DETLM_BF16 or DETLM_FP16). The integer
+ * sum is exact; it, the product of the scales and their product are rounded
+ * once each to fp32, then once to out_dtype. Other heads:
+ * DETLM_EUNSUPPORTED. B == 0 is a no-op; q_dev 16-byte aligned, out_dev
+ * aligned to its element (rows that start on 16-byte boundaries are written
+ * fastest). Rows are the same bits for any B. */
+int detlm_head_scaled_logits(detlm_head_t* head, const int8_t* q_dev,
+                             const float* x_scale_dev, const float* w_scale_dev,
+                             int64_t B, int out_dtype, void* out_dev,
+                             cudaStream_t stream);
 
 /* Wait for the stream and for the copies of the handle's pending
  * asynchronous host-buffer calls, read and clear the handle's device error

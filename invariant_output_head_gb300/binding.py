@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib",
                          "libdetlm_head.so")
@@ -18,6 +19,8 @@ DTYPES = {"bf16": DETLM_BF16, "fp16": DETLM_FP16, "int8": DETLM_INT8}
 DETLM_OK, DETLM_EINVAL, DETLM_EUNSUPPORTED, DETLM_ECUDA = 0, -1, -2, -3
 DETLM_ETIMEOUT, DETLM_ENOMEM, DETLM_ETARGET = -4, -5, -6
 DETLM_DEBUG_STALL = 1
+DETLM_NO_TARGET = -1
+DETLM_MAX_TOP = 32
 
 _vp, _i64, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
 _SIGS = {
@@ -29,6 +32,14 @@ _SIGS = {
     "detlm_head_greedy_gated": (_i32, [_vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp, _vp, _vp,
                                        _vp]),
     "detlm_head_sample": (_i32, [_vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "detlm_head_score": (_i32, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                _vp, _vp]),
+    "detlm_head_reserve_score": (_i32, [_vp, _i64, _i32]),
+    "detlm_head_score_backward": (_i32, [_vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp]),
+    "detlm_head_reserve_backward": (_i32, [_vp, _i64]),
+    "detlm_head_weights_changed": (_i32, [_vp, _vp]),
+    "detlm_head_scaled_logits": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp]),
     "detlm_quantize_rows": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_from_float": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_host": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
@@ -152,6 +163,44 @@ def detlm_head_sample(handle, h_ptr, B, temperature, seeds_ptr, positions_ptr, t
                                             positions_ptr, token_ptr, score_gap_ptr, logits_ptr,
                                             stream),
            "detlm_head_sample")
+
+
+def detlm_head_score(handle, h_ptr, targets_ptr, B, top_k, temperature, logp_ptr, entropy_ptr,
+                     lse_ptr, top_token_ptr, top_logp_ptr, stream) -> None:
+    _check(load_library().detlm_head_score(handle, h_ptr, targets_ptr, B, top_k, temperature,
+                                           logp_ptr, entropy_ptr, lse_ptr, top_token_ptr,
+                                           top_logp_ptr, stream),
+           "detlm_head_score")
+
+
+def detlm_head_reserve_score(handle, max_B, top_k) -> None:
+    _check(load_library().detlm_head_reserve_score(handle, max_B, top_k),
+           "detlm_head_reserve_score")
+
+
+def detlm_head_score_backward(handle, h_ptr, targets_ptr, B, temperature, lse_ptr, entropy_ptr,
+                              dlogp_ptr, dentropy_ptr, dh_ptr, dW_ptr, stream) -> None:
+    _check(load_library().detlm_head_score_backward(handle, h_ptr, targets_ptr, B, temperature,
+                                                    lse_ptr, entropy_ptr, dlogp_ptr,
+                                                    dentropy_ptr, dh_ptr, dW_ptr, stream),
+           "detlm_head_score_backward")
+
+
+def detlm_head_reserve_backward(handle, max_B) -> None:
+    _check(load_library().detlm_head_reserve_backward(handle, max_B),
+           "detlm_head_reserve_backward")
+
+
+def detlm_head_weights_changed(handle, stream) -> None:
+    _check(load_library().detlm_head_weights_changed(handle, stream),
+           "detlm_head_weights_changed")
+
+
+def detlm_head_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr, B, out_dtype, out_ptr,
+                             stream) -> None:
+    _check(load_library().detlm_head_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr, B,
+                                                   out_dtype, out_ptr, stream),
+           "detlm_head_scaled_logits")
 
 
 def detlm_quantize_rows(x_ptr, dtype, B, d, q_ptr, mult_ptr, shift_ptr, stream) -> None:
@@ -278,10 +327,30 @@ def detlm_merge_logprob_shards(recs_ptr, P, B, V, targets_ptr, logp_ptr, err_ptr
 
 # ---- torch convenience wrapper ------------------------------------------
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream_ptr(stream) -> int:
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+class Score(NamedTuple):
+    """What Head.score returns (and the buffers it can be given as `out`)."""
+    logp: object        # float32 [B] (None without targets)
+    entropy: object     # float32 [B]
+    lse: object         # float32 [B]
+    top_token: object   # int32 [B, top_k] (None when top_k is 0)
+    top_logp: object    # float32 [B, top_k]
+
+
+def _vector(t, name, B, dtype, device):
+    """A contiguous 1-D CUDA tensor of B values, or a ValueError."""
+    if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != B \
+            or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{B}]")
 
 
 class Head:
@@ -349,6 +418,116 @@ class Head:
         detlm_head_logprob(self.handle, h.data_ptr(), targets.data_ptr(), B, logp.data_ptr(),
                            _stream_ptr(stream))
         return logp
+
+    def score_buffers(self, B: int, top_k: int = 0, targets: bool = True) -> Score:
+        """Output buffers for score calls of B rows (pass them as `out`)."""
+        import torch
+        f32 = dict(dtype=torch.float32, device=self.W.device)
+        top = (torch.empty((B, top_k), dtype=torch.int32, device=self.W.device) if top_k else None)
+        return Score(torch.empty(B, **f32) if targets else None, torch.empty(B, **f32),
+                     torch.empty(B, **f32), top, torch.empty((B, top_k), **f32) if top_k else None)
+
+    def score(self, h, targets=None, top_k: int = 0, temperature: float = 1.0, stream=None,
+              out: Score | None = None) -> Score:
+        """Log-probability of targets int32 [B] (DETLM_NO_TARGET: nothing to
+        score, 0), entropy and log-sum-exp of each row's distribution at the
+        given temperature, and its top_k most likely tokens with their
+        log-probabilities (detlm_head_score)."""
+        import torch
+        self._check_h(h)
+        B = int(h.shape[0])
+        if targets is not None:
+            _vector(targets, "targets", B, torch.int32, h.device)
+        if out is None:
+            out = self.score_buffers(B, top_k, targets is not None)
+        else:
+            for name, t in (("out.logp", out.logp), ("out.entropy", out.entropy),
+                            ("out.lse", out.lse)):
+                if t is not None:
+                    _vector(t, name, B, torch.float32, h.device)
+            if (out.logp is None) != (targets is None):
+                raise ValueError("out.logp goes with targets")
+            if top_k:
+                for t, dt in ((out.top_token, torch.int32), (out.top_logp, torch.float32)):
+                    if t is None or t.dtype != dt or tuple(t.shape) != (B, top_k) \
+                            or not t.is_contiguous() or t.device != h.device:
+                        raise ValueError("out.top_token and out.top_logp must be contiguous "
+                                         f"[{B}, {top_k}] tensors")
+        ptr = _ptr
+        detlm_head_score(self.handle, h.data_ptr(), ptr(targets), B, top_k, temperature,
+                         ptr(out.logp), ptr(out.entropy), ptr(out.lse),
+                         ptr(out.top_token) if top_k else None,
+                         ptr(out.top_logp) if top_k else None, _stream_ptr(stream))
+        return out
+
+    def reserve_score(self, max_B: int, top_k: int = 0) -> None:
+        """Workspace for score calls of up to max_B rows and top_k alternatives."""
+        detlm_head_reserve_score(self.handle, int(max_B), int(top_k))
+
+    def score_backward(self, h, targets, lse, entropy, dlogp, dentropy=None,
+                       temperature: float = 1.0, need_dh: bool = True, need_dW: bool = True,
+                       stream=None, out=None):
+        """Gradients (dh [B, d], dW [V, d]) in the head's type of a loss whose
+        gradients with respect to score's logp and entropy are dlogp and
+        dentropy, float32 [B] (detlm_head_score_backward). lse and entropy are
+        what score returned. One that is not needed is None."""
+        import torch
+        self._check_h(h)
+        B = int(h.shape[0])
+        if h.dtype != self.W.dtype:
+            raise ValueError("h must have the head's dtype")
+        _vector(targets, "targets", B, torch.int32, h.device)
+        for name, t in (("lse", lse), ("dlogp", dlogp), ("dentropy", dentropy),
+                        ("entropy", entropy if dentropy is not None else None)):
+            if t is not None:
+                _vector(t, name, B, torch.float32, h.device)
+        if out is None:
+            dh = torch.empty_like(h) if need_dh else None
+            dW = torch.empty_like(self.W) if need_dW else None
+        else:
+            dh, dW = out
+            for name, t, like in (("dh", dh, h), ("dW", dW, self.W)):
+                if t is not None and (t.dtype != like.dtype or t.shape != like.shape
+                                      or not t.is_contiguous() or t.device != like.device):
+                    raise ValueError(f"{name} must be like {'h' if name == 'dh' else 'W'}")
+        detlm_head_score_backward(self.handle, h.data_ptr(), targets.data_ptr(), B, temperature,
+                                  lse.data_ptr(),
+                                  entropy.data_ptr() if dentropy is not None else None,
+                                  dlogp.data_ptr(), _ptr(dentropy), _ptr(dh), _ptr(dW),
+                                  _stream_ptr(stream))
+        return dh, dW
+
+    def reserve_backward(self, max_B: int) -> None:
+        """Workspace for gradient calls of up to max_B rows."""
+        detlm_head_reserve_backward(self.handle, int(max_B))
+
+    def weights_changed(self, stream=None) -> None:
+        """Tell the head that W was changed in place on the stream
+        (detlm_head_weights_changed)."""
+        detlm_head_weights_changed(self.handle, _stream_ptr(stream))
+
+    def scaled_logits(self, q, x_scale, w_scale, out_dtype=None, stream=None, out=None):
+        """int8 head: (q . W^T) * x_scale[:, None] * w_scale[None, :] as
+        float32 (default), bfloat16 or float16 [B, V]; q int8 [B, d], x_scale
+        float32 [B] (one scale a token), w_scale float32 [V] (one a channel)."""
+        import torch
+        if self.dtype != "int8":
+            raise DetlmError(DETLM_EUNSUPPORTED, "scaled_logits")
+        self._check_h(q)
+        if q.dtype != torch.int8:
+            raise ValueError("q must be an int8 tensor")
+        B = int(q.shape[0])
+        _vector(x_scale, "x_scale", B, torch.float32, q.device)
+        _vector(w_scale, "w_scale", self.V, torch.float32, q.device)
+        if out is None:
+            out = torch.empty((B, self.V), dtype=out_dtype or torch.float32, device=q.device)
+        elif (out.shape != (B, self.V) or not out.is_contiguous() or out.device != q.device
+              or (out_dtype is not None and out.dtype != out_dtype)):
+            raise ValueError(f"out must be a contiguous [{B}, {self.V}] CUDA tensor")
+        detlm_head_scaled_logits(self.handle, q.data_ptr(), x_scale.data_ptr(),
+                                 w_scale.data_ptr(), B, _float_dtype_code(out), out.data_ptr(),
+                                 _stream_ptr(stream))
+        return out
 
     def greedy_gated(self, h, tau: float = 0.001, with_logits: bool = False, stream=None):
         """Margin-gated greedy call. Returns (token, gap, logits or None,

@@ -23,6 +23,8 @@
 #include "rows_kernels.cuh"
 #include "pair_kernels.cuh"
 #include "shard_kernels.cuh"
+#include "pairop_kernels.cuh"
+#include "score_kernels.cuh"
 
 using namespace detlm;
 
@@ -65,6 +67,7 @@ struct detlm_head {
   // integer head, wide batches: fp16 copy of W (made at the first such call)
   // and the call's hidden rows in fp16
   void* W16 = nullptr;
+  bool w16_stale = false;    // W changed since the copy was made
   CUtensorMap tmW16;
   void* h16 = nullptr;
   size_t h16_bytes = 0;
@@ -76,6 +79,12 @@ struct detlm_head {
   // integer front end: the quantized rows and their multipliers and shifts
   void* q8 = nullptr;
   size_t q8_bytes = 0;
+  // score and gradient calls: one buffer each, laid out per call
+  void* sws = nullptr;
+  size_t sws_bytes = 0;
+  void* gws = nullptr;
+  size_t gws_bytes = 0;
+  int op_pairs = 0;          // CTA pairs of the pair-product kernels that fit at once
   // test hook and timing hook
   int stall = 0;
   uint64_t timeout_ns = 2000000000ull;
@@ -370,9 +379,11 @@ int pair_stages() {
 // memory with 16-byte aligned rows (V a multiple of 4, a 16-byte aligned
 // base); otherwise (host memory the kernel writes through its mapping, such
 // as the asynchronous host-buffer calls' pinned buffers) the kernel stores
-// the logits with plain stores (returns false).
-bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B, bool int32) {
-  if (logits == nullptr || (V & 3) != 0 || !aligned(logits, 16)) return false;
+// the logits with plain stores (returns false). Two-byte logits (the scaled
+// call): box 32 x 32, V a multiple of 8.
+bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B,
+                   CUtensorMapDataType type, int size = 4) {
+  if (logits == nullptr || (V * size) % 16 != 0 || !aligned(logits, 16)) return false;
   cudaPointerAttributes pa;
   if (cudaPointerGetAttributes(&pa, logits) != cudaSuccess) {
     cudaGetLastError();   // clear the error the query recorded
@@ -380,11 +391,10 @@ bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B, boo
   }
   if (pa.type != cudaMemoryTypeDevice) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(V), static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(V) * 4u};
-  cuuint32_t box[2] = {16u, 32u};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(V) * size};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32u};
   cuuint32_t estr[2] = {1, 1};
-  return g_encode(m, int32 ? CU_TENSOR_MAP_DATA_TYPE_INT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                  const_cast<void*>(logits), dims, strides, box, estr,
+  return g_encode(m, type, 2, const_cast<void*>(logits), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -559,7 +569,7 @@ int launch_float(detlm_head* h, const void* h_dev, int64_t B, const int32_t* tar
                              : static_cast<int64_t>(p.n_vt) * p.n_nt;
   const int grid = static_cast<int>(units < h->num_sms ? units : h->num_sms);
   CUtensorMap tmL = tmH;   // the pair kernel's logits map; not read unless valid
-  if (wide) p.tma_logits = encode_logits(&tmL, logits, h->V, B, false) ? 1 : 0;
+  if (wide) p.tma_logits = encode_logits(&tmL, logits, h->V, B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32) ? 1 : 0;
   if (h->t_start) cudaEventRecord(h->t_start, stream);
   cudaError_t e;
   if constexpr (rows) {
@@ -621,10 +631,10 @@ int launch_float(detlm_head* h, const void* h_dev, int64_t B, const int32_t* tar
   return status_from_cuda(e);
 }
 
-template <int N>
+template <int N, bool SCALED>
 cudaError_t launch_int8_t(const CUtensorMap& tmW, const CUtensorMap& tmH, const Int8Params& p,
                           int grid, size_t smem, cudaStream_t stream) {
-  cudaError_t e = prepare_kernel<int8_gemm_kernel<N>>(0);
+  cudaError_t e = prepare_kernel<int8_gemm_kernel<N, SCALED>>(0);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the previous kernel on the stream (its
   // prologue and W prefetch overlap that kernel's tail)
@@ -639,16 +649,17 @@ cudaError_t launch_int8_t(const CUtensorMap& tmW, const CUtensorMap& tmH, const 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<N>, tmW, tmH, p);
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<N, SCALED>, tmW, tmH, p);
 }
 
+template <bool SCALED>
 cudaError_t launch_int8_n(int N, const CUtensorMap& tmW, const CUtensorMap& tmH,
                           const Int8Params& p, int grid, size_t smem, cudaStream_t stream) {
   switch (N) {
-    case 16: return launch_int8_t<16>(tmW, tmH, p, grid, smem, stream);
-    case 32: return launch_int8_t<32>(tmW, tmH, p, grid, smem, stream);
-    case 48: return launch_int8_t<48>(tmW, tmH, p, grid, smem, stream);
-    case 64: return launch_int8_t<64>(tmW, tmH, p, grid, smem, stream);
+    case 16: return launch_int8_t<16, SCALED>(tmW, tmH, p, grid, smem, stream);
+    case 32: return launch_int8_t<32, SCALED>(tmW, tmH, p, grid, smem, stream);
+    case 48: return launch_int8_t<48, SCALED>(tmW, tmH, p, grid, smem, stream);
+    case 64: return launch_int8_t<64, SCALED>(tmW, tmH, p, grid, smem, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -685,6 +696,11 @@ int ensure_wide(detlm_head* h, int64_t B, cudaStream_t stream) {
       return e != cudaSuccess ? status_from_cuda(e) : DETLM_EINVAL;
     }
     h->W16 = w16;
+    h->w16_stale = false;
+  } else if (h->w16_stale) {
+    e = i8_to_f16(h->W, h->W16, static_cast<size_t>(h->V) * h->d, stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    h->w16_stale = false;
   }
   const size_t hb = static_cast<size_t>(B) * h->d * 2;
   if (hb > h->h16_bytes) {
@@ -700,6 +716,30 @@ int ensure_wide(detlm_head* h, int64_t B, cudaStream_t stream) {
     h->h16_bytes = hb;
   }
   return DETLM_OK;
+}
+
+// Launch parameters of the wide integer path that do not depend on what the
+// call writes.
+void int8_wide_params(const detlm_head* h, int64_t B, HeadParams* out) {
+  HeadParams& p = *out;
+  std::memset(&p, 0, sizeof(p));
+  p.V = static_cast<int32_t>(h->V);
+  p.d = static_cast<int32_t>(h->d);
+  p.B = static_cast<int32_t>(B);
+  p.N = kPairN;
+  p.n_vt = h->n_vt;
+  p.n_nt = static_cast<int32_t>((B + kPairN - 1) / kPairN);
+  p.nk = static_cast<int32_t>((h->d * 2 + kRowBytes - 1) / kRowBytes);
+  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
+  p.n_slots = 2;
+  p.stages = pair_stages();
+  p.n_issuers = 1;
+  p.tmem_cols = 512;
+  p.idesc = idesc_f16(0u, 2 * kBM, kPairN);
+  p.err = h->d_err;
+  p.stall = h->stall;
+  p.timeout_ns = h->timeout_ns;
+  p.v_off = static_cast<int32_t>(h->v_off);
 }
 
 int launch_int8_wide(detlm_head* h, const void* h_dev, int64_t B, int32_t* token, int32_t* gap,
@@ -719,32 +759,15 @@ int launch_int8_wide(detlm_head* h, const void* h_dev, int64_t B, int32_t* token
   const WsView w = ws_view(h);
 
   HeadParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.V = static_cast<int32_t>(h->V);
-  p.d = static_cast<int32_t>(h->d);
-  p.B = static_cast<int32_t>(B);
-  p.N = kPairN;
-  p.n_vt = h->n_vt;
-  p.n_nt = static_cast<int32_t>((B + kPairN - 1) / kPairN);
-  p.nk = static_cast<int32_t>((h->d * 2 + kRowBytes - 1) / kRowBytes);
-  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
-  p.n_slots = 2;
-  p.stages = pair_stages();
-  p.n_issuers = 1;
-  p.tmem_cols = 512;
-  p.idesc = idesc_f16(0u, 2 * kBM, kPairN);
+  int8_wide_params(h, B, &p);
   p.logits = reinterpret_cast<float*>(logits);
   p.rec_m = w.m;
   p.rec_i = w.i;
   p.rec_s = w.s;
-  p.err = h->d_err;
-  p.stall = h->stall;
-  p.timeout_ns = h->timeout_ns;
-  p.v_off = static_cast<int32_t>(h->v_off);
   const size_t smem = pair_layout(p.stages).total + 1024;
   const int64_t units = static_cast<int64_t>((p.n_vt + 1) / 2) * p.n_nt;
   CUtensorMap tmL = tmH;   // not read unless the logits map is valid
-  p.tma_logits = encode_logits(&tmL, logits, h->V, B, true) ? 1 : 0;
+  p.tma_logits = encode_logits(&tmL, logits, h->V, B, CU_TENSOR_MAP_DATA_TYPE_INT32) ? 1 : 0;
   if (h->t_start) cudaEventRecord(h->t_start, stream);
   e = launch_pair_kernel<MODE_INT>(h, h->tmW16, tmH, tmL, p, units, smem, stream);
   if (h->t_stop) {
@@ -779,17 +802,10 @@ int launch_int8_wide(detlm_head* h, const void* h_dev, int64_t B, int32_t* token
   return status_from_cuda(e);
 }
 
-int launch_int8(detlm_head* h, const void* h_dev, int64_t B, int32_t* token, int32_t* gap,
-                int32_t* logits, cudaStream_t stream, ShardRec* shard_out = nullptr) {
-  if (B >= kI8WideB) return launch_int8_wide(h, h_dev, B, token, gap, logits, stream, shard_out);
-  const int N = int8_cols_for(B, h->d);
-  CUtensorMap tmH;
-  if (!encode_2d(&tmH, DETLM_INT8, h_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
-  int st = ensure_ws(h, B, stream);
-  if (st != DETLM_OK) return st;
-  const WsView w = ws_view(h);
-
-  Int8Params p;
+// Launch parameters of the int8-streaming kernel that do not depend on what
+// the call writes.
+bool int8_params(const detlm_head* h, int64_t B, int N, Int8Params* out) {
+  Int8Params& p = *out;
   std::memset(&p, 0, sizeof(p));
   p.V = static_cast<int32_t>(h->V);
   p.d = static_cast<int32_t>(h->d);
@@ -805,22 +821,37 @@ int launch_int8(detlm_head* h, const void* h_dev, int64_t B, int32_t* token, int
   const uint32_t stage_bytes = int8_layout(N, 1).stage;
   p.stages = static_cast<int32_t>((kSmemLimit - fixed) / stage_bytes);
   if (p.stages > kI8MaxStages) p.stages = kI8MaxStages;
-  if (p.stages < 2) return DETLM_EINVAL;   // cannot happen for N <= kI8MaxN
+  if (p.stages < 2) return false;   // cannot happen for N <= kI8MaxN
   p.idesc = idesc_f16(0u, kBM, static_cast<uint32_t>(N));
-  p.logits = logits;
-  p.rec_m = reinterpret_cast<int32_t*>(w.m);
-  p.rec_i = w.i;
-  p.rec_s = reinterpret_cast<int32_t*>(w.s);
   p.err = h->d_err;
   p.stall = h->stall;
   p.timeout_ns = h->timeout_ns;
   p.v_off = static_cast<int32_t>(h->v_off);
+  return true;
+}
+
+int launch_int8(detlm_head* h, const void* h_dev, int64_t B, int32_t* token, int32_t* gap,
+                int32_t* logits, cudaStream_t stream, ShardRec* shard_out = nullptr) {
+  if (B >= kI8WideB) return launch_int8_wide(h, h_dev, B, token, gap, logits, stream, shard_out);
+  const int N = int8_cols_for(B, h->d);
+  CUtensorMap tmH;
+  if (!encode_2d(&tmH, DETLM_INT8, h_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
+  int st = ensure_ws(h, B, stream);
+  if (st != DETLM_OK) return st;
+  const WsView w = ws_view(h);
+
+  Int8Params p;
+  if (!int8_params(h, B, N, &p)) return DETLM_EINVAL;
+  p.logits = logits;
+  p.rec_m = reinterpret_cast<int32_t*>(w.m);
+  p.rec_i = w.i;
+  p.rec_s = reinterpret_cast<int32_t*>(w.s);
 
   const size_t smem = int8_layout(N, p.stages).total + 1024;
   const int64_t units = static_cast<int64_t>(p.n_vt) * p.n_nt;
   const int grid = static_cast<int>(units < h->num_sms ? units : h->num_sms);
   if (h->t_start) cudaEventRecord(h->t_start, stream);
-  cudaError_t e = launch_int8_n(N, h->tmW, tmH, p, grid, smem, stream);
+  cudaError_t e = launch_int8_n<false>(N, h->tmW, tmH, p, grid, smem, stream);
   if (h->t_stop) {
     cudaEventRecord(h->t_stop, stream);
     h->t_start = h->t_stop = nullptr;
@@ -1568,6 +1599,8 @@ void detlm_head_destroy(detlm_head_t* h) {
   if (h->W16) cudaFree(h->W16);
   if (h->h16) cudaFree(h->h16);
   if (h->stage) cudaFree(h->stage);
+  if (h->sws) cudaFree(h->sws);
+  if (h->gws) cudaFree(h->gws);
   if (h->err_mapped) cudaFreeHost(h->err_mapped);
   else if (h->d_err) cudaFree(h->d_err);
   if (h->err_host) cudaFreeHost(h->err_host);
@@ -1575,6 +1608,8 @@ void detlm_head_destroy(detlm_head_t* h) {
 }
 
 }  // extern "C"
+
+#include "score_host.cuh"
 
 // ---------------------------------------------------------------------------
 // Greedy call without any device allocation (see the header for who needs

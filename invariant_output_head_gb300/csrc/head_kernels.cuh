@@ -57,6 +57,7 @@
 #include <cmath>
 #include <type_traits>
 #include "ptx.cuh"
+#include "score_stats.cuh"
 
 namespace detlm {
 
@@ -80,7 +81,13 @@ constexpr int kSmemLimit = 232448;  // 227 KB dynamic shared memory per CTA
 // MODE_SAMPLE: seeded Gumbel-max sampling ("TandemLLM docs, 12 Exactness",
 // 12.5): the record is the greedy record of the scores z / T + G, G the
 // Gumbel noise of the row's (seed, position) at each vocabulary entry.
-enum : int { MODE_GREEDY = 0, MODE_LOGPROB = 1, MODE_INT = 2, MODE_GATED = 3, MODE_SAMPLE = 4 };
+// MODE_SCORE: the score call's projection of up to 128 rows: logits into the
+// handle's workspace and, per 128-row tile, the softmax statistics of
+// score_stats.cuh (rec_m, rec_s and, in rec_i's storage, U).
+// MODE_SCALED: MODE_INT whose int32 sums are written times a scale of the
+// hidden row and one of the vocabulary row, and nothing else.
+enum : int { MODE_GREEDY = 0, MODE_LOGPROB = 1, MODE_INT = 2, MODE_GATED = 3, MODE_SAMPLE = 4,
+             MODE_SCORE = 5, MODE_SCALED = 6 };
 enum : int { ERR_TIMEOUT = 1, ERR_TARGET = 2 };
 
 // Kept at 128 bytes or less: with the parameter struct above 128 bytes the
@@ -108,15 +115,18 @@ struct HeadParams {
     const int32_t* targets;   // logprob: [B]
     int32_t* rec_b;           // gated: [B, n_vt] lowest index of the rounded maximum
     const uint64_t* seeds;    // sample: [B] generator key of each row
+    const float* x_scale;     // scaled: [B] scale of each hidden row
   };
   union {
     float* zt;                // logprob: [B] target logit
     const uint64_t* positions;  // sample: [B] position t of each row
+    const float* w_scale;       // scaled: [V] scale of each vocabulary row
   };
   union {
     int32_t round_fp16;       // gated: 1 rounds logits to fp16, 0 to bf16
-    float temperature;        // sample: T > 0
-    int32_t tma_logits;       // pair kernel: 1 = logits leave through the logits tensor map
+    float temperature;        // sample: T > 0; score: log2(e) / T
+    int32_t tma_logits;       // pair kernel: bit 0 = logits leave through the logits tensor
+                              // map; scaled: bits 1, 2 = the output's type
   };
   int32_t v_off;            // vocabulary index of this head's first W row
 };
@@ -267,6 +277,26 @@ __device__ __forceinline__ Top2 xp_top2(const float* xp, int lane, int v_row0) {
     }
   }
   return top2_merge(t, shfl_xor(t, 16));
+}
+
+// score: the statistics of a column over the warp's 32 vocabulary rows (rows
+// past the vocabulary are -inf and count as nothing)
+__device__ __forceinline__ Stat xp_stat(const float* xp, int lane, float c) {
+  const int col = lane & 15, h = lane >> 4;
+  float x[16];
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    x[j] = xp[(h * 16 + j) * kXpStride + col];
+    m = fmaxf(m, x[j]);
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+  const float mm = fmaxf(m, kVeryLow);
+  float S = 0.0f, U = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) stat_add(x[j], mm, c, S, U);
+  return Stat{m, __fadd_rn(S, __shfl_xor_sync(0xffffffffu, S, 16)),
+              __fadd_rn(U, __shfl_xor_sync(0xffffffffu, U, 16))};
 }
 
 // A logit rounded once (to nearest, ties to even) into the head's 16-bit
@@ -442,7 +472,8 @@ template <int MODE, int NBLK>
 __global__ void __launch_bounds__(threads_for(16 * NBLK), 1)
 head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmH, const HeadParams p) {
-  static_assert(MODE == MODE_GREEDY || MODE == MODE_GATED || MODE == MODE_SAMPLE,
+  static_assert(MODE == MODE_GREEDY || MODE == MODE_GATED || MODE == MODE_SAMPLE ||
+                    MODE == MODE_SCORE,
                 "log-prob runs on head_rows_kernel, the integer wide path on head_pair_kernel");
   constexpr int N = 16 * NBLK;
   constexpr int EW = epi_warps_for(N);          // epilogue warps
@@ -787,6 +818,13 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
             red_i[q * N + c0 + lane] = t.i;
             red_s[q * N + c0 + lane] = t.s;
           }
+        } else if constexpr (MODE == MODE_SCORE) {
+          const Stat t = xp_stat(xp, lane, p.temperature);
+          if (lane < 16) {
+            red_m[q * N + c0 + lane] = t.m;
+            red_i[q * N + c0 + lane] = __float_as_int(t.U);
+            red_s[q * N + c0 + lane] = t.S;
+          }
         } else {
           static_assert(MODE == MODE_GATED, "the log-prob call runs on head_rows_kernel");
           int32_t i16;
@@ -806,7 +844,18 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
         const int n = n0 + c;
         if (n >= p.B) continue;
         const size_t o = static_cast<size_t>(n) * p.n_vt + vt;   // records [B][n_vt]
-        {
+        if constexpr (MODE == MODE_SCORE) {
+          Stat t[4];
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq)
+            t[qq] = Stat{red_m[qq * N + c], red_s[qq * N + c],
+                         __int_as_float(red_i[qq * N + c])};
+          const float k = p.temperature;
+          const Stat r = stat_merge(stat_merge(t[0], t[1], k), stat_merge(t[2], t[3], k), k);
+          p.rec_m[o] = r.m;
+          p.rec_s[o] = r.S;
+          reinterpret_cast<float*>(p.rec_i)[o] = r.U;
+        } else {
           Top2 t[4];
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq)

@@ -71,7 +71,7 @@ struct Int8Params {
   int32_t N, n_vt, n_nt, nk, n_chunks;
   int32_t stages;            // int8 ring depth
   uint32_t idesc;
-  int32_t* logits;           // optional int32 [B, V]
+  int32_t* logits;           // optional int32 [B, V]; scaled logits: the output
   int32_t* rec_m;            // [B, n_vt]
   int32_t* rec_i;
   int32_t* rec_s;
@@ -79,6 +79,9 @@ struct Int8Params {
   int32_t stall;
   uint64_t timeout_ns;
   int32_t v_off;             // vocabulary index of this head's first W row
+  int32_t out_type;          // scaled logits: OUT_F32, OUT_BF16 or OUT_FP16
+  const float* x_scale;      // scaled logits: [B] scale of each hidden row
+  const float* w_scale;      // scaled logits: [V] scale of each vocabulary row
 };
 static_assert(sizeof(Int8Params) <= 128, "kernel parameter struct above 128 bytes");
 
@@ -169,6 +172,13 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
   }
 }
 
+enum : int { OUT_F32 = 0, OUT_BF16 = 1, OUT_FP16 = 2 };   // scaled logits' type
+__device__ __forceinline__ void store_scaled(void* out, size_t at, float y, int type) {
+  if (type == OUT_F32) reinterpret_cast<float*>(out)[at] = y;
+  else if (type == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
+  else reinterpret_cast<__half*>(out)[at] = __float2half_rn(y);
+}
+
 // tcgen05 helpers used only here: 32 consecutive 32-bit columns stored per
 // thread (thread i -> lane base + i), the wait for them, and an MMA whose A
 // operand is read from tensor memory (row m of A in lane m, two fp16 of K
@@ -198,7 +208,11 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
-template <int N_>
+// SCALED: the scaled-logits call. Instead of int32 logits and records the
+// epilogue writes acc * (x_scale[n] * w_scale[v]) in the output's type (the
+// int32 sum rounded once to fp32 -- exact below 2^24 --, one rounded product
+// of the scales, one rounded product, and the output's own rounding).
+template <int N_, bool SCALED>
 __global__ void __launch_bounds__(kI8Threads, 1)
 int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
                  const Int8Params p) {
@@ -464,42 +478,65 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int v = vt * kBM + row;
       const bool vok = v < p.V;
       const int n0 = nt * N;
+      if constexpr (SCALED) {
+        // a warp writes 32 consecutive entries of one row at a time; nothing
+        // is shared between warps, so the next unit needs no barrier
+        const float sw = vok ? p.w_scale[v] : 0.0f;
+        void* out = p.logits;
 #pragma unroll
-      for (int bb = 0; bb < N / 16; ++bb) {
-        const int c0 = bb * 16;
-        if (p.logits != nullptr && vok) {
+        for (int bb = 0; bb < N / 16; ++bb) {
+          if (n0 + bb * 16 >= p.B) break;
+          float sx[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sx[i] = n0 + bb * 16 + i < p.B ? __ldg(p.x_scale + n0 + bb * 16 + i) : 0.0f;
+          if (!vok) continue;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int n = n0 + c0 + i;
-            if (n < p.B) p.logits[static_cast<size_t>(n) * p.V + v] = acc[bb][i];
+            const int n = n0 + bb * 16 + i;
+            if (n < p.B)
+              store_scaled(out, static_cast<size_t>(n) * p.V + v,
+                           __fmul_rn(__int2float_rn(acc[bb][i]), __fmul_rn(sx[i], sw)), p.out_type);
           }
         }
-        int32_t* xp = xpose + q * kXpWords;
+      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xp[lane * kXpStride + i] = vok ? acc[bb][i] : INT32_MIN;
-        __syncwarp();
-        const ITop2 t = xp_itop2(xp, lane, p.v_off + vt * kBM + q * 32);
-        if (lane < 16) {
-          red_m[q * N + c0 + lane] = t.m;
-          red_i[q * N + c0 + lane] = t.i;
-          red_s[q * N + c0 + lane] = t.s;
+        for (int bb = 0; bb < N / 16; ++bb) {
+          const int c0 = bb * 16;
+          if (p.logits != nullptr && vok) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int n = n0 + c0 + i;
+              if (n < p.B) p.logits[static_cast<size_t>(n) * p.V + v] = acc[bb][i];
+            }
+          }
+          int32_t* xp = xpose + q * kXpWords;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) xp[lane * kXpStride + i] = vok ? acc[bb][i] : INT32_MIN;
+          __syncwarp();
+          const ITop2 t = xp_itop2(xp, lane, p.v_off + vt * kBM + q * 32);
+          if (lane < 16) {
+            red_m[q * N + c0 + lane] = t.m;
+            red_i[q * N + c0 + lane] = t.i;
+            red_s[q * N + c0 + lane] = t.s;
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      named_bar_sync(1, 128);
-      for (int c = et; c < N; c += 128) {
-        const int n = n0 + c;
-        if (n >= p.B) continue;
-        ITop2 t[4];
+        named_bar_sync(1, 128);
+        for (int c = et; c < N; c += 128) {
+          const int n = n0 + c;
+          if (n >= p.B) continue;
+          ITop2 t[4];
 #pragma unroll
-        for (int qq = 0; qq < 4; ++qq) t[qq] = ITop2{red_m[qq * N + c], red_i[qq * N + c], red_s[qq * N + c]};
-        const ITop2 rr = itop2_merge(itop2_merge(t[0], t[1]), itop2_merge(t[2], t[3]));
-        const size_t o = static_cast<size_t>(n) * p.n_vt + vt;   // records [B][n_vt]
-        p.rec_m[o] = rr.m;
-        p.rec_i[o] = rr.i;
-        p.rec_s[o] = rr.s;
+          for (int qq = 0; qq < 4; ++qq) t[qq] = ITop2{red_m[qq * N + c], red_i[qq * N + c], red_s[qq * N + c]};
+          const ITop2 rr = itop2_merge(itop2_merge(t[0], t[1]), itop2_merge(t[2], t[3]));
+          const size_t o = static_cast<size_t>(n) * p.n_vt + vt;   // records [B][n_vt]
+          p.rec_m[o] = rr.m;
+          p.rec_i[o] = rr.i;
+          p.rec_s[o] = rr.s;
+        }
+        named_bar_sync(1, 128);
       }
-      named_bar_sync(1, 128);
     }
     if (failed && et == 0) atomicOr(p.err, ERR_TIMEOUT);
   }

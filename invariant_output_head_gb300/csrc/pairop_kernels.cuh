@@ -1,0 +1,738 @@
+// pairop_kernels.cuh -- the matrix products of the score call and of its
+// gradient, on CTA pairs.
+//
+// One kernel body, five products. A unit is a 256 x 256 tile of
+// D = A * B^T, computed by a cluster of two CTAs with tcgen05.mma.cta_group::2
+// (each CTA holds 128 rows of A and 128 of B per stage and finds its own 128
+// rows of D in its tensor memory), with the pair protocol of
+// rows_kernels.cuh: the leader issues every MMA, both producers' loads
+// complete on the leader's stage barrier, commits arrive on both CTAs, a
+// chunk's accumulator slot goes back when the epilogue warps of both CTAs have
+// drained it, every wait is bounded.
+//
+//   OP_SCORE   D[n, v] = h W^T: softmax statistics of each row and 256-entry
+//              tile, the target's logit, and the candidates for the row's
+//              largest logits; logits are never written.
+//   OP_SELECT  the same product again, for the 256-row tiles that hold a row
+//              whose candidates overflowed: only its candidates, with the
+//              exact threshold found meanwhile.
+//   OP_DZ      D[n, v] = h W^T again, turned into the gradient with respect
+//              to the logits and written in 16 bits, but for the target's
+//              entry, which goes to an fp32 word of the row.
+//   OP_DH      D[n, k] = sum_v dz[n, v] W[v, k]: A = dz with the contracted
+//              axis contiguous, B = W with the free axis contiguous.
+//   OP_DW      D[v, k] = sum_n dz[n, v] h[n, k]: both operands with the free
+//              axis contiguous.
+//
+// The target's entry (g_l (1 - p) - ...) / T of the gradient never passes
+// through 16 bits: it is by far the largest of its row, and its rounding would
+// be as large as that of the result. dz holds a zero in its place; its fp32
+// value contributes a row of W to dh and a row of h to dW, added in fp32
+// (grad_fold_kernel, and this kernel's OP_DW epilogue).
+//
+// The first three use the logits' own arithmetic (128-element K chunks, each
+// accumulated from zero and added in fp32 in ascending order), so they see
+// the bits that every other call of the head computes. The gradient products
+// contract over the vocabulary or the rows, in chunks of 2048: 128 MMA steps
+// of the tensor core's accumulation before a round-to-nearest fp32 add, which
+// leaves at most about 128 half-ulps of fp32 (8e-6) per chunk, far below the
+// 16-bit rounding of what goes in (dz) and comes out.
+//
+// Operands with the free axis contiguous ("MN-major") are loaded as boxes of
+// 64 free x 64 contracted elements, 128-byte swizzle: 64 rows of 128 bytes,
+// the rows running along the contracted axis. Eight rows make a 1024-byte
+// atom (the descriptor's stride offset), the next 64 free elements start 8 KB
+// on (its leading offset), and a K = 16 step is 16 rows = 2048 bytes.
+//
+// What bounds them: the tensor pipe. Per chunk of 128 the pair's MMAs take
+// ~0.52 us; the epilogue drains it in about half of that, so the statistics
+// (5 instructions a logit) run while the MMA fills the two slots of the next
+// unit's first chunks.
+#pragma once
+#include "head_kernels.cuh"
+#include "pair_kernels.cuh"
+#include "rows_kernels.cuh"
+
+namespace detlm {
+
+enum : int { OP_SCORE = 0, OP_SELECT = 1, OP_DZ = 2, OP_DH = 3, OP_DW = 4 };
+
+constexpr int kGradChunkBoxes = 32;      // 64-element K boxes per gradient chunk (2048)
+constexpr int kSegChunks = 8;            // gradient chunks per vocabulary segment (16384)
+constexpr int kCandFloats = 20;          // a candidate block: 16 logits, its index, padding
+constexpr int kRowWords = 4;             // words of a row before its slots
+enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
+
+__host__ __device__ constexpr int row_words(int K) { return kRowWords + ((K + 3) & ~3); }
+
+// Offset of the score products' half-row records, behind the control words.
+__host__ __device__ inline uint32_t pairop_red_off(int stages) {
+  return pair_layout(stages).ctrl_off + (2u * stages + 6u) * 8u + 16u;
+}
+constexpr uint32_t kPairopRedBytes = 3u * 128u * 4u;
+
+// MN-major operand tile in the 128-byte swizzle layout written by TMA as
+// boxes of 64 (free) x 64 (contracted) 16-bit elements.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);   // start address
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;               // next 64 free elements
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;               // next 8 contracted elements
+  d |= static_cast<uint64_t>(1) << 46;                       // descriptor version
+  d |= static_cast<uint64_t>(2) << 61;                       // 128-byte swizzle
+  return d;
+}
+// Instruction descriptor bits: operand with the free axis contiguous.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
+
+struct ScoreArgs {
+  float* rec;               // [3][rec_part]: m, S, U of each [B][n_vt] tile
+  float* zt;                // [B] target logits
+  const int32_t* targets;   // optional [B]
+  int32_t* words;           // [B][row_words(K)]: candidate count, ..., K slot maxima
+  float* cand;              // [B][C][kCandFloats]
+  const int32_t* tile_over; // OP_SELECT: [n_rt] tiles to compute
+};
+struct GradArgs {
+  const float* lse;         // [B]
+  const float* entropy;     // [B]
+  const float* dlogp;       // [B]
+  const float* dentropy;    // optional [B]
+  const int32_t* targets;   // [B], vocabulary index of the whole head
+  const float* scale;       // optional: {power of two dz is held in, its inverse}
+};
+
+struct DwArgs {
+  const int32_t* tiles;     // [n_vt][2]: where a tile's targets start in the list, how many
+  const int2* list;         // (row of h, entry within the tile), by tile, then by row
+  const void* h;            // [B][d]
+  const void* unused[2];
+  const float* scale;       // as above
+};
+
+// 128 bytes or less (see HeadParams).
+struct PairOpParams {
+  int32_t B, V;             // hidden rows; vocabulary entries (of this pass)
+  int32_t n0, n1;           // unit grid (see unit_of)
+  int32_t nk;               // K boxes of 64
+  int32_t seg;              // K boxes per unit (OP_DH; else nk)
+  int32_t units;
+  uint16_t stages, stall;
+  uint32_t idesc;
+  int32_t K, C;             // score: alternatives wanted, candidate blocks a row can hold;
+                            // OP_DH, OP_DW: K is the number of columns of D (d);
+                            // OP_DZ: K is the whole head's V
+  int32_t t_off;            // gradient: vocabulary index of this pass's first entry
+  float c, inv_t;           // log2(e) / T, 1 / T
+  union {
+    int64_t rec_part;       // score: elements between the record arrays
+    float* coef;            // OP_DZ: [B] out, OP_DW: in: the target's entry of dz (as scaled)
+  };
+  uint64_t timeout_ns;
+  int* err;
+  union {
+    ScoreArgs s;
+    GradArgs g;
+    DwArgs w;
+  };
+};
+static_assert(sizeof(PairOpParams) <= 128, "kernel parameter struct above 128 bytes");
+
+// Origins of unit u in the operands: 256 rows of A from a0, 256 of B from b0,
+// nkb K boxes from kb0.
+//   OP_SCORE, OP_SELECT, OP_DZ: n1 hidden-row tiles, fastest (they share each
+//     W tile from L2)
+//   OP_DH: n1 tiles of d, fastest, then n0 hidden-row tiles, then segments
+//   OP_DW: n1 tiles of d, fastest, then vocabulary tiles
+struct PairUnit { int a0, b0, kb0, nkb, seg; };
+template <int OP>
+__device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, int u) {
+  PairUnit t;
+  const int q = u / p.n1, r = u - q * p.n1;
+  t.kb0 = 0;
+  t.nkb = p.nk;
+  t.seg = 0;
+  if constexpr (OP == OP_DH) {
+    t.seg = q / p.n0;
+    t.a0 = (q - t.seg * p.n0) * 256;
+    t.b0 = r * 256;
+    t.kb0 = t.seg * p.seg;
+    t.nkb = min(p.seg, p.nk - t.kb0);
+  } else if constexpr (OP == OP_DW) {
+    t.a0 = q * 256;
+    t.b0 = r * 256;
+  } else {
+    t.a0 = r * 256;
+    t.b0 = q * 256;
+  }
+  return t;
+}
+
+// 32 rows x 64 bytes of a warp (lane = row) through one of its two staging
+// buffers to the tensor map's box at (c0, row0); asynchronous.
+__device__ __forceinline__ void stage_store(const void* tmap, uint8_t* xs, uint32_t xs_u32,
+                                            uint32_t& nbuf, const uint4 (&w)[4], int lane, int c0,
+                                            int row0) {
+  const uint32_t buf = nbuf & 1u;
+  if (nbuf >= 2) {
+    if (lane == 0) bulk_wait_group_read<1>();   // this buffer's previous store has read it
+    __syncwarp();
+  }
+  uint8_t* sb = xs + buf * kPairStageBuf;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4*>(sb + lane * 64 + 16 * (k ^ ((lane >> 1) & 3))) = w[k];
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tmap, xs_u32 + buf * kPairStageBuf, c0, row0);
+    bulk_commit_group();
+  }
+  ++nbuf;
+}
+
+// The score call's epilogue of one half-unit: this thread's row n, 128
+// entries from vb (nv of them exist).
+//
+// Candidates. The row keeps K slots; slot j holds the largest logit of the
+// 32-entry groups j, j + K, ... seen so far, so K different entries are at
+// least as large as the smallest slot: that value is a threshold no entry
+// below which can be among the K largest, however many CTAs add to it and
+// however late a reader sees it. Every 16-entry block that reaches the
+// threshold is appended whole to the row's list (its place there depends on
+// timing, the set of entries above the final threshold does not). About
+// K H_K entries stay above the final threshold (H_K the harmonic number), so
+// of V / 16 blocks some K H_K log(n_vt) are appended.
+template <bool RAGGED>
+__device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&acc)[8][16], int n,
+                                           int vb, int nv, float thr, bool records) {
+  float bm[8];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    bm[b] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!RAGGED || b * 16 + i < nv) bm[b] = fmaxf(bm[b], acc[b][i]);
+  }
+  uint32_t mask = 0;
+  int base = 0;
+  int32_t* w = p.s.words + static_cast<size_t>(n) * row_words(p.K);
+  if (p.K > 0) {
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+      if (bm[b] >= thr && (!RAGGED || b * 16 < nv)) mask |= 1u << b;
+    if (mask != 0) {
+      base = atomicAdd(&w[RW_COUNT], __popc(mask));
+      if (records) {
+        int slot = (vb >> 5) % p.K;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float gm = fmaxf(bm[2 * j], bm[2 * j + 1]);
+          if (gm >= thr && (!RAGGED || j * 32 < nv))
+            atomicMax(reinterpret_cast<uint32_t*>(w + kRowWords + slot), score_key(gm));
+          if (++slot == p.K) slot = 0;
+        }
+      }
+    }
+  }
+  Stat st{-INFINITY, 0.0f, 0.0f};
+  if (records) {
+    Stat g[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (RAGGED && j * 32 >= nv) {
+        g[j] = Stat{-INFINITY, 0.0f, 0.0f};
+      } else {
+        g[j] = stat32<RAGGED>(acc[2 * j], acc[2 * j + 1], fmaxf(bm[2 * j], bm[2 * j + 1]), p.c,
+                              nv - j * 32);
+      }
+    }
+    st = stat_merge(stat_merge(g[0], g[1], p.c), stat_merge(g[2], g[3], p.c), p.c);
+  }
+  if (mask != 0) {
+    float* cd = p.s.cand + static_cast<size_t>(n) * p.C * kCandFloats;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (!(mask & (1u << b))) continue;
+      if (base < p.C) {
+        float* o = cd + static_cast<size_t>(base) * kCandFloats;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float4 v = make_float4(acc[b][4 * k], acc[b][4 * k + 1], acc[b][4 * k + 2],
+                                 acc[b][4 * k + 3]);
+          reinterpret_cast<float4*>(o)[k] = v;
+        }
+        o[16] = __int_as_float((vb >> 4) + b);
+      }
+      ++base;
+    }
+  }
+  return st;
+}
+
+// OP_DW: the targets' entries of this warp's 32 vocabulary rows (from row0 of
+// the tile on): each hidden row whose target is one of them adds its entry
+// times itself, in ascending order of the rows. A tile's list is short (B / n_vt
+// entries on average); the lane that owns the row adds 128 columns.
+__device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[8][16], int tile,
+                                            int row0, int col0, int lane, bool f16) {
+  const int2 range = *reinterpret_cast<const int2*>(p.w.tiles + 2 * tile);
+  for (int i0 = 0; i0 < range.y; i0 += 32) {
+    const int2 e = i0 + lane < range.y ? p.w.list[range.x + i0 + lane] : make_int2(0, -1);
+    uint32_t hits = __ballot_sync(0xffffffffu, e.y >= row0 && e.y < row0 + 32);
+    while (hits != 0) {
+      const int src = __ffs(hits) - 1;
+      hits &= hits - 1;
+      const int n = __shfl_sync(0xffffffffu, e.x, src);
+      const int row = __shfl_sync(0xffffffffu, e.y, src) - row0;
+      if (lane != row) continue;
+      const float g = p.coef[n];
+      const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
+                                                      static_cast<size_t>(n) * p.K + col0);
+#pragma unroll
+      for (int b = 0; b < 16; ++b) {
+        if (col0 + 8 * b >= p.K) break;      // d is a multiple of 8
+        const uint4 w = __ldg(h + b);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack16(x[k], f16);
+          float* a = &acc[b >> 1][(b & 1) * 8 + 2 * k];
+          a[0] = fmaf(g, v.x, a[0]);
+          a[1] = fmaf(g, v.y, a[1]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmO, const PairOpParams p) {
+  constexpr bool kScore = OP == OP_SCORE || OP == OP_SELECT;
+  constexpr bool kLogits = kScore || OP == OP_DZ;      // D = h W^T
+  constexpr bool kStore = !kScore;                     // D leaves through staging and tmO
+  constexpr bool kMnA = OP == OP_DW, kMnB = OP == OP_DH || OP == OP_DW;
+  constexpr int kBoxes = kLogits ? kBlocksPerChunk : kGradChunkBoxes;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int S = p.stages;
+  const PairLayout L = pair_layout(S);             // without staging: the same up to xs_off
+  const uint32_t rank = cluster_rank();            // 0: leader, 1: peer
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int n_pairs = static_cast<int>(gridDim.x >> 1);
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.ctrl_off);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto accf_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
+  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+  const uint32_t never_bar = bar0 + 8u * (2 * S + 4);
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 6) * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  // after the control words: staging buffers (1024-byte aligned), or the
+  // half-row records [3][128]
+  uint8_t* tail = smem + (kStore ? L.xs_off : pairop_red_off(S));
+  const uint32_t smem_base = smem_u32(smem);
+  auto sA = [&](int s) { return smem_base + static_cast<uint32_t>(s) * L.stage_bytes; };
+  auto sB = [&](int s) { return sA(s) + L.a_bytes; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);       // the leader's arrival (+ both CTAs' loads)
+      mbar_init(empty_bar(s), 1);      // the leader's MMA commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);       // the leader's MMA commit
+      mbar_init(acce_bar(b), 16);      // eight epilogue warps of each CTA
+    }
+    mbar_init(never_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (kStore) tma_prefetch_desc(&tmO);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_holder), 512u);
+    tmem_relinquish_pair();
+  }
+  // both CTAs' barriers are initialised before any load or arrival of the
+  // other CTA can reach them
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int half = static_cast<int>(rank) * kRowsHalf;
+  // OP_SELECT computes the units of the marked hidden-row tiles alone (the
+  // marks are the previous kernel's, read after the wait by every role)
+  auto skip = [&](int u) {
+    if constexpr (OP == OP_SELECT) return p.s.tile_over[u % p.n1] == 0;
+    return false;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+    if (lane == 0) {
+      const uint64_t pol_n = policy_evict_normal();
+      const uint64_t pol_l = policy_evict_last();
+      const bool leader = rank == 0;
+      auto load_a = [&](int s, const PairUnit& t, int kb, uint32_t fb) {
+        if constexpr (kMnA) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            tma_load_2d_pair(sA(s) + i * 8192, &tmA, t.a0 + half + i * 64, kb * 64, fb, pol_n);
+        } else {
+          tma_load_2d_pair(sA(s), &tmA, kb * 64, t.a0 + half, fb, kLogits ? pol_l : pol_n);
+        }
+      };
+      auto load_b = [&](int s, const PairUnit& t, int kb, uint32_t fb) {
+        if constexpr (kMnB) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            tma_load_2d_pair(sB(s) + i * 8192, &tmB, t.b0 + half + i * 64, kb * 64, fb, pol_l);
+        } else {
+          tma_load_2d_pair(sB(s), &tmB, kb * 64, t.b0 + half, fb, pol_n);
+        }
+      };
+      // unlike the other projections, no W box is requested before the wait:
+      // a trainer updates W on the stream between calls
+      grid_dep_wait();
+      uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
+      bool ok = true;
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
+        if (skip(u)) continue;
+        const PairUnit t = unit_of<OP>(p, u);
+        for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb) {
+          const uint32_t fb = cluster_addr(full_bar(stage), 0);
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * L.stage_bytes);
+          load_b(stage, t, kb, fb);
+          load_a(stage, t, kb, fb);
+          outstanding |= 1u << stage;
+          out_par = (out_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == static_cast<uint32_t>(S)) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, ERR_TIMEOUT);
+        if (leader) {
+          // the armed stages complete once both CTAs' loads have landed
+          const int zero = 0;
+          for (int s = 0; s < S; ++s)
+            if ((outstanding >> s) & 1u) mbar_wait(full_bar(s), (out_par >> s) & 1u, &zero, p.timeout_ns);
+        } else {
+          // the peer's loads complete on the leader's barriers: give the
+          // ones in flight time to land before this CTA may leave
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < kPairSettleNs) __nanosleep(1000);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+    if (lane == 0 && rank == 0) {
+      if constexpr (OP == OP_SELECT) grid_dep_wait();
+      uint32_t stage = 0, phase = 0, slot = 0, sph = 0;
+      bool ok = true;
+      if (p.stall) ok = mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
+        if (skip(u)) continue;
+        const int nkb = unit_of<OP>(p, u).nkb;
+        for (int c0 = 0; c0 < nkb && ok; c0 += kBoxes) {
+          if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + slot * 256u;
+          const int nb = min(kBoxes, nkb - c0);
+#pragma unroll(kBoxes <= 2 ? kBoxes : 1)
+          for (int sc = 0; sc < kBoxes; ++sc) {
+            if (sc >= nb) break;
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t da = kMnA ? sdesc_mn_sw128(sA(stage)) : sdesc_sw128(sA(stage));
+            const uint64_t db = kMnB ? sdesc_mn_sw128(sB(stage)) : sdesc_sw128(sB(stage));
+            constexpr uint32_t ka = kMnA ? 128u : 2u, kb = kMnB ? 128u : 2u;   // K = 16 step, 16 B units
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_pair(d_tmem, da + ka * k, db + kb * k, p.idesc, !(sc == 0 && k == 0));
+            mma_commit_pair(empty_bar(stage), 3);
+            if (++stage == static_cast<uint32_t>(S)) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          mma_commit_pair(accf_bar(slot), 3);
+          if (++slot == 2u) { slot = 0; sph ^= 1u; }
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, ERR_TIMEOUT);
+      }
+      mma_commit_pair(drain_bar, 1);
+      const int zero = 0;
+      mbar_wait(drain_bar, 0, &zero, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // warps 2 and 3: no role, fewer registers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+  } else {
+    // --------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsEpiWide));
+    grid_dep_wait();          // outputs and records: only after the previous kernels
+    const int q = warp & 3;                    // TMEM lane quarter
+    const int g = (warp - 4) >> 2;             // column half of the unit
+    const int r = q * 32 + lane;               // row within this CTA's half
+    const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
+    uint8_t* xs = tail + (warp - 4) * kPairXsBytes;
+    const uint32_t xs_u32 = smem_u32(xs);
+    float* red = reinterpret_cast<float*>(tail);              // [3][128]
+    uint32_t nbuf = 0;                         // staging buffers used so far
+    uint32_t slot = 0, sph = 0;
+    bool failed = false;
+    for (int u = pair; u < p.units; u += n_pairs) {
+      if (skip(u)) continue;
+      const PairUnit t = unit_of<OP>(p, u);
+      const int nw0 = t.a0 + half + q * 32;    // the warp's first row of D
+      const int n = nw0 + lane;                // this thread's row
+      const int rows = OP == OP_DW ? p.V : p.B;
+      const int vb = t.b0 + g * 128;           // first column of this half
+      float acc[8][16];
+      float thr = -INFINITY;
+      const int n_chunks = (t.nkb + kBoxes - 1) / kBoxes;
+      for (int c = 0; c < n_chunks; ++c) {
+        const uint32_t cur = slot, cph = sph;
+        if (++slot == 2u) { slot = 0; sph ^= 1u; }
+        if (!failed && !mbar_wait(accf_bar(cur), cph, abort_flag, p.timeout_ns)) {
+          failed = true;
+          *abort_flag = 1;
+        }
+        if (failed) continue;
+        tc_fence_after();
+        if (nw0 < rows) {
+          const uint32_t sbase = tmem_base + tlane + cur * 256u + static_cast<uint32_t>(g * 128);
+          // two groups of two 32-column loads, one wait each
+#pragma unroll
+          for (int h4 = 0; h4 < 2; ++h4) {
+            uint32_t rw[2][32];
+#pragma unroll
+            for (int b2 = 0; b2 < 2; ++b2) tmem_ld32(sbase + (h4 * 2 + b2) * 32, rw[b2]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int b4 = 0; b4 < 4; ++b4) {
+              const int bb = h4 * 4 + b4;
+              const uint32_t* rr = &rw[b4 >> 1][(b4 & 1) * 16];   // this block's 16 columns
+              if (c == 0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[bb][i] = __uint_as_float(rr[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                  add2_rn(acc[bb][i], acc[bb][i + 1], __uint_as_float(rr[i]),
+                          __uint_as_float(rr[i + 1]));
+              }
+            }
+          }
+        }
+        tc_fence_before();   // slot fully read: hand it back to the leader's MMA warp
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(acce_bar(cur));
+          else mbar_arrive_remote(cluster_addr(acce_bar(cur), 0));
+        }
+        if constexpr (OP == OP_SCORE) {
+          // the row's threshold as of now: read here, where the epilogue
+          // waits for the tensor core anyway
+          if (c == (n_chunks >> 1) && p.K > 0 && n < p.B) {
+            const uint4* sl = reinterpret_cast<const uint4*>(
+                p.s.words + static_cast<size_t>(n) * row_words(p.K) + kRowWords);
+            uint32_t lo = 0xFFFFFFFFu;
+            for (int k = 0; k < p.K; k += 4) {
+              const uint4 v = __ldcg(sl + (k >> 2));
+              lo = min(lo, v.x);
+              if (k + 1 < p.K) lo = min(lo, v.y);
+              if (k + 2 < p.K) lo = min(lo, v.z);
+              if (k + 3 < p.K) lo = min(lo, v.w);
+            }
+            thr = score_unkey(lo);
+          }
+        }
+      }
+      if (epi_bar_or<256>(failed || *abort_flag)) {
+        if (threadIdx.x == 128) { *abort_flag = 1; atomicOr(p.err, ERR_TIMEOUT); }
+        break;
+      }
+      if constexpr (kScore) {
+        const int vt = t.b0 >> 8;
+        const int n_vt = p.units / p.n1;
+        const int nv = min(128, p.V - vb);      // valid entries in this half (<= 0: none)
+        const bool row_ok = n < p.B;
+        const size_t o = static_cast<size_t>(n) * n_vt + vt;   // records [B][n_vt]
+        Stat st{-INFINITY, 0.0f, 0.0f};
+        if constexpr (OP == OP_SCORE) {
+          if (row_ok && nv > 0) {
+            // the target's logit, if it lies in this half: a select chain
+            // over the 16-entry blocks, then over the block
+            const int tl = p.s.targets != nullptr ? p.s.targets[n] - vb : -1;
+            if (tl >= 0 && tl < 128) {
+              const int tb = tl >> 4, ti = tl & 15;
+              float sel[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sel[i] = acc[0][i];
+#pragma unroll
+              for (int bb = 1; bb < 8; ++bb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sel[i] = bb == tb ? acc[bb][i] : sel[i];
+              float z = sel[0];
+#pragma unroll
+              for (int i = 1; i < 16; ++i) z = i == ti ? sel[i] : z;
+              p.s.zt[n] = z;
+            }
+            st = nv == 128 ? score_tail<false>(p, acc, n, vb, nv, thr, true)
+                           : score_tail<true>(p, acc, n, vb, nv, thr, true);
+          }
+          // the two halves of a row: the second hands its record to the first
+          if (g == 1) {
+            red[r] = st.m;
+            red[128 + r] = st.S;
+            red[256 + r] = st.U;
+          }
+          named_bar_sync(1, 256);
+          if (g == 0 && row_ok) {
+            const Stat tot = stat_merge(st, Stat{red[r], red[128 + r], red[256 + r]}, p.c);
+            p.s.rec[o] = tot.m;
+            p.s.rec[p.rec_part + o] = tot.S;
+            p.s.rec[2 * p.rec_part + o] = tot.U;
+          }
+          named_bar_sync(1, 256);
+        } else {
+          if (row_ok && nv > 0) {
+            // only tiles among the row's K best, by (maximum, lowest index)
+            const int32_t* w = p.s.words + static_cast<size_t>(n) * row_words(p.K);
+            const float sm = __int_as_float(w[RW_SEL_M]);
+            const float m = p.s.rec[o];
+            if (w[RW_OVER] != 0 && (m > sm || (m == sm && vt <= w[RW_SEL_T]))) {
+              if (nv == 128) score_tail<false>(p, acc, n, vb, nv, sm, false);
+              else score_tail<true>(p, acc, n, vb, nv, sm, false);
+            }
+          }
+        }
+      } else if constexpr (OP == OP_DZ) {
+        // dz - (1/T) g_l 1[v = t] = -(1/T) p (g_l + g_H (log p + H)),
+        // p = e^(z/T - lse), written as p (a1 z + a0) with the row's own a1, a0
+        float a0 = 0.0f, a1 = 0.0f, l2 = 0.0f, gl = 0.0f;
+        int tl = -1;                        // the target's place in this half
+        if (n < p.B) {
+          const int tg = p.g.targets[n];
+          const float s = -p.inv_t * (p.g.scale != nullptr ? p.g.scale[0] : 1.0f);
+          const float lse = p.g.lse[n];
+          // (no such token: no term)
+          if (tg >= 0 && tg < p.K) {
+            gl = p.g.dlogp[n] * s;
+            tl = tg - p.t_off - vb;
+          }
+          a0 = gl;
+          if (p.g.dentropy != nullptr) {
+            const float gh = p.g.dentropy[n] * s;
+            a1 = gh * p.inv_t;
+            a0 = fmaf(gh, p.g.entropy[n] - lse, a0);
+          }
+          l2 = -lse * kLog2eScore;
+        }
+        if (vb < p.V && nw0 < p.B) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint4 w[4];
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float z = acc[2 * b + (i >> 4)][i & 15];
+              x[i] = exp2_approx(fmaf(z, p.c, l2)) * fmaf(z, a1, a0);
+            }
+            const bool hit = tl >= 32 * b && tl < 32 * b + 32;
+            if (__any_sync(0xffffffffu, hit)) {
+              float at = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                at = tl == 32 * b + i ? x[i] : at;
+                x[i] = tl == 32 * b + i ? 0.0f : x[i];
+              }
+              if (hit) p.coef[n] = at - gl;
+            }
+            const bool f16 = (p.idesc & (7u << 7)) == 0;   // the head's format
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k].x = pack16(x[8 * k], x[8 * k + 1], f16);
+              w[k].y = pack16(x[8 * k + 2], x[8 * k + 3], f16);
+              w[k].z = pack16(x[8 * k + 4], x[8 * k + 5], f16);
+              w[k].w = pack16(x[8 * k + 6], x[8 * k + 7], f16);
+            }
+            if (vb + 32 * b < p.V) stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, nw0);
+          }
+        }
+      } else if constexpr (OP == OP_DH) {
+        // fp32 partial sums of the segment, rows padded to whole tiles
+        const int row0 = t.seg * (p.n0 * 256) + nw0;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          uint4 w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = make_uint4(__float_as_uint(acc[b][4 * k]), __float_as_uint(acc[b][4 * k + 1]),
+                              __float_as_uint(acc[b][4 * k + 2]), __float_as_uint(acc[b][4 * k + 3]));
+          if (vb + 16 * b < p.K && nw0 < p.B)
+            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 16 * b, row0);
+        }
+      } else {
+        const bool f16 = (p.idesc & (7u << 7)) == 0;
+        if (nw0 < p.V) add_targets(p, acc, t.a0 >> 8, half + q * 32, vb, lane, f16);
+        const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint4 w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* x = &acc[2 * b + (k >> 1)][(k & 1) * 8];
+            w[k].x = pack16(x[0] * s, x[1] * s, f16);
+            w[k].y = pack16(x[2] * s, x[3] * s, f16);
+            w[k].z = pack16(x[4] * s, x[5] * s, f16);
+            w[k].w = pack16(x[6] * s, x[7] * s, f16);
+          }
+          if (vb + 32 * b < p.K && nw0 < p.V)
+            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, nw0);
+        }
+      }
+    }
+    if (failed && threadIdx.x == 128) atomicOr(p.err, ERR_TIMEOUT);
+    if (kStore) {
+      // the stores are complete before the CTA (and its shared memory) goes
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
+    }
+  }
+
+  // neither CTA leaves (or frees its tensor memory) before the leader's MMAs
+  // and both CTAs' remote arrivals are done
+  tc_fence_before();
+  cluster_sync();
+  grid_dep_launch();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512u);
+  }
+}
+
+}  // namespace detlm

@@ -1,0 +1,669 @@
+// score_host.cuh -- the host side of the score call, its gradient and the
+// scaled logits: argument checks, workspaces, tensor maps and launches. Part
+// of detlm_head.cu's translation unit (it uses that file's handle and
+// helpers).
+#pragma once
+
+namespace {
+
+constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
+constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
+
+// 2-D tensor map of 16-bit or 32-bit elements: `inner` contiguous, rows of
+// `stride` bytes.
+bool encode_box(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t inner,
+                int64_t outer, int64_t stride, uint32_t box_inner, uint32_t box_outer,
+                CUtensorMapSwizzle swizzle, bool load) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  load ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == DETLM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+int ensure_buffer(void** buf, size_t* have, size_t need, cudaStream_t stream) {
+  if (need <= *have) return DETLM_OK;
+  if (*buf != nullptr) {
+    cudaError_t e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    cudaFree(*buf);
+    *buf = nullptr;
+    *have = 0;
+  }
+  cudaError_t e = cudaMalloc(buf, need);
+  if (e != cudaSuccess) {
+    *buf = nullptr;
+    cudaGetLastError();
+    return status_from_cuda(e);
+  }
+  *have = need;
+  return DETLM_OK;
+}
+
+template <typename Kern, typename Params>
+cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned block, const Params& p,
+                             cudaStream_t stream) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// CTA pairs of the pair-product kernels that fit on the GPU at once (they all
+// have one shape: 384 threads, the full shared memory).
+cudaError_t op_pairs(detlm_head* h, int* pairs) {
+  if (h->op_pairs == 0) {
+    cudaError_t e = prepare_kernel<pairop_kernel<OP_DZ>>(kRegsLaunchWide);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = pair_layout(pair_stages()).total + 1024;
+    cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms & ~1));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, pairop_kernel<OP_DZ>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters <= 0) return cudaErrorInvalidConfiguration;
+    h->op_pairs = clusters < h->num_sms / 2 ? clusters : h->num_sms / 2;
+  }
+  *pairs = h->op_pairs;
+  return cudaSuccess;
+}
+
+// The stages of a product: all of shared memory, less the staging buffers of
+// those that store D (the score products need 1.5 KB there).
+template <int OP>
+int op_stages() {
+  if (OP != OP_SCORE && OP != OP_SELECT) return pair_stages();
+  int s = kPairMaxStages;
+  while (s > 2 && pairop_red_off(s) + kPairopRedBytes + 1024u > kSmemLimit) --s;
+  return s;
+}
+
+template <int OP>
+cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap& b,
+                          const CUtensorMap& o, PairOpParams p, cudaStream_t stream) {
+  cudaError_t e = prepare_kernel<pairop_kernel<OP>>(kRegsLaunchWide);
+  if (e != cudaSuccess) return e;
+  int pairs = 0;
+  e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return e;
+  p.stages = static_cast<uint16_t>(op_stages<OP>());
+  p.stall = static_cast<uint16_t>(h->stall);
+  p.err = h->d_err;
+  p.timeout_ns = h->timeout_ns;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.dynamicSmemBytes = (OP == OP_SCORE || OP == OP_SELECT)
+                             ? pairop_red_off(p.stages) + kPairopRedBytes + 1024u
+                             : pair_layout(p.stages).total + 1024u;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.units < pairs ? p.units : pairs)));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pairop_kernel<OP>, a, b, o, p);
+}
+
+// An ordinary (not programmatic) launch between a change of W on the stream
+// and a call whose kernels request W boxes before waiting for the stream: it
+// starts when everything before it is complete and visible.
+__global__ void weights_fence_kernel() {}
+
+void time_start(detlm_head* h, cudaStream_t stream) {
+  if (h->t_start) cudaEventRecord(h->t_start, stream);
+}
+void time_stop(detlm_head* h, cudaStream_t stream) {
+  if (h->t_stop) cudaEventRecord(h->t_stop, stream);
+  h->t_start = h->t_stop = nullptr;
+}
+
+// ------------------------------------------------------------------- score
+// Candidate blocks a row's list can hold: those of the tiles that run before
+// any threshold can reach them (two rounds of the pairs over n_rt row tiles),
+// what passes a threshold of K slots (see score_tail), and room. More is not
+// an error: such rows are computed again (OP_SELECT).
+int cand_blocks(int pairs, int64_t n_rt, int K) {
+  return 64 + 32 * K + 16 * static_cast<int>((pairs + n_rt - 1) / n_rt + 2);
+}
+
+struct ScoreLayout {
+  size_t logits, rec, rec_part, zt, words, words_bytes, tiles, cand, total;
+};
+// Narrow: logits [B][V], records [3][B][n_vt]. Wide: records, target logits,
+// row words and tile marks (cleared together), candidates.
+ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
+  ScoreLayout L;
+  std::memset(&L, 0, sizeof(L));
+  const bool narrow = B <= kNarrowRows;
+  size_t at = 0;
+  auto part = [&](size_t bytes) {
+    const size_t a = at;
+    at += round256(bytes);
+    return a;
+  };
+  const int64_t n_vt = narrow ? h->n_vt : tiles256(h->V);
+  if (narrow) L.logits = part(static_cast<size_t>(B) * h->V * 4);
+  L.rec_part = round256(static_cast<size_t>(B) * n_vt * 4) / 4;
+  L.rec = part(3 * L.rec_part * 4);
+  if (!narrow) {
+    const int64_t n_rt = (B + kRowsM - 1) / kRowsM;
+    L.zt = part(static_cast<size_t>(B) * 4);
+    L.words_bytes = (static_cast<size_t>(B) * row_words(K) + n_rt) * 4;
+    L.words = part(L.words_bytes);
+    L.tiles = L.words + static_cast<size_t>(B) * row_words(K) * 4;
+    // an upper bound of B * cand_blocks that grows with B, so that a
+    // workspace for B rows serves fewer
+    const size_t blocks = static_cast<size_t>(B) * (64 + 32 * K) +
+                          static_cast<size_t>(kRowsM) * 16 * (pairs + 3 * n_rt);
+    L.cand = part(K > 0 ? blocks * kCandFloats * 4 : 0);
+  }
+  L.total = at;
+  return L;
+}
+
+struct ScoreOut {
+  float* logp;
+  float* entropy;
+  float* lse;
+  int32_t* top_token;
+  float* top_logp;
+};
+
+void score_merge_params(ScoreMergeParams* mp, const detlm_head* h, const ScoreLayout& L, int64_t B,
+                        int K, float inv_t, const int32_t* targets, const ScoreOut& out) {
+  std::memset(mp, 0, sizeof(*mp));
+  float* rec = reinterpret_cast<float*>(static_cast<uint8_t*>(h->sws) + L.rec);
+  mp->V = static_cast<int32_t>(h->V);
+  mp->B = static_cast<int32_t>(B);
+  mp->K = K;
+  mp->c = kLog2eScore * inv_t;
+  mp->inv_t = inv_t;
+  mp->rec_m = rec;
+  mp->rec_s = rec + L.rec_part;
+  mp->rec_u = rec + 2 * L.rec_part;
+  mp->targets = targets;
+  mp->logp = out.logp;
+  mp->entropy = out.entropy;
+  mp->lse = out.lse;
+  mp->top_token = out.top_token;
+  mp->top_logp = out.top_logp;
+  mp->err = h->d_err;
+}
+
+int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t B, int K,
+                 float inv_t, const ScoreOut& out, cudaStream_t stream) {
+  const int N = cols_for(B);
+  CUtensorMap tmH;
+  if (!encode_2d(&tmH, h->dtype, h_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
+  const ScoreLayout L = score_layout(h, B, K, 0);
+  const int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
+  if (st != DETLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(h->sws);
+  float* rec = reinterpret_cast<float*>(ws + L.rec);
+  HeadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.V = static_cast<int32_t>(h->V);
+  p.d = static_cast<int32_t>(h->d);
+  p.B = static_cast<int32_t>(B);
+  p.N = N;
+  p.nk = h->nk;
+  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
+  p.n_vt = h->n_vt;
+  p.n_nt = 1;
+  p.n_slots = slots_for(N);
+  p.stages = stages_for(N);
+  p.n_issuers = issuers_for(N, p.stages, &p.n_slots);
+  p.tmem_cols = tmem_cols_for(p.n_slots * N);
+  p.idesc = idesc_f16(h->dtype == DETLM_BF16 ? 1u : 0u, kBM, static_cast<uint32_t>(N));
+  p.logits = reinterpret_cast<float*>(ws + L.logits);
+  p.rec_m = rec;
+  p.rec_s = rec + L.rec_part;
+  p.rec_i = reinterpret_cast<int32_t*>(rec + 2 * L.rec_part);
+  p.err = h->d_err;
+  p.stall = h->stall;
+  p.timeout_ns = h->timeout_ns;
+  p.temperature = kLog2eScore * inv_t;
+  const int grid = p.n_vt < h->num_sms ? p.n_vt : h->num_sms;
+  time_start(h, stream);
+  cudaError_t e = launch_gemm<MODE_SCORE>(h->tmW, tmH, p, grid, smem_layout(N, p.stages).total + 1024,
+                                          stream);
+  time_stop(h, stream);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  ScoreMergeParams mp;
+  score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
+  mp.n_vt = p.n_vt;
+  mp.logits = p.logits;
+  return status_from_cuda(launch_dependent(score_narrow_kernel, static_cast<unsigned>(B),
+                                           kScoreThreads, mp, stream));
+}
+
+int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t B, int K,
+               float inv_t, const ScoreOut& out, cudaStream_t stream) {
+  CUtensorMap tmH;
+  if (!encode_2d(&tmH, h->dtype, h_dev, h->d, B, static_cast<uint32_t>(kRowsHalf)))
+    return DETLM_EINVAL;
+  int pairs = 0;
+  cudaError_t e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  const ScoreLayout L = score_layout(h, B, K, pairs);
+  const int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
+  if (st != DETLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(h->sws);
+  const int64_t n_vt = tiles256(h->V), n_rt = (B + kRowsM - 1) / kRowsM;
+  if (n_vt * n_rt >= (int64_t{1} << 31)) return DETLM_EINVAL;
+  PairOpParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.B = static_cast<int32_t>(B);
+  p.V = static_cast<int32_t>(h->V);
+  p.n1 = static_cast<int32_t>(n_rt);
+  p.nk = h->nk;
+  p.seg = p.nk;
+  p.units = static_cast<int32_t>(n_vt * n_rt);
+  p.idesc = idesc_f16(h->dtype == DETLM_BF16 ? 1u : 0u, kRowsM, kRowsN);
+  p.K = K;
+  p.C = cand_blocks(pairs, n_rt, K);
+  p.c = kLog2eScore * inv_t;
+  p.inv_t = inv_t;
+  p.rec_part = static_cast<int64_t>(L.rec_part);
+  p.s.rec = reinterpret_cast<float*>(ws + L.rec);
+  p.s.zt = reinterpret_cast<float*>(ws + L.zt);
+  p.s.targets = targets;
+  p.s.words = reinterpret_cast<int32_t*>(ws + L.words);
+  p.s.cand = reinterpret_cast<float*>(ws + L.cand);
+  p.s.tile_over = reinterpret_cast<const int32_t*>(ws + L.tiles);
+  if (K > 0) {
+    e = cudaMemsetAsync(ws + L.words, 0, L.words_bytes, stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+  }
+  time_start(h, stream);
+  e = launch_pairop<OP_SCORE>(h, tmH, h->tmW, tmH, p, stream);
+  time_stop(h, stream);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  ScoreMergeParams mp;
+  score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
+  mp.n_vt = static_cast<int32_t>(n_vt);
+  mp.C = p.C;
+  mp.zt = p.s.zt;
+  mp.cand = p.s.cand;
+  mp.words = p.s.words;
+  mp.tile_over = reinterpret_cast<int32_t*>(ws + L.tiles);
+  e = launch_dependent(score_wide_kernel, static_cast<unsigned>(B), kScoreThreads, mp, stream);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  // a row's list can overflow only where it is shorter than all its blocks
+  if (K == 0 || 16 * n_vt <= p.C) return DETLM_OK;
+  e = launch_pairop<OP_SELECT>(h, tmH, h->tmW, tmH, p, stream);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  const int64_t blocks = (B + 15) / 16 < 2 * h->num_sms ? (B + 15) / 16 : 2 * h->num_sms;
+  return status_from_cuda(launch_dependent(score_select_kernel, static_cast<unsigned>(blocks),
+                                           kScoreThreads, mp, stream));
+}
+
+// ---------------------------------------------------------------- gradient
+// The vocabulary is passed over in pieces of whole 16384-entry segments, as
+// many as keep dz within kGradPassBytes (one at least).
+struct GradLayout {
+  int64_t pass;             // vocabulary entries of a pass
+  int64_t ld;               // dz row stride, elements
+  int64_t rows_pad, n_rt, n_dt;
+  size_t scale, coef, tiles, list, dz, part, acc, total;
+};
+GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
+  GradLayout L;
+  const int64_t seg = static_cast<int64_t>(kSegChunks) * kGradChunkBoxes * 64;
+  const int64_t segs = (h->V + seg - 1) / seg;
+  int64_t per = kGradPassBytes / (2 * seg * B);
+  per = per < 1 ? 1 : per > segs ? segs : per;
+  L.pass = per * seg;
+  const int64_t entries = L.pass < h->V ? L.pass : h->V;
+  L.ld = (entries + 63) / 64 * 64;
+  L.n_rt = (B + 255) / 256;
+  L.n_dt = (h->d + 255) / 256;
+  L.rows_pad = L.n_rt * 256;
+  size_t at = 0;
+  auto part = [&](size_t bytes) {
+    const size_t a = at;
+    at += round256(bytes);
+    return a;
+  };
+  L.scale = part(8);
+  L.coef = part(static_cast<size_t>(B) * 4);
+  L.tiles = part(static_cast<size_t>((entries + 255) / 256) * 8);
+  L.list = part(static_cast<size_t>(B) * 8);
+  L.dz = part(static_cast<size_t>(B) * L.ld * 2);
+  // split (few units) or whole segments, whichever is used
+  const bool split = per * L.n_rt * L.n_dt < 2 * pairs;
+  const int64_t parts = split ? per * kSegChunks : per;
+  L.part = part(static_cast<size_t>(parts) * L.rows_pad * h->d * 4);
+  L.acc = part(L.pass < h->V ? static_cast<size_t>(B) * h->d * 4 : 0);
+  L.total = at;
+  return L;
+}
+
+struct GradIn {
+  const void* h;
+  const int32_t* targets;
+  const float *lse, *entropy, *dlogp, *dentropy;
+};
+
+int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void* dh, void* dW,
+                   cudaStream_t stream) {
+  int pairs = 0;
+  cudaError_t e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  const GradLayout L = grad_layout(h, B, pairs);
+  const int st = ensure_buffer(&h->gws, &h->gws_bytes, L.total, stream);
+  if (st != DETLM_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(h->gws);
+  float* scale = h->dtype == DETLM_FP16 ? reinterpret_cast<float*>(ws + L.scale) : nullptr;
+  void* dz = ws + L.dz;
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  const CUtensorMapDataType t16 = map_type(h->dtype);
+  const uint32_t idesc = idesc_f16(h->dtype == DETLM_BF16 ? 1u : 0u, 256, 256);
+  const int64_t row = h->d * 2;
+
+  if (scale != nullptr) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    const float h_max = 1.0f + std::log(static_cast<float>(h->V));
+    e = cudaLaunchKernelEx(&cfg, grad_scale_kernel, in.dlogp, in.dentropy, in.targets,
+                           static_cast<int>(B), inv_t, h_max, scale);
+    if (e != cudaSuccess) return status_from_cuda(e);
+  }
+  time_start(h, stream);
+  for (int64_t v0 = 0; v0 < h->V; v0 += L.pass) {
+    const int64_t vc = h->V - v0 < L.pass ? h->V - v0 : L.pass;
+    const uint8_t* W = static_cast<const uint8_t*>(h->W) + v0 * row;
+    const int64_t n_vt = (vc + 255) / 256;
+    const int64_t vboxes = (vc + 63) / 64;
+    CUtensorMap hK, wK, zOut, zK, wN, pOut, zN, hN, dwOut;
+    if (!encode_box(&hK, t16, in.h, h->d, B, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+        !encode_box(&wK, t16, W, h->d, vc, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+        !encode_box(&zOut, t16, dz, vc, B, L.ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+      return DETLM_EINVAL;
+    PairOpParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.B = static_cast<int32_t>(B);
+    p.V = static_cast<int32_t>(vc);
+    p.n1 = static_cast<int32_t>(L.n_rt);
+    p.nk = h->nk;
+    p.seg = p.nk;
+    p.units = static_cast<int32_t>(n_vt * L.n_rt);
+    p.idesc = idesc;
+    p.K = static_cast<int32_t>(h->V);
+    p.t_off = static_cast<int32_t>(v0);
+    p.c = kLog2eScore * inv_t;
+    p.inv_t = inv_t;
+    p.coef = reinterpret_cast<float*>(ws + L.coef);
+    p.g.lse = in.lse;
+    p.g.entropy = in.entropy;
+    p.g.dlogp = in.dlogp;
+    p.g.dentropy = in.dentropy;
+    p.g.targets = in.targets;
+    p.g.scale = scale;
+    e = launch_pairop<OP_DZ>(h, hK, wK, zOut, p, stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    if (dh != nullptr) {
+      // whole segments per unit, or single chunks where those would leave
+      // SMs idle; the fold adds either in the same order
+      const int64_t seg_boxes = static_cast<int64_t>(kSegChunks) * kGradChunkBoxes;
+      const int64_t segs = (vboxes + seg_boxes - 1) / seg_boxes;
+      const bool split = (L.pass * L.n_rt * L.n_dt) / (seg_boxes * 64) < 2 * pairs;
+      const int64_t per_part = split ? kGradChunkBoxes : seg_boxes;
+      const int64_t parts = split ? (vboxes + per_part - 1) / per_part : segs;
+      if (!encode_box(&zK, t16, dz, vc, B, L.ld * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&wN, t16, W, h->d, vc, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&pOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, h->d, parts * L.rows_pad,
+                      h->d * 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+        return DETLM_EINVAL;
+      PairOpParams q = p;
+      q.n0 = static_cast<int32_t>(L.n_rt);
+      q.n1 = static_cast<int32_t>(L.n_dt);
+      q.nk = static_cast<int32_t>(vboxes);
+      q.seg = static_cast<int32_t>(per_part);
+      q.units = static_cast<int32_t>(parts * L.n_rt * L.n_dt);
+      q.K = static_cast<int32_t>(h->d);
+      q.idesc = idesc | kIdescMnB;
+      e = launch_pairop<OP_DH>(h, zK, wN, pOut, q, stream);
+      if (e != cudaSuccess) return status_from_cuda(e);
+      FoldParams f;
+      std::memset(&f, 0, sizeof(f));
+      f.part = part;
+      f.rows_pad = L.rows_pad;
+      f.B = static_cast<int32_t>(B);
+      f.d8 = static_cast<int32_t>(h->d / 8);
+      f.n_part = static_cast<int32_t>(parts);
+      f.per_seg = split ? kSegChunks : 1;
+      f.acc = reinterpret_cast<float*>(ws + L.acc);
+      f.first = v0 == 0;
+      f.last = v0 + L.pass >= h->V;
+      f.fp16 = h->dtype == DETLM_FP16;
+      f.scale = scale;
+      f.targets = in.targets;
+      f.coef = p.coef;
+      f.W = h->W;
+      f.V = static_cast<int32_t>(h->V);
+      f.out = static_cast<uint32_t*>(dh);
+      const int64_t blocks = (B * f.d8 + 255) / 256;
+      e = launch_dependent(grad_fold_kernel, static_cast<unsigned>(blocks), 256, f, stream);
+      if (e != cudaSuccess) return status_from_cuda(e);
+    }
+    if (dW != nullptr) {
+      uint8_t* out = static_cast<uint8_t*>(dW) + v0 * row;
+      if (!encode_box(&zN, t16, dz, vc, B, L.ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&hN, t16, in.h, h->d, B, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&dwOut, t16, out, h->d, vc, row, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+        return DETLM_EINVAL;
+      PairOpParams q = p;
+      q.n1 = static_cast<int32_t>(L.n_dt);
+      q.nk = static_cast<int32_t>((B + 63) / 64);
+      q.seg = q.nk;
+      q.units = static_cast<int32_t>(n_vt * L.n_dt);
+      q.K = static_cast<int32_t>(h->d);
+      q.idesc = idesc | kIdescMnA | kIdescMnB;
+      TargetListParams tl;
+      tl.targets = in.targets;
+      tl.B = p.B;
+      tl.v0 = p.t_off;
+      tl.vc = p.V;
+      tl.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+      tl.list = reinterpret_cast<int2*>(ws + L.list);
+      e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, tl, stream);
+      if (e != cudaSuccess) return status_from_cuda(e);
+      q.w.tiles = tl.tiles;
+      q.w.list = tl.list;
+      q.w.h = in.h;
+      q.w.scale = scale;
+      e = launch_pairop<OP_DW>(h, zN, hN, dwOut, q, stream);
+      if (e != cudaSuccess) return status_from_cuda(e);
+    }
+  }
+  time_stop(h, stream);
+  return DETLM_OK;
+}
+
+bool bad_temperature(float t) { return !(t > 0.0f) || !std::isfinite(t) || !std::isfinite(1.0f / t); }
+
+}  // namespace
+
+extern "C" {
+
+int detlm_head_weights_changed(detlm_head_t* h, cudaStream_t stream) {
+  if (h == nullptr) return DETLM_EINVAL;
+  h->w16_stale = true;
+  weights_fence_kernel<<<1, 32, 0, stream>>>();
+  return status_from_cuda(cudaGetLastError());
+}
+
+int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
+  if (h == nullptr || bad_B(max_B) || top_k < 0 || top_k > kTopMax) return DETLM_EINVAL;
+  if (h->P > 1 || h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (max_B == 0) return DETLM_OK;
+  const int64_t narrow = max_B < kNarrowRows ? max_B : kNarrowRows;
+  size_t need = score_layout(h, narrow, top_k, 0).total;
+  if (max_B > kNarrowRows) {
+    int pairs = 0;
+    const cudaError_t e = op_pairs(h, &pairs);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    const size_t wide = score_layout(h, max_B, top_k, pairs).total;
+    if (wide > need) need = wide;
+  }
+  return ensure_buffer(&h->sws, &h->sws_bytes, need, nullptr);
+}
+
+int detlm_head_score(detlm_head_t* h, const void* h_dev, const int32_t* targets_dev, int64_t B,
+                     int top_k, float temperature, float* logp_dev, float* entropy_dev,
+                     float* lse_dev, int32_t* top_token_dev, float* top_logp_dev,
+                     cudaStream_t stream) {
+  if (h == nullptr || bad_B(B) || bad_temperature(temperature)) return DETLM_EINVAL;
+  if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (top_k < 0 || top_k > kTopMax || top_k > h->V) return DETLM_EINVAL;
+  if (B == 0) return DETLM_OK;
+  if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
+  if ((targets_dev == nullptr) != (logp_dev == nullptr)) return DETLM_EINVAL;
+  if (!aligned(targets_dev, 4) || !aligned(logp_dev, 4)) return DETLM_EINVAL;
+  if (!aligned(entropy_dev, 4) || !aligned(lse_dev, 4)) return DETLM_EINVAL;
+  if (top_k > 0 && (top_token_dev == nullptr || top_logp_dev == nullptr ||
+                    !aligned(top_token_dev, 4) || !aligned(top_logp_dev, 4)))
+    return DETLM_EINVAL;
+  const ScoreOut out{logp_dev, entropy_dev, lse_dev, top_token_dev, top_logp_dev};
+  const float inv_t = 1.0f / temperature;
+  if (B <= kNarrowRows)
+    return score_narrow(h, h_dev, targets_dev, B, top_k, inv_t, out, stream);
+  return score_wide(h, h_dev, targets_dev, B, top_k, inv_t, out, stream);
+}
+
+int detlm_head_reserve_backward(detlm_head_t* h, int64_t max_B) {
+  if (h == nullptr || bad_B(max_B)) return DETLM_EINVAL;
+  if (h->P > 1 || h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (max_B == 0) return DETLM_OK;
+  int pairs = 0;
+  const cudaError_t e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  // a smaller call may split its segments (more partial sums): the largest
+  // of every 256-row step
+  size_t need = 0;
+  for (int64_t b = max_B; b > 0; b = (b - 1) / 256 * 256) {
+    const size_t n = grad_layout(h, b, pairs).total;
+    if (n > need) need = n;
+  }
+  return ensure_buffer(&h->gws, &h->gws_bytes, need, nullptr);
+}
+
+int detlm_head_score_backward(detlm_head_t* h, const void* h_dev, const int32_t* targets_dev,
+                              int64_t B, float temperature, const float* lse_dev,
+                              const float* entropy_dev, const float* dlogp_dev,
+                              const float* dentropy_dev, void* dh_dev, void* dW_dev,
+                              cudaStream_t stream) {
+  if (h == nullptr || bad_B(B) || bad_temperature(temperature)) return DETLM_EINVAL;
+  if (h->P > 1) return DETLM_EUNSUPPORTED;
+  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!aligned(dh_dev, 16) || !aligned(dW_dev, 16)) return DETLM_EINVAL;
+  if (B == 0) {   // no rows: the weight's gradient is zero
+    if (dW_dev == nullptr) return DETLM_OK;
+    return status_from_cuda(cudaMemsetAsync(dW_dev, 0, static_cast<size_t>(h->V) * h->d * 2, stream));
+  }
+  if (dh_dev == nullptr && dW_dev == nullptr) return DETLM_OK;
+  if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
+  if (targets_dev == nullptr || !aligned(targets_dev, 4)) return DETLM_EINVAL;
+  if (lse_dev == nullptr || !aligned(lse_dev, 4)) return DETLM_EINVAL;
+  if (dlogp_dev == nullptr || !aligned(dlogp_dev, 4)) return DETLM_EINVAL;
+  if (dentropy_dev != nullptr && (entropy_dev == nullptr || !aligned(entropy_dev, 4) ||
+                                  !aligned(dentropy_dev, 4)))
+    return DETLM_EINVAL;
+  const GradIn in{h_dev, targets_dev, lse_dev, entropy_dev, dlogp_dev, dentropy_dev};
+  return score_backward(h, in, B, 1.0f / temperature, dh_dev, dW_dev, stream);
+}
+
+int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* x_scale_dev,
+                             const float* w_scale_dev, int64_t B, int out_dtype, void* out_dev,
+                             cudaStream_t stream) {
+  if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
+  if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype != DETLM_INT8) return DETLM_EUNSUPPORTED;
+  int type = 0;
+  if (out_dtype == DETLM_FP32) type = OUT_F32;
+  else if (out_dtype == DETLM_BF16) type = OUT_BF16;
+  else if (out_dtype == DETLM_FP16) type = OUT_FP16;
+  else return DETLM_EINVAL;
+  const int size = type == OUT_F32 ? 4 : 2;
+  if (B == 0) return DETLM_OK;
+  if (q_dev == nullptr || !aligned(q_dev, 16)) return DETLM_EINVAL;
+  if (x_scale_dev == nullptr || !aligned(x_scale_dev, 4)) return DETLM_EINVAL;
+  if (w_scale_dev == nullptr || !aligned(w_scale_dev, 4)) return DETLM_EINVAL;
+  if (out_dev == nullptr || !aligned(out_dev, static_cast<size_t>(size))) return DETLM_EINVAL;
+  cudaError_t e;
+  if (B < kI8WideB) {
+    const int N = int8_cols_for(B, h->d);
+    CUtensorMap tmH;
+    if (!encode_2d(&tmH, DETLM_INT8, q_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
+    Int8Params p;
+    if (!int8_params(h, B, N, &p)) return DETLM_EINVAL;
+    p.logits = static_cast<int32_t*>(out_dev);
+    p.out_type = type;
+    p.x_scale = x_scale_dev;
+    p.w_scale = w_scale_dev;
+    const int64_t units = static_cast<int64_t>(p.n_vt) * p.n_nt;
+    const int grid = static_cast<int>(units < h->num_sms ? units : h->num_sms);
+    time_start(h, stream);
+    e = launch_int8_n<true>(N, h->tmW, tmH, p, grid, int8_layout(N, p.stages).total + 1024, stream);
+    time_stop(h, stream);
+    return status_from_cuda(e);
+  }
+  const int st = ensure_wide(h, B, stream);
+  if (st != DETLM_OK) return st;
+  e = i8_to_f16(q_dev, h->h16, static_cast<size_t>(B) * h->d, stream);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  CUtensorMap tmH;
+  if (!encode_2d(&tmH, DETLM_FP16, h->h16, h->d, B, static_cast<uint32_t>(kRowsHalf)))
+    return DETLM_EINVAL;
+  HeadParams p;
+  int8_wide_params(h, B, &p);
+  p.logits = static_cast<float*>(out_dev);
+  p.x_scale = x_scale_dev;
+  p.w_scale = w_scale_dev;
+  CUtensorMap tmL = tmH;   // not read unless the map is valid
+  const CUtensorMapDataType t = type == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : type == OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  p.tma_logits = (encode_logits(&tmL, out_dev, h->V, B, t, size) ? 1 : 0) | (type << 1);
+  const int64_t units = static_cast<int64_t>((p.n_vt + 1) / 2) * p.n_nt;
+  time_start(h, stream);
+  e = launch_pair_kernel<MODE_SCALED>(h, h->tmW16, tmH, tmL, p, units,
+                                      pair_layout(p.stages).total + 1024, stream);
+  time_stop(h, stream);
+  return status_from_cuda(e);
+}
+
+}  // extern "C"

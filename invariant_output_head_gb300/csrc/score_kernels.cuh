@@ -1,0 +1,551 @@
+// score_kernels.cuh -- from the projection's records to the score call's
+// outputs, one block of 256 threads per hidden row: warps 0..3 fold the
+// softmax statistics in the fixed tree, warps 4..7 meanwhile find the row's K
+// largest logits; then every thread ranks candidates.
+//
+// The K largest, from K disjoint maxima. Any K disjoint sets of entries have
+// K maxima; the smallest of those is a value that at least K entries reach.
+// With the sets' maxima at hand (tile records, or the slots of the wide
+// projection) this threshold costs no search, and only entries at or above it
+// -- K H_K of them on average for exchangeable entries, H_K the harmonic
+// number: 22 for K = 8, 130 for K = 32 -- need be ranked. A candidate's rank
+// is the number of candidates that come before it (larger value, or the same
+// value and a lower index), so every output slot has one writer and the
+// result does not depend on the order in which candidates were gathered.
+//
+// Bound: latency. A block makes four dependent rounds of loads (records,
+// their tree, the candidates' logits, the target), and a launch of up to ~1200
+// rows is one wave of blocks.
+#pragma once
+#include "head_kernels.cuh"
+#include "pairop_kernels.cuh"
+
+namespace detlm {
+
+constexpr int kScoreThreads = 256;
+constexpr int kTopMax = 32;          // alternatives a row can return
+constexpr int kEntryCap = 512;       // candidates ranked in shared memory
+constexpr int kTileCap = 512;        // tiles at or above the threshold
+
+struct ScoreMergeParams {
+  int32_t V, B, n_vt;       // n_vt: record tiles of a row
+  int32_t K, C;
+  float c, inv_t;
+  const float* rec_m;       // [B][n_vt]
+  const float* rec_s;
+  const float* rec_u;
+  const float* logits;      // narrow: [B][V]
+  const float* zt;          // wide: [B] target logits
+  const float* cand;        // wide: [B][C][kCandFloats]
+  int32_t* words;           // wide: [B][row_words(K)]
+  int32_t* tile_over;       // wide: [ceil(B / 256)]
+  const int32_t* targets;   // optional
+  float* logp;              // with targets
+  float* entropy;           // optional
+  float* lse;               // optional
+  int32_t* top_token;       // [B][K]
+  float* top_logp;          // [B][K]
+  int* err;
+};
+
+struct ScoreShared {
+  Stat part[4];
+  Stat tot;
+  uint32_t slots[kTopMax];
+  int n_tiles, n_entries;
+  int32_t tiles[kTileCap];
+  uint32_t key[kEntryCap];
+  int32_t id[kEntryCap];
+  unsigned long long best[kScoreThreads / 32];
+};
+
+// Statistics of a row, by 128 threads (warps 0 .. 3). Narrow records are of
+// 128-entry halves: a tile is the union of two.
+template <bool NARROW>
+__device__ __forceinline__ Stat row_stat(const ScoreMergeParams& p, size_t base, int g) {
+  const int n_tiles = NARROW ? (p.n_vt + 1) >> 1 : p.n_vt;
+  const int t1 = leaf_lo(g + 1, n_tiles);
+  Stat acc{-INFINITY, 0.0f, 0.0f};
+  auto rec = [&](int i) {
+    return i < p.n_vt ? Stat{p.rec_m[base + i], p.rec_s[base + i], p.rec_u[base + i]}
+                      : Stat{-INFINITY, 0.0f, 0.0f};
+  };
+#pragma unroll 2
+  for (int t = leaf_lo(g, n_tiles); t < t1; ++t)
+    acc = stat_merge(acc, NARROW ? stat_merge(rec(2 * t), rec(2 * t + 1), p.c) : rec(t), p.c);
+  return acc;
+}
+
+// Order of alternatives as one word: larger value first, then lower index.
+__device__ __forceinline__ unsigned long long order_word(uint32_t key, int32_t id) {
+  return (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+}
+
+// The entry of the whole block that comes first among those after `last`
+// (0: none left). visit(f) calls f(value, id) on this thread's share.
+template <typename Visit>
+__device__ __forceinline__ unsigned long long next_best(ScoreShared& sh, unsigned long long last,
+                                                        Visit visit) {
+  unsigned long long b = 0;
+  visit([&](float z, int32_t id) {
+    if (!(z == z)) return;                            // a NaN is no alternative
+    const unsigned long long o = order_word(score_key(z), id);
+    if (o < last && o > b) b = o;
+  });
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const unsigned long long x = __shfl_xor_sync(0xffffffffu, b, s);
+    b = x > b ? x : b;
+  }
+  __syncthreads();                                    // the previous round's reads are done
+  if ((threadIdx.x & 31) == 0) sh.best[threadIdx.x >> 5] = b;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kScoreThreads / 32; ++w) b = sh.best[w] > b ? sh.best[w] : b;
+  return b;
+}
+
+// Write the row's alternatives: by rank when the gathered entries fit, else
+// (very many equal values) one after the other by rescans.
+template <typename Visit>
+__device__ __forceinline__ void write_top(const ScoreMergeParams& p, ScoreShared& sh, int n,
+                                          Visit visit) {
+  const Stat tot = sh.tot;
+  const float log_s = logf(tot.S);
+  auto put = [&](int k, uint32_t key, int32_t id) {
+    const size_t o = static_cast<size_t>(n) * p.K + k;
+    p.top_token[o] = id;
+    p.top_logp[o] = (score_unkey(key) - tot.m) * p.inv_t - log_s;
+  };
+  const int ne = sh.n_entries;
+  int found = min(ne, p.K);
+  if (ne <= kEntryCap) {
+    for (int e = threadIdx.x; e < ne; e += kScoreThreads) {
+      const unsigned long long me = order_word(sh.key[e], sh.id[e]);
+      int rank = 0;
+      for (int j = 0; j < ne; ++j) rank += order_word(sh.key[j], sh.id[j]) > me;
+      if (rank < p.K) put(rank, sh.key[e], sh.id[e]);
+    }
+  } else {
+    unsigned long long last = ~0ull;
+    found = 0;
+    for (int k = 0; k < p.K; ++k) {
+      last = next_best(sh, last, visit);
+      if (last == 0) break;
+      found = k + 1;
+      if (threadIdx.x == 0)
+        put(k, static_cast<uint32_t>(last >> 32),
+            static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(last)));
+    }
+  }
+  // fewer logits than alternatives that are numbers
+  for (int k = found + threadIdx.x; k < p.K; k += kScoreThreads) {
+    p.top_token[static_cast<size_t>(n) * p.K + k] = -1;
+    p.top_logp[static_cast<size_t>(n) * p.K + k] = __int_as_float(0x7fc00000);
+  }
+}
+
+__device__ __forceinline__ void push_entry(ScoreShared& sh, float z, int32_t id, float thr) {
+  if (z >= thr) {
+    const int at = atomicAdd(&sh.n_entries, 1);
+    if (at < kEntryCap) {
+      sh.key[at] = score_key(z);
+      sh.id[at] = id;
+    }
+  }
+}
+
+// The row's statistics from the four warps' partial trees, and its outputs.
+__device__ __forceinline__ void write_stats(const ScoreMergeParams& p, ScoreShared& sh, int n,
+                                            float zt, int tg) {
+  const Stat tot = stat_merge(stat_merge(sh.part[0], sh.part[1], p.c),
+                              stat_merge(sh.part[2], sh.part[3], p.c), p.c);
+  sh.tot = tot;
+  const float log_s = logf(tot.S);
+  const float nan = __int_as_float(0x7fc00000);
+  const bool some = tot.m > -INFINITY;      // a row without a number has no distribution
+  if (p.lse != nullptr) p.lse[n] = some ? fmaf(tot.m, p.inv_t, log_s) : nan;
+  if (p.entropy != nullptr) p.entropy[n] = some ? log_s - (tot.U / tot.S) * p.inv_t : nan;
+  if (p.targets != nullptr) {
+    float lp = (zt - tot.m) * p.inv_t - log_s;
+    if (tg == -1) {
+      lp = 0.0f;                            // no token to score
+    } else if (tg < 0 || tg >= p.V) {
+      lp = nan;
+      atomicOr(p.err, ERR_TARGET);
+    }
+    p.logp[n] = lp;
+  }
+}
+
+// Up to 128 rows: logits [B][V] and 128-entry records.
+__global__ void __launch_bounds__(kScoreThreads) score_narrow_kernel(const ScoreMergeParams p) {
+  __shared__ ScoreShared sh;
+  grid_dep_launch();   // the next call's projection may start (it prefetches only W)
+  const int n = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t base = static_cast<size_t>(n) * p.n_vt;
+  const float* z = p.logits + static_cast<size_t>(n) * p.V;
+  const int g = static_cast<int>(threadIdx.x) - 128;
+  if (g >= 0 && g < kTopMax) sh.slots[g] = 0;
+  if (g == 0) sh.n_tiles = sh.n_entries = 0;
+  grid_dep_wait();     // records and logits are complete and visible
+  float zt = 0.0f;
+  int tg = -1;
+  if (threadIdx.x == 0 && p.targets != nullptr) {
+    tg = p.targets[n];
+    if (tg >= 0 && tg < p.V) zt = z[tg];
+  }
+  if (warp < 4) {
+    Stat x = row_stat<true>(p, base, threadIdx.x);
+#pragma unroll
+    for (int b = 1; b < 32; b <<= 1) x = stat_merge(x, shfl_xor(x, b), p.c);
+    if (lane == 0) sh.part[warp] = x;
+  } else if (p.K > 0) {
+    named_bar_sync(1, 128);                       // slots are zero
+    for (int t = g; t < p.n_vt; t += 128)
+      atomicMax(&sh.slots[t % p.K], score_key(p.rec_m[base + t]));
+    named_bar_sync(1, 128);
+    uint32_t lo = lane < p.K ? sh.slots[lane] : 0xFFFFFFFFu;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    const float thr = score_unkey(lo);
+    for (int t = g; t < p.n_vt; t += 128)
+      if (p.rec_m[base + t] >= thr) {
+        const int at = atomicAdd(&sh.n_tiles, 1);
+        if (at < kTileCap) sh.tiles[at] = t;
+      }
+    named_bar_sync(1, 128);
+    const int nt = sh.n_tiles;
+    if (nt > kTileCap) {
+      if (g == 0) sh.n_entries = kEntryCap + 1;   // rescans below
+    } else {
+      // four tiles at a time per warp: 16 loads in flight a lane
+      for (int i0 = (warp - 4) * 4; i0 < nt; i0 += 16) {
+        float x[4][4];
+        int v0[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v0[i] = i0 + i < nt ? sh.tiles[i0 + i] * kBM + lane : p.V;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[i][j] = v0[i] + 32 * j < p.V ? z[v0[i] + 32 * j] : __int_as_float(0x7fc00000);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) push_entry(sh, x[i][j], v0[i] + 32 * j, thr);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) write_stats(p, sh, n, zt, tg);
+  if (p.K == 0) return;
+  __syncthreads();
+  write_top(p, sh, n, [&](auto f) {
+    for (int v = threadIdx.x; v < p.V; v += kScoreThreads) f(z[v], v);
+  });
+}
+
+// The candidates of a wide row at or above thr into shared memory.
+__device__ __forceinline__ void gather_blocks(const ScoreMergeParams& p, ScoreShared& sh, int n,
+                                              int nb, float thr, int g, int threads) {
+  const float* cd = p.cand + static_cast<size_t>(n) * p.C * kCandFloats;
+  constexpr int kU = 4;
+  for (int i0 = g; i0 < nb * 4; i0 += threads * kU) {
+    float4 x[kU];
+    int v0[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int i = i0 + k * threads;
+      v0[k] = p.V;
+      if (i < nb * 4) {
+        const float* b = cd + static_cast<size_t>(i >> 2) * kCandFloats;
+        x[k] = reinterpret_cast<const float4*>(b)[i & 3];
+        v0[k] = __float_as_int(b[16]) * 16 + (i & 3) * 4;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (v0[k] < p.V) push_entry(sh, x[k].x, v0[k], thr);
+      if (v0[k] + 1 < p.V) push_entry(sh, x[k].y, v0[k] + 1, thr);
+      if (v0[k] + 2 < p.V) push_entry(sh, x[k].z, v0[k] + 2, thr);
+      if (v0[k] + 3 < p.V) push_entry(sh, x[k].w, v0[k] + 3, thr);
+    }
+  }
+}
+
+template <typename F>
+__device__ __forceinline__ void visit_blocks(const ScoreMergeParams& p, int n, int nb, F f) {
+  const float* cd = p.cand + static_cast<size_t>(n) * p.C * kCandFloats;
+  for (int i = threadIdx.x; i < nb * 16; i += kScoreThreads) {
+    const float* b = cd + static_cast<size_t>(i >> 4) * kCandFloats;
+    const int v = __float_as_int(b[16]) * 16 + (i & 15);
+    if (v < p.V) f(b[i & 15], v);
+  }
+}
+
+// More than 128 rows: 256-entry records, slots and candidate blocks. A row
+// whose list overflowed gets the exact rule for its K best tiles -- (maximum,
+// lowest index) of the K-th -- and its 256-row tile is marked for OP_SELECT.
+__global__ void __launch_bounds__(kScoreThreads) score_wide_kernel(const ScoreMergeParams p) {
+  __shared__ ScoreShared sh;
+  const int n = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t base = static_cast<size_t>(n) * p.n_vt;
+  const int g = static_cast<int>(threadIdx.x) - 128;
+  if (g == 0) sh.n_entries = 0;
+  grid_dep_launch();
+  grid_dep_wait();
+  int32_t* w = p.words + static_cast<size_t>(n) * row_words(p.K);
+  float zt = 0.0f;
+  int tg = -1;
+  if (threadIdx.x == 0 && p.targets != nullptr) {
+    tg = p.targets[n];
+    if (tg >= 0 && tg < p.V) zt = p.zt[n];
+  }
+  const int nb = p.K > 0 ? w[RW_COUNT] : 0;
+  const bool over = nb > p.C;
+  if (warp < 4) {
+    Stat x = row_stat<false>(p, base, threadIdx.x);
+#pragma unroll
+    for (int b = 1; b < 32; b <<= 1) x = stat_merge(x, shfl_xor(x, b), p.c);
+    if (lane == 0) sh.part[warp] = x;
+  } else if (p.K > 0 && !over) {
+    named_bar_sync(1, 128);                       // the entry count is zero
+    uint32_t lo = lane < p.K ? static_cast<uint32_t>(w[kRowWords + lane]) : 0xFFFFFFFFu;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    gather_blocks(p, sh, n, nb, score_unkey(lo), g, 128);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) write_stats(p, sh, n, zt, tg);
+  if (p.K == 0) return;
+  __syncthreads();
+  if (!over) {
+    write_top(p, sh, n, [&](auto f) { visit_blocks(p, n, nb, f); });
+    return;
+  }
+  unsigned long long last = ~0ull;
+  for (int k = 0; k < p.K; ++k) {
+    const unsigned long long b = next_best(sh, last, [&](auto f) {
+      for (int t = threadIdx.x; t < p.n_vt; t += kScoreThreads) f(p.rec_m[base + t], t);
+    });
+    if (b == 0) break;
+    last = b;
+  }
+  if (threadIdx.x == 0) {
+    w[RW_COUNT] = 0;
+    w[RW_SEL_M] = __float_as_int(score_unkey(static_cast<uint32_t>(last >> 32)));
+    w[RW_SEL_T] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(last));
+    w[RW_OVER] = 1;
+    p.tile_over[n >> 8] = 1;
+  }
+}
+
+// The rows that OP_SELECT served: alternatives from their second lists (K
+// tiles of 16 blocks at most, which the list always holds).
+__global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const ScoreMergeParams p) {
+  __shared__ ScoreShared sh;
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int n = blockIdx.x; n < p.B; n += gridDim.x) {
+    if (p.tile_over[n >> 8] == 0) continue;
+    const int32_t* w = p.words + static_cast<size_t>(n) * row_words(p.K);
+    if (w[RW_OVER] == 0) continue;
+    const size_t base = static_cast<size_t>(n) * p.n_vt;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n_entries = 0;
+    if (threadIdx.x < 128) {
+      Stat x = row_stat<false>(p, base, threadIdx.x);
+#pragma unroll
+      for (int b = 1; b < 32; b <<= 1) x = stat_merge(x, shfl_xor(x, b), p.c);
+      if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = x;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+      sh.tot = stat_merge(stat_merge(sh.part[0], sh.part[1], p.c),
+                          stat_merge(sh.part[2], sh.part[3], p.c), p.c);
+    const int nb = min(w[RW_COUNT], p.C);
+    gather_blocks(p, sh, n, nb, __int_as_float(w[RW_SEL_M]), threadIdx.x, kScoreThreads);
+    __syncthreads();
+    write_top(p, sh, n, [&](auto f) { visit_blocks(p, n, nb, f); });
+  }
+}
+
+// ------------------------------------------------------- gradient helpers
+// The power of two that dz of an fp16 head is held in: |dz| is at most
+// (|g_l| + |g_H| (1 + log V)) / T, whose largest value over the rows goes just
+// below 2^14. fp16 then keeps every dz above 2^-38 of that with its full 11
+// bits. (bf16 has fp32's exponents and needs none.) One block; the maximum is
+// exact, so the result does not depend on any order.
+__global__ void __launch_bounds__(1024)
+grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targets, int B,
+                  float inv_t, float h_max, float* scale) {
+  __shared__ float wm[32];
+  grid_dep_launch();
+  grid_dep_wait();
+  float m = 0.0f;
+  for (int n = threadIdx.x; n < B; n += 1024) {
+    float b = targets[n] >= 0 ? fabsf(dlogp[n]) : 0.0f;
+    if (dentropy != nullptr) b = fmaf(fabsf(dentropy[n]), h_max, b);
+    m = fmax_nan(m, b * inv_t);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
+  if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) m = fmax_nan(m, wm[w]);
+    int e = 0;
+    // frexp: m = f 2^e with f in [1/2, 1), so m 2^(14 - e) < 2^14; nothing to
+    // scale (all zero) or no number: 1
+    if (m > 0.0f && m < INFINITY) frexpf(m, &e);
+    int s = m > 0.0f && m < INFINITY ? 14 - e : 0;
+    s = max(-100, min(100, s));
+    scale[0] = ldexpf(1.0f, s);
+    scale[1] = ldexpf(1.0f, -s);
+  }
+}
+
+// The hidden rows by the vocabulary tile of their target, ascending within a
+// tile: block t counts the targets of lower tiles (its start) and then writes
+// its own rows in order. Targets outside [v0, v0 + vc) take no part. Every
+// block reads all B targets (from L2); no sums depend on an order.
+struct TargetListParams {
+  const int32_t* targets;
+  int32_t B, v0, vc;
+  int32_t* tiles;           // [n_vt][2]
+  int2* list;               // [B]
+};
+
+__global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams p) {
+  __shared__ int sums[8][2];
+  __shared__ int counts[8];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int tile = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int less = 0, mine = 0;
+  for (int n = threadIdx.x; n < p.B; n += 256) {
+    const int64_t t = static_cast<int64_t>(p.targets[n]) - p.v0;
+    if (p.targets[n] < 0 || t < 0 || t >= p.vc) continue;
+    less += (t >> 8) < tile;
+    mine += (t >> 8) == tile;
+  }
+  less = __reduce_add_sync(0xffffffffu, less);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) {
+    sums[warp][0] = less;
+    sums[warp][1] = mine;
+  }
+  __syncthreads();
+  less = mine = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    less += sums[w][0];
+    mine += sums[w][1];
+  }
+  if (threadIdx.x == 0) {
+    p.tiles[2 * tile] = less;
+    p.tiles[2 * tile + 1] = mine;
+  }
+  int at = less;
+  const int end = less + mine;
+  for (int n0 = 0; n0 < p.B && at < end; n0 += 256) {
+    const int n = n0 + threadIdx.x;
+    int64_t t = -1;
+    if (n < p.B && p.targets[n] >= 0) t = static_cast<int64_t>(p.targets[n]) - p.v0;
+    const bool hit = t >= 0 && t < p.vc && (t >> 8) == tile;
+    const uint32_t m = __ballot_sync(0xffffffffu, hit);
+    if (lane == 0) counts[warp] = __popc(m);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      before += w < warp ? counts[w] : 0;
+      all += counts[w];
+    }
+    if (hit)
+      p.list[at + before + __popc(m & ((1u << lane) - 1))] = make_int2(n, static_cast<int>(t & 255));
+    at += all;
+    __syncthreads();
+  }
+}
+
+// dh from the partial sums [n_part][rows_pad][d] (fp32): partials of a segment
+// are added in ascending order (per_seg of them; one when a unit covered the
+// whole segment), the segments' sums in ascending order onto the running
+// sum -- the same additions however the segments were split over units or
+// passes -- and last the target's entry of dz times its row of W.
+// Eight columns a thread; bound by reading the partials.
+struct FoldParams {
+  const float* part;
+  int64_t rows_pad;
+  int32_t B, d8;            // d / 8
+  int32_t n_part, per_seg;
+  float* acc;               // running sum [B][d] between passes
+  int32_t first, last;      // first pass: start from zero; last: write dh
+  int32_t fp16;
+  const float* scale;
+  const int32_t* targets;
+  const float* coef;        // [B] the target's entry of dz
+  const void* W;            // [V][d]
+  int32_t V;
+  uint32_t* out;            // dh [B][d], two elements a word
+};
+
+__global__ void __launch_bounds__(256) grad_fold_kernel(const FoldParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  if (i >= static_cast<int64_t>(p.B) * p.d8) return;
+  const int64_t step = p.rows_pad * p.d8 * 2;           // float4 per partial
+  const float4* src = reinterpret_cast<const float4*>(p.part) + i * 2;
+  float a[8];
+  float4* run = reinterpret_cast<float4*>(p.acc) + i * 2;
+  if (p.first) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = 0.0f;
+  } else {
+    const float4 x = run[0], y = run[1];
+    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+    a[4] = y.x; a[5] = y.y; a[6] = y.z; a[7] = y.w;
+  }
+  for (int s = 0; s < p.n_part; s += p.per_seg) {
+    float t[8];
+    const int e = min(s + p.per_seg, p.n_part);
+#pragma unroll 4
+    for (int j = s; j < e; ++j) {
+      const float4 x = __ldcs(src + j * step), y = __ldcs(src + j * step + 1);
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = j == s ? v[k] : __fadd_rn(t[k], v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = __fadd_rn(a[k], t[k]);
+  }
+  if (!p.last) {
+    run[0] = make_float4(a[0], a[1], a[2], a[3]);
+    run[1] = make_float4(a[4], a[5], a[6], a[7]);
+    return;
+  }
+  const float s = p.scale != nullptr ? p.scale[1] : 1.0f;
+  const bool f16 = p.fp16 != 0;
+  const int n = static_cast<int>(i / p.d8), c8 = static_cast<int>(i - static_cast<int64_t>(n) * p.d8);
+  const int tg = p.targets[n];
+  if (tg >= 0 && tg < p.V) {
+    const float g = p.coef[n];
+    const uint4 w = reinterpret_cast<const uint4*>(p.W)[static_cast<size_t>(tg) * p.d8 + c8];
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = unpack16(x[k], f16);
+      a[2 * k] = fmaf(g, v.x, a[2 * k]);
+      a[2 * k + 1] = fmaf(g, v.y, a[2 * k + 1]);
+    }
+  }
+  reinterpret_cast<uint4*>(p.out)[i] =
+      make_uint4(pack16(a[0] * s, a[1] * s, f16), pack16(a[2] * s, a[3] * s, f16),
+                 pack16(a[4] * s, a[5] * s, f16), pack16(a[6] * s, a[7] * s, f16));
+}
+
+}  // namespace detlm
