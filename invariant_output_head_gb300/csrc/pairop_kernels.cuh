@@ -30,13 +30,13 @@
 // value contributes a row of W to dh and a row of h to dW, added in fp32
 // (grad_fold_kernel, and this kernel's OP_DW epilogue).
 //
-// The first three use the logits' own arithmetic (128-element K chunks, each
+// The first two use the logits' own arithmetic (128-element K chunks, each
 // accumulated from zero and added in fp32 in ascending order), so they see
-// the bits that every other call of the head computes. The gradient products
-// contract over the vocabulary or the rows, in chunks of 2048: 128 MMA steps
-// of the tensor core's accumulation before a round-to-nearest fp32 add, which
-// leaves at most about 128 half-ulps of fp32 (8e-6) per chunk, far below the
-// 16-bit rounding of what goes in (dz) and comes out.
+// the bits that every other call of the head computes. The gradient's three
+// products run in chunks of 2048: 128 MMA steps of the tensor core's
+// accumulation before a round-to-nearest fp32 add, which leaves at most about
+// 128 half-ulps of fp32 (8e-6) per chunk, far below the 16-bit rounding of dz
+// and of what comes out; one sixteenth of the drains.
 //
 // Operands with the free axis contiguous ("MN-major") are loaded as boxes of
 // 64 free x 64 contracted elements, 128-byte swizzle: 64 rows of 128 bytes,
@@ -64,12 +64,6 @@ constexpr int kRowWords = 4;             // words of a row before its slots
 enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
 
 __host__ __device__ constexpr int row_words(int K) { return kRowWords + ((K + 3) & ~3); }
-
-// Offset of the score products' half-row records, behind the control words.
-__host__ __device__ inline uint32_t pairop_red_off(int stages) {
-  return pair_layout(stages).ctrl_off + (2u * stages + 6u) * 8u + 16u;
-}
-constexpr uint32_t kPairopRedBytes = 3u * 128u * 4u;
 
 // MN-major operand tile in the 128-byte swizzle layout written by TMA as
 // boxes of 64 (free) x 64 (contracted) 16-bit elements.
@@ -168,24 +162,51 @@ __device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, int u) {
   return t;
 }
 
-// 32 rows x 64 bytes of a warp (lane = row) through one of its two staging
-// buffers to the tensor map's box at (c0, row0); asynchronous.
+// Staging of D: per epilogue warp two buffers of 32 rows x 128 bytes (whole
+// cache lines leave; 128-byte swizzle: 16-byte chunk c of row r sits at chunk
+// c ^ (r & 7)), each stored by the tensor map's box while the warp goes on.
+constexpr uint32_t kOpStageBuf = 32 * 128;
+constexpr uint32_t kOpXsBytes = 2 * kOpStageBuf;
+constexpr int kOpMaxStages = 7;
+
+struct OpLayout {
+  uint32_t a_bytes, stage_bytes, ctrl_off, red_off, xs_off, store_total, score_total;
+};
+// Stage s: this CTA's 128 rows of A, then its 128 of B (128 bytes of K each,
+// or two MN-major boxes of 8 KB each); then the barriers (full[S], empty[S],
+// slot_full[2], slot_empty[2], never, drain), the TMEM address holder and the
+// abort flag; then the staging buffers, or the score products' half-row
+// records [3][128].
+__host__ __device__ inline OpLayout op_layout(int stages) {
+  OpLayout L;
+  L.a_bytes = kRowsHalf * kRowBytes;
+  L.stage_bytes = 2 * L.a_bytes;
+  L.ctrl_off = static_cast<uint32_t>(stages) * L.stage_bytes;
+  L.red_off = L.ctrl_off + (2u * stages + 6u) * 8u + 16u;
+  L.score_total = L.red_off + 3u * 128u * 4u;
+  L.xs_off = (L.red_off + 1023u) & ~1023u;
+  L.store_total = L.xs_off + 8u * kOpXsBytes;
+  return L;
+}
+
+// 32 rows x 128 bytes of a warp (lane = row) to the tensor map's box at
+// (c0, row0); asynchronous.
 __device__ __forceinline__ void stage_store(const void* tmap, uint8_t* xs, uint32_t xs_u32,
-                                            uint32_t& nbuf, const uint4 (&w)[4], int lane, int c0,
+                                            uint32_t& nbuf, const uint4 (&w)[8], int lane, int c0,
                                             int row0) {
   const uint32_t buf = nbuf & 1u;
   if (nbuf >= 2) {
     if (lane == 0) bulk_wait_group_read<1>();   // this buffer's previous store has read it
     __syncwarp();
   }
-  uint8_t* sb = xs + buf * kPairStageBuf;
+  uint8_t* sb = xs + buf * kOpStageBuf;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    *reinterpret_cast<uint4*>(sb + lane * 64 + 16 * (k ^ ((lane >> 1) & 3))) = w[k];
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint4*>(sb + lane * 128 + 16 * (k ^ (lane & 7))) = w[k];
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    tma_store_2d(tmap, xs_u32 + buf * kPairStageBuf, c0, row0);
+    tma_store_2d(tmap, xs_u32 + buf * kOpStageBuf, c0, row0);
     bulk_commit_group();
   }
   ++nbuf;
@@ -315,14 +336,14 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   constexpr bool kLogits = kScore || OP == OP_DZ;      // D = h W^T
   constexpr bool kStore = !kScore;                     // D leaves through staging and tmO
   constexpr bool kMnA = OP == OP_DW, kMnB = OP == OP_DH || OP == OP_DW;
-  constexpr int kBoxes = kLogits ? kBlocksPerChunk : kGradChunkBoxes;
+  constexpr int kBoxes = kScore ? kBlocksPerChunk : kGradChunkBoxes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int S = p.stages;
-  const PairLayout L = pair_layout(S);             // without staging: the same up to xs_off
+  const OpLayout L = op_layout(S);
   const uint32_t rank = cluster_rank();            // 0: leader, 1: peer
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int n_pairs = static_cast<int>(gridDim.x >> 1);
@@ -339,7 +360,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // after the control words: staging buffers (1024-byte aligned), or the
   // half-row records [3][128]
-  uint8_t* tail = smem + (kStore ? L.xs_off : pairop_red_off(S));
+  uint8_t* tail = smem + (kStore ? L.xs_off : L.red_off);
   const uint32_t smem_base = smem_u32(smem);
   auto sA = [&](int s) { return smem_base + static_cast<uint32_t>(s) * L.stage_bytes; };
   auto sB = [&](int s) { return sA(s) + L.a_bytes; };
@@ -497,7 +518,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int g = (warp - 4) >> 2;             // column half of the unit
     const int r = q * 32 + lane;               // row within this CTA's half
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    uint8_t* xs = tail + (warp - 4) * kPairXsBytes;
+    uint8_t* xs = tail + (warp - 4) * kOpXsBytes;
     const uint32_t xs_u32 = smem_u32(xs);
     float* red = reinterpret_cast<float*>(tail);              // [3][128]
     uint32_t nbuf = 0;                         // staging buffers used so far
@@ -653,66 +674,68 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           l2 = -lse * kLog2eScore;
         }
         if (vb < p.V && nw0 < p.B) {
+          const bool f16 = (p.idesc & (7u << 7)) == 0;   // the head's format
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            uint4 w[4];
-            float x[32];
+          for (int b = 0; b < 2; ++b) {
+            uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float z = acc[2 * b + (i >> 4)][i & 15];
-              x[i] = exp2_approx(fmaf(z, p.c, l2)) * fmaf(z, a1, a0);
-            }
-            const bool hit = tl >= 32 * b && tl < 32 * b + 32;
-            if (__any_sync(0xffffffffu, hit)) {
-              float at = 0.0f;
+            for (int hb = 0; hb < 2; ++hb) {
+              const int c0 = 64 * b + 32 * hb;             // first of 32 columns
+              float x[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                at = tl == 32 * b + i ? x[i] : at;
-                x[i] = tl == 32 * b + i ? 0.0f : x[i];
+                const float z = acc[(c0 + i) >> 4][i & 15];
+                x[i] = exp2_approx(fmaf(z, p.c, l2)) * fmaf(z, a1, a0);
               }
-              if (hit) p.coef[n] = at - gl;
-            }
-            const bool f16 = (p.idesc & (7u << 7)) == 0;   // the head's format
+              const bool hit = tl >= c0 && tl < c0 + 32;
+              if (__any_sync(0xffffffffu, hit)) {
+                float at = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[k].x = pack16(x[8 * k], x[8 * k + 1], f16);
-              w[k].y = pack16(x[8 * k + 2], x[8 * k + 3], f16);
-              w[k].z = pack16(x[8 * k + 4], x[8 * k + 5], f16);
-              w[k].w = pack16(x[8 * k + 6], x[8 * k + 7], f16);
+                for (int i = 0; i < 32; ++i) {
+                  at = tl == c0 + i ? x[i] : at;
+                  x[i] = tl == c0 + i ? 0.0f : x[i];
+                }
+                if (hit) p.coef[n] = at - gl;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[4 * hb + k] = make_uint4(
+                    pack16(x[8 * k], x[8 * k + 1], f16), pack16(x[8 * k + 2], x[8 * k + 3], f16),
+                    pack16(x[8 * k + 4], x[8 * k + 5], f16), pack16(x[8 * k + 6], x[8 * k + 7], f16));
             }
-            if (vb + 32 * b < p.V) stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, nw0);
+            if (vb + 64 * b < p.V) stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 64 * b, nw0);
           }
         }
       } else if constexpr (OP == OP_DH) {
         // fp32 partial sums of the segment, rows padded to whole tiles
         const int row0 = t.seg * (p.n0 * 256) + nw0;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          uint4 w[4];
+        for (int b = 0; b < 4; ++b) {
+          uint4 w[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = make_uint4(__float_as_uint(acc[b][4 * k]), __float_as_uint(acc[b][4 * k + 1]),
-                              __float_as_uint(acc[b][4 * k + 2]), __float_as_uint(acc[b][4 * k + 3]));
-          if (vb + 16 * b < p.K && nw0 < p.B)
-            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 16 * b, row0);
+          for (int k = 0; k < 8; ++k) {
+            const float* x = &acc[2 * b + (k >> 2)][4 * (k & 3)];
+            w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                              __float_as_uint(x[3]));
+          }
+          if (vb + 32 * b < p.K && nw0 < p.B)
+            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, row0);
         }
       } else {
         const bool f16 = (p.idesc & (7u << 7)) == 0;
         if (nw0 < p.V) add_targets(p, acc, t.a0 >> 8, half + q * 32, vb, lane, f16);
         const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint4 w[4];
+        for (int b = 0; b < 2; ++b) {
+          uint4 w[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float* x = &acc[2 * b + (k >> 1)][(k & 1) * 8];
-            w[k].x = pack16(x[0] * s, x[1] * s, f16);
-            w[k].y = pack16(x[2] * s, x[3] * s, f16);
-            w[k].z = pack16(x[4] * s, x[5] * s, f16);
-            w[k].w = pack16(x[6] * s, x[7] * s, f16);
+          for (int k = 0; k < 8; ++k) {
+            const float* x = &acc[4 * b + (k >> 1)][(k & 1) * 8];
+            w[k] = make_uint4(pack16(x[0] * s, x[1] * s, f16), pack16(x[2] * s, x[3] * s, f16),
+                              pack16(x[4] * s, x[5] * s, f16), pack16(x[6] * s, x[7] * s, f16));
           }
-          if (vb + 32 * b < p.K && nw0 < p.V)
-            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, nw0);
+          if (vb + 64 * b < p.K && nw0 < p.V)
+            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 64 * b, nw0);
         }
       }
     }

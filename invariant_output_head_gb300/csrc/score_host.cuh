@@ -6,6 +6,9 @@
 
 namespace {
 
+// Scaled logits of as many rows as this run on the fp16 copies: above 64 rows
+// the int8-streaming kernel converts W again for every 64.
+constexpr int64_t kI8ScaledWideB = 65;
 constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
 constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
 
@@ -71,7 +74,7 @@ cudaError_t op_pairs(detlm_head* h, int* pairs) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = pair_layout(pair_stages()).total + 1024;
+    cfg.dynamicSmemBytes = kSmemLimit;
     cfg.gridDim = dim3(static_cast<unsigned>(h->num_sms & ~1));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -90,13 +93,17 @@ cudaError_t op_pairs(detlm_head* h, int* pairs) {
   return cudaSuccess;
 }
 
-// The stages of a product: all of shared memory, less the staging buffers of
-// those that store D (the score products need 1.5 KB there).
+// The shared memory and stages of a product: as many stages as fit beside
+// the staging buffers, or beside the score products' records.
+template <int OP>
+uint32_t op_smem(int stages) {
+  const OpLayout L = op_layout(stages);
+  return (OP == OP_SCORE || OP == OP_SELECT ? L.score_total : L.store_total) + 1024u;
+}
 template <int OP>
 int op_stages() {
-  if (OP != OP_SCORE && OP != OP_SELECT) return pair_stages();
-  int s = kPairMaxStages;
-  while (s > 2 && pairop_red_off(s) + kPairopRedBytes + 1024u > kSmemLimit) --s;
+  int s = kOpMaxStages;
+  while (s > 2 && op_smem<OP>(s) > kSmemLimit) --s;
   return s;
 }
 
@@ -115,9 +122,7 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.blockDim = dim3(kRowsThreads);
-  cfg.dynamicSmemBytes = (OP == OP_SCORE || OP == OP_SELECT)
-                             ? pairop_red_off(p.stages) + kPairopRedBytes + 1024u
-                             : pair_layout(p.stages).total + 1024u;
+  cfg.dynamicSmemBytes = op_smem<OP>(p.stages);
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.units < pairs ? p.units : pairs)));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -409,7 +414,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
     CUtensorMap hK, wK, zOut, zK, wN, pOut, zN, hN, dwOut;
     if (!encode_box(&hK, t16, in.h, h->d, B, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
         !encode_box(&wK, t16, W, h->d, vc, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-        !encode_box(&zOut, t16, dz, vc, B, L.ld * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+        !encode_box(&zOut, t16, dz, vc, B, L.ld * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
       return DETLM_EINVAL;
     PairOpParams p;
     std::memset(&p, 0, sizeof(p));
@@ -444,7 +449,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       if (!encode_box(&zK, t16, dz, vc, B, L.ld * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&wN, t16, W, h->d, vc, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&pOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, h->d, parts * L.rows_pad,
-                      h->d * 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+                      h->d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
         return DETLM_EINVAL;
       PairOpParams q = p;
       q.n0 = static_cast<int32_t>(L.n_rt);
@@ -482,7 +487,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       uint8_t* out = static_cast<uint8_t*>(dW) + v0 * row;
       if (!encode_box(&zN, t16, dz, vc, B, L.ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&hN, t16, in.h, h->d, B, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-          !encode_box(&dwOut, t16, out, h->d, vc, row, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, false))
+          !encode_box(&dwOut, t16, out, h->d, vc, row, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
         return DETLM_EINVAL;
       PairOpParams q = p;
       q.n1 = static_cast<int32_t>(L.n_dt);
@@ -624,7 +629,7 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   if (w_scale_dev == nullptr || !aligned(w_scale_dev, 4)) return DETLM_EINVAL;
   if (out_dev == nullptr || !aligned(out_dev, static_cast<size_t>(size))) return DETLM_EINVAL;
   cudaError_t e;
-  if (B < kI8WideB) {
+  if (B < kI8ScaledWideB) {
     const int N = int8_cols_for(B, h->d);
     CUtensorMap tmH;
     if (!encode_2d(&tmH, DETLM_INT8, q_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
