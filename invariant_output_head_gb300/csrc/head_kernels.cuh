@@ -66,6 +66,12 @@ constexpr int kRowBytes = 128;    // bytes of K per stage and tile row (one swiz
 constexpr int kMaxN = 256;        // largest MMA N
 constexpr int kChunkK = 128;      // K elements per accumulation chunk
 constexpr int kBlocksPerChunk = kChunkK / 64;   // 128-byte K blocks of 16-bit data
+// The score call accumulates longer chunks (four times the MMA steps before a
+// round-to-nearest add): the drains of 128-element chunks hold the wide
+// projection to ~0.72 us a chunk where its MMAs take 0.52. Its logits differ
+// from the other calls' in their last bits for that (by at most 32 half-ulps
+// of a chunk's running sum); they are the same on both of its projections.
+constexpr int kScoreChunkK = 512;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSlots = 8;
 constexpr int kSmemLimit = 232448;  // 227 KB dynamic shared memory per CTA
@@ -625,13 +631,15 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
     if constexpr (EW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
     const int which = warp == 1 ? 0 : warp - (E0 + EW) + 1;   // chunks which, which + NWAY, ...
     if (lane == 0 && which < NWAY) {
-      constexpr int SPC = kBlocksPerChunk / KPS;     // pipeline stages per chunk
+      constexpr int CHUNK = MODE == MODE_SCORE ? kScoreChunkK / 64 : kBlocksPerChunk;   // K boxes
+      constexpr int SPC = CHUNK / KPS;               // pipeline stages per chunk
       // ring lengths must be multiples of NWAY (the host only enables two
       // issuers then)
       bool ok = S % NWAY == 0 && p.n_slots % NWAY == 0 && NWAY <= S && NWAY <= p.n_slots;
       if (p.stall) ok = ok && mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
-      if constexpr (max_mma_issuers(N) == 1) {
-        // one issuer (N = 256, 40 registers): ring positions by increments
+      if constexpr (max_mma_issuers(N) == 1 || MODE == MODE_SCORE) {
+        // one issuer (N = 256, 40 registers; score: chunks of several
+        // stages): ring positions by increments
         uint32_t stage = 0, phase = 0, slot = 0, sph = 0;
         for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
           for (int c = 0; c < p.n_chunks && ok; ++c) {
@@ -640,7 +648,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
             const uint32_t d_tmem = tmem_base + slot * static_cast<uint32_t>(N);
 #pragma unroll
             for (int sc = 0; sc < SPC; ++sc) {
-              const int kb0 = c * kBlocksPerChunk + sc * KPS;
+              const int kb0 = c * CHUNK + sc * KPS;
               if (kb0 >= p.nk) break;
               if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
               tc_fence_after();
@@ -648,7 +656,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
               for (int b = 0; b < nb; ++b) {
                 const uint64_t da = sdesc_sw128(sA(stage) + b * kBM * kRowBytes);
                 const uint64_t db = sdesc_sw128(sB(stage) + b * N * kRowBytes);
-                const bool first = (kb0 + b) == c * kBlocksPerChunk;
+                const bool first = (kb0 + b) == c * CHUNK;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   mma_f16(d_tmem, da + 2u * k, db + 2u * k, p.idesc, !(first && k == 0));

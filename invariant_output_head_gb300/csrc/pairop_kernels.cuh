@@ -336,7 +336,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   constexpr bool kLogits = kScore || OP == OP_DZ;      // D = h W^T
   constexpr bool kStore = !kScore;                     // D leaves through staging and tmO
   constexpr bool kMnA = OP == OP_DW, kMnB = OP == OP_DH || OP == OP_DW;
-  constexpr int kBoxes = kScore ? kBlocksPerChunk : kGradChunkBoxes;
+  constexpr int kBoxes = kScore ? kScoreChunkK / 64 : kGradChunkBoxes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -479,7 +479,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + slot * 256u;
           const int nb = min(kBoxes, nkb - c0);
-#pragma unroll(kBoxes <= 2 ? kBoxes : 1)
+#pragma unroll 1
           for (int sc = 0; sc < kBoxes; ++sc) {
             if (sc >= nb) break;
             if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }

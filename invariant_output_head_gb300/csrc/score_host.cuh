@@ -240,12 +240,12 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
   p.B = static_cast<int32_t>(B);
   p.N = N;
   p.nk = h->nk;
-  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
+  p.n_chunks = static_cast<int32_t>((h->d + kScoreChunkK - 1) / kScoreChunkK);
   p.n_vt = h->n_vt;
   p.n_nt = 1;
   p.n_slots = slots_for(N);
   p.stages = stages_for(N);
-  p.n_issuers = issuers_for(N, p.stages, &p.n_slots);
+  p.n_issuers = 1;
   p.tmem_cols = tmem_cols_for(p.n_slots * N);
   p.idesc = idesc_f16(h->dtype == DETLM_BF16 ? 1u : 0u, kBM, static_cast<uint32_t>(N));
   p.logits = reinterpret_cast<float*>(ws + L.logits);
