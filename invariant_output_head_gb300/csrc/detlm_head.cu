@@ -379,11 +379,9 @@ int pair_stages() {
 // memory with 16-byte aligned rows (V a multiple of 4, a 16-byte aligned
 // base); otherwise (host memory the kernel writes through its mapping, such
 // as the asynchronous host-buffer calls' pinned buffers) the kernel stores
-// the logits with plain stores (returns false). Two-byte logits (the scaled
-// call): box 32 x 32, V a multiple of 8.
-bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B,
-                   CUtensorMapDataType type, int size = 4) {
-  if (logits == nullptr || (V * size) % 16 != 0 || !aligned(logits, 16)) return false;
+// the logits with plain stores (returns false).
+bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B, bool int32) {
+  if (logits == nullptr || (V & 3) != 0 || !aligned(logits, 16)) return false;
   cudaPointerAttributes pa;
   if (cudaPointerGetAttributes(&pa, logits) != cudaSuccess) {
     cudaGetLastError();   // clear the error the query recorded
@@ -391,10 +389,11 @@ bool encode_logits(CUtensorMap* m, const void* logits, int64_t V, int64_t B,
   }
   if (pa.type != cudaMemoryTypeDevice) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(V), static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(V) * size};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32u};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(V) * 4u};
+  cuuint32_t box[2] = {16u, 32u};
   cuuint32_t estr[2] = {1, 1};
-  return g_encode(m, type, 2, const_cast<void*>(logits), dims, strides, box, estr,
+  return g_encode(m, int32 ? CU_TENSOR_MAP_DATA_TYPE_INT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                  const_cast<void*>(logits), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -569,7 +568,7 @@ int launch_float(detlm_head* h, const void* h_dev, int64_t B, const int32_t* tar
                              : static_cast<int64_t>(p.n_vt) * p.n_nt;
   const int grid = static_cast<int>(units < h->num_sms ? units : h->num_sms);
   CUtensorMap tmL = tmH;   // the pair kernel's logits map; not read unless valid
-  if (wide) p.tma_logits = encode_logits(&tmL, logits, h->V, B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32) ? 1 : 0;
+  if (wide) p.tma_logits = encode_logits(&tmL, logits, h->V, B, false) ? 1 : 0;
   if (h->t_start) cudaEventRecord(h->t_start, stream);
   cudaError_t e;
   if constexpr (rows) {
@@ -718,30 +717,6 @@ int ensure_wide(detlm_head* h, int64_t B, cudaStream_t stream) {
   return DETLM_OK;
 }
 
-// Launch parameters of the wide integer path that do not depend on what the
-// call writes.
-void int8_wide_params(const detlm_head* h, int64_t B, HeadParams* out) {
-  HeadParams& p = *out;
-  std::memset(&p, 0, sizeof(p));
-  p.V = static_cast<int32_t>(h->V);
-  p.d = static_cast<int32_t>(h->d);
-  p.B = static_cast<int32_t>(B);
-  p.N = kPairN;
-  p.n_vt = h->n_vt;
-  p.n_nt = static_cast<int32_t>((B + kPairN - 1) / kPairN);
-  p.nk = static_cast<int32_t>((h->d * 2 + kRowBytes - 1) / kRowBytes);
-  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
-  p.n_slots = 2;
-  p.stages = pair_stages();
-  p.n_issuers = 1;
-  p.tmem_cols = 512;
-  p.idesc = idesc_f16(0u, 2 * kBM, kPairN);
-  p.err = h->d_err;
-  p.stall = h->stall;
-  p.timeout_ns = h->timeout_ns;
-  p.v_off = static_cast<int32_t>(h->v_off);
-}
-
 int launch_int8_wide(detlm_head* h, const void* h_dev, int64_t B, int32_t* token, int32_t* gap,
                      int32_t* logits, cudaStream_t stream, ShardRec* shard_out = nullptr) {
   cudaError_t e;
@@ -759,15 +734,32 @@ int launch_int8_wide(detlm_head* h, const void* h_dev, int64_t B, int32_t* token
   const WsView w = ws_view(h);
 
   HeadParams p;
-  int8_wide_params(h, B, &p);
+  std::memset(&p, 0, sizeof(p));
+  p.V = static_cast<int32_t>(h->V);
+  p.d = static_cast<int32_t>(h->d);
+  p.B = static_cast<int32_t>(B);
+  p.N = kPairN;
+  p.n_vt = h->n_vt;
+  p.n_nt = static_cast<int32_t>((B + kPairN - 1) / kPairN);
+  p.nk = static_cast<int32_t>((h->d * 2 + kRowBytes - 1) / kRowBytes);
+  p.n_chunks = static_cast<int32_t>((h->d + kChunkK - 1) / kChunkK);
+  p.n_slots = 2;
+  p.stages = pair_stages();
+  p.n_issuers = 1;
+  p.tmem_cols = 512;
+  p.idesc = idesc_f16(0u, 2 * kBM, kPairN);
   p.logits = reinterpret_cast<float*>(logits);
   p.rec_m = w.m;
   p.rec_i = w.i;
   p.rec_s = w.s;
+  p.err = h->d_err;
+  p.stall = h->stall;
+  p.timeout_ns = h->timeout_ns;
+  p.v_off = static_cast<int32_t>(h->v_off);
   const size_t smem = pair_layout(p.stages).total + 1024;
   const int64_t units = static_cast<int64_t>((p.n_vt + 1) / 2) * p.n_nt;
   CUtensorMap tmL = tmH;   // not read unless the logits map is valid
-  p.tma_logits = encode_logits(&tmL, logits, h->V, B, CU_TENSOR_MAP_DATA_TYPE_INT32) ? 1 : 0;
+  p.tma_logits = encode_logits(&tmL, logits, h->V, B, true) ? 1 : 0;
   if (h->t_start) cudaEventRecord(h->t_start, stream);
   e = launch_pair_kernel<MODE_INT>(h, h->tmW16, tmH, tmL, p, units, smem, stream);
   if (h->t_stop) {

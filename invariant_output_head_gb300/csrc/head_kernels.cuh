@@ -90,10 +90,8 @@ constexpr int kSmemLimit = 232448;  // 227 KB dynamic shared memory per CTA
 // MODE_SCORE: the score call's projection of up to 128 rows: logits into the
 // handle's workspace and, per 128-row tile, the softmax statistics of
 // score_stats.cuh (rec_m, rec_s and, in rec_i's storage, U).
-// MODE_SCALED: MODE_INT whose int32 sums are written times a scale of the
-// hidden row and one of the vocabulary row, and nothing else.
 enum : int { MODE_GREEDY = 0, MODE_LOGPROB = 1, MODE_INT = 2, MODE_GATED = 3, MODE_SAMPLE = 4,
-             MODE_SCORE = 5, MODE_SCALED = 6 };
+             MODE_SCORE = 5 };
 enum : int { ERR_TIMEOUT = 1, ERR_TARGET = 2 };
 
 // Kept at 128 bytes or less: with the parameter struct above 128 bytes the
@@ -121,18 +119,15 @@ struct HeadParams {
     const int32_t* targets;   // logprob: [B]
     int32_t* rec_b;           // gated: [B, n_vt] lowest index of the rounded maximum
     const uint64_t* seeds;    // sample: [B] generator key of each row
-    const float* x_scale;     // scaled: [B] scale of each hidden row
   };
   union {
     float* zt;                // logprob: [B] target logit
     const uint64_t* positions;  // sample: [B] position t of each row
-    const float* w_scale;       // scaled: [V] scale of each vocabulary row
   };
   union {
     int32_t round_fp16;       // gated: 1 rounds logits to fp16, 0 to bf16
     float temperature;        // sample: T > 0; score: log2(e) / T
-    int32_t tma_logits;       // pair kernel: bit 0 = logits leave through the logits tensor
-                              // map; scaled: bits 1, 2 = the output's type
+    int32_t tma_logits;       // pair kernel: 1 = logits leave through the logits tensor map
   };
   int32_t v_off;            // vocabulary index of this head's first W row
 };

@@ -45,21 +45,6 @@ constexpr int kPairMaxStages = 7;
 constexpr int kPairN = 256;         // hidden rows per unit (the pair's MMA M); also its N
 constexpr int kPairWarps = 8;       // epilogue warps 4 .. 11, 128 columns each
 
-// Two fp32 values rounded to bf16 or fp16, the first in the low half.
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
-  if (fp16) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
-  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
-
 // Logits staging: per epilogue warp two buffers of 32 hidden rows x 16
 // logits (64-byte rows, 64-byte swizzle: 16-byte chunk c of row r sits at
 // chunk c ^ ((r >> 1) & 3), so a warp's row-per-lane writes and the 8-row
@@ -89,87 +74,6 @@ __host__ __device__ inline PairLayout pair_layout(int stages) {
   return L;
 }
 
-// The scaled-logits call's epilogue of one 128-entry tile: this thread's row
-// n, columns vt0 .. (lim of them exist). acc * (x_scale * w_scale), each
-// product rounded once to fp32, then the output's own rounding. A staging
-// buffer holds 32 rows of 64 bytes (16 fp32 or 32 16-bit entries); it leaves
-// by the tensor map's store, or, where the rows do not start on 16-byte
-// boundaries, row by row with one entry a lane.
-__device__ __forceinline__ void scaled_tail(const HeadParams& p, const void* tmL,
-                                            const int32_t (&acc)[8][16], uint8_t* xs,
-                                            uint32_t xs_u32, uint32_t& nbuf, int lane, int n,
-                                            int nw0, int vt0, int lim) {
-  const int type = p.tma_logits >> 1;
-  const bool tma = (p.tma_logits & 1) != 0;
-  const float sx = n < p.B ? p.x_scale[n] : 0.0f;
-  auto flush = [&](const uint4 (&w)[4], int c0, int cols) {
-    const uint32_t buf = nbuf & 1u;
-    uint8_t* sb = xs + buf * kPairStageBuf;
-    if (tma && nbuf >= 2) {
-      if (lane == 0) bulk_wait_group_read<1>();   // this buffer's previous store has read it
-      __syncwarp();
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4*>(sb + lane * 64 + 16 * (k ^ ((lane >> 1) & 3))) = w[k];
-    ++nbuf;
-    if (tma) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(tmL, xs_u32 + buf * kPairStageBuf, c0, nw0);
-        bulk_commit_group();
-      }
-      return;
-    }
-    __syncwarp();
-    const int size = 64 / cols;                   // bytes of an entry
-    const int rows = min(32, p.B - nw0);
-    const int v = c0 + (lane & (cols - 1));
-    const int r0 = cols == 16 ? lane >> 4 : 0;
-    for (int r = r0; r < rows; r += 32 / cols) {
-      const int at = (lane & (cols - 1)) * size;  // byte of the row
-      const uint8_t* src = sb + r * 64 + 16 * ((at >> 4) ^ ((r >> 1) & 3)) + (at & 15);
-      const size_t o = static_cast<size_t>(nw0 + r) * p.V + v;
-      if (v >= p.V) continue;
-      if (size == 4) p.logits[o] = *reinterpret_cast<const float*>(src);
-      else reinterpret_cast<uint16_t*>(p.logits)[o] = *reinterpret_cast<const uint16_t*>(src);
-    }
-    __syncwarp();
-  };
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    if (b * 32 >= lim) continue;
-    float y[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float sw = b * 32 + i < lim ? __ldg(p.w_scale + vt0 + b * 32 + i) : 0.0f;
-      y[i] = __fmul_rn(__int2float_rn(acc[2 * b + (i >> 4)][i & 15]), __fmul_rn(sx, sw));
-    }
-    uint4 w[4];
-    if (type == 0) {
-#pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        if (b * 32 + hb * 16 >= lim) continue;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = make_uint4(__float_as_uint(y[hb * 16 + 4 * k]), __float_as_uint(y[hb * 16 + 4 * k + 1]),
-                            __float_as_uint(y[hb * 16 + 4 * k + 2]),
-                            __float_as_uint(y[hb * 16 + 4 * k + 3]));
-        flush(w, vt0 + b * 32 + hb * 16, 16);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = make_uint4(pack16(y[8 * k], y[8 * k + 1], type == 2),
-                          pack16(y[8 * k + 2], y[8 * k + 3], type == 2),
-                          pack16(y[8 * k + 4], y[8 * k + 5], type == 2),
-                          pack16(y[8 * k + 6], y[8 * k + 7], type == 2));
-      flush(w, vt0 + b * 32, 32);
-    }
-  }
-}
-
 // p.n_vt: 128-row vocabulary tiles (the records' tiles); a unit covers tiles
 // 2 vp and 2 vp + 1 (the second may lie past V: its rows read as zeros and
 // no record of it is written). p.n_nt: 256-row hidden tiles.
@@ -177,8 +81,7 @@ template <int MODE>
 __global__ void __launch_bounds__(kPairThreads, 1)
 head_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
                  const __grid_constant__ CUtensorMap tmL, const HeadParams p) {
-  static_assert(MODE == MODE_GREEDY || MODE == MODE_INT || MODE == MODE_SCALED, "mode");
-  constexpr bool kInt = MODE != MODE_GREEDY;       // int8 values held as fp16, int32 sums
+  static_assert(MODE == MODE_GREEDY || MODE == MODE_INT, "mode");
   constexpr int N = kPairN;
   constexpr int WBLK = 8;                          // 16-column blocks per epilogue warp
   constexpr int ET = 32 * kPairWarps;
@@ -225,7 +128,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmH);
-    if (p.tma_logits & 1) tma_prefetch_desc(&tmL);
+    if (p.tma_logits) tma_prefetch_desc(&tmL);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_holder), 512u);
@@ -359,13 +262,13 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
     uint8_t* xs = xsall + (warp - 4) * kPairXsBytes;
     const uint32_t xs_u32 = smem_u32(xs);
-    const bool tma_lg = (p.tma_logits & 1) != 0;
+    const bool tma_lg = p.tma_logits != 0;
     // without the tensor map (rows not 16-byte aligned): plain stores
     const bool vec = (p.V & 3) == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0;
     uint32_t nbuf = 0;                         // staging buffers used so far
     uint32_t slot = 0, sph = 0;
     bool failed = false;
-    using Acc = typename std::conditional<kInt, int32_t, float>::type;
+    using Acc = typename std::conditional<MODE == MODE_INT, int32_t, float>::type;
     for (int u = pair; u < n_units; u += n_pairs) {
       const int vp = u / p.n_nt, nt = u - (u / p.n_nt) * p.n_nt;
       Acc acc[WBLK][16];
@@ -392,7 +295,7 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           for (int b4 = 0; b4 < 4; ++b4) {
             const int bb = h4 * 4 + b4;
             const uint32_t* rr = &rw[b4 >> 1][(b4 & 1) * 16];   // this block's 16 columns
-            if constexpr (kInt) {
+            if constexpr (MODE == MODE_INT) {
               // exact integer chunk sums (|sum| <= 128 * 2^14 = 2^21): adding
               // 1.5 * 2^23 is exact and leaves the integer in the low
               // mantissa bits; int32 fold
@@ -432,11 +335,6 @@ head_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int lim = p.V - vt0;                       // its rows below V (<= 0: none)
       const int nw0 = nt * N + static_cast<int>(rank) * kRowsHalf + q * 32;   // warp's row 0
       const int n = nw0 + lane;                        // this thread's hidden row
-      if constexpr (MODE == MODE_SCALED) {
-        if (lim > 0 && nw0 < p.B)
-          scaled_tail(p, &tmL, acc, xs, xs_u32, nbuf, lane, n, nw0, vt0, lim);
-        continue;
-      }
       if (p.logits != nullptr && lim > 0) {
         // per 16-column block the warp's 32 rows x 16 logits go to a staging
         // buffer (row = lane); the tensor map's store (clipped at B and V)

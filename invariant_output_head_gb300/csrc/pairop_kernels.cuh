@@ -1,7 +1,7 @@
 // pairop_kernels.cuh -- the matrix products of the score call and of its
 // gradient, on CTA pairs.
 //
-// One kernel body, five products. A unit is a 256 x 256 tile of
+// One kernel body, eight products. A unit is a 256 x 256 tile of
 // D = A * B^T, computed by a cluster of two CTAs with tcgen05.mma.cta_group::2
 // (each CTA holds 128 rows of A and 128 of B per stage and finds its own 128
 // rows of D in its tensor memory), with the pair protocol of
@@ -13,7 +13,10 @@
 //   OP_SCORE   D[n, v] = h W^T: softmax statistics of each row and 256-entry
 //              tile, the target's logit, and the candidates for the row's
 //              largest logits; logits are never written.
-//   OP_SELECT  the same product again, for the 256-row tiles that hold a row
+//   OP_SCOREZ  the same with the logits written to a workspace instead of
+//              candidates (few rows, where the candidates' thresholds come too
+//              late to thin them out).
+//   OP_SELECT  OP_SCORE again, for the 256-row tiles that hold a row
 //              whose candidates overflowed: only its candidates, with the
 //              exact threshold found meanwhile.
 //   OP_DZ      D[n, v] = h W^T again, turned into the gradient with respect
@@ -23,6 +26,9 @@
 //              axis contiguous, B = W with the free axis contiguous.
 //   OP_DW      D[v, k] = sum_n dz[n, v] h[n, k]: both operands with the free
 //              axis contiguous.
+//   OP_SCALED  D[n, v] = q W^T of int8 values held as fp16, written times a
+//              scale of the row and one of the column; OP_SCALED1 where d is
+//              at most one chunk (no integer conversions).
 //
 // The target's entry (g_l (1 - p) - ...) / T of the gradient never passes
 // through 16 bits: it is by far the largest of its row, and its rounding would
@@ -30,13 +36,14 @@
 // value contributes a row of W to dh and a row of h to dW, added in fp32
 // (grad_fold_kernel, and this kernel's OP_DW epilogue).
 //
-// The first two use the logits' own arithmetic (128-element K chunks, each
-// accumulated from zero and added in fp32 in ascending order), so they see
-// the bits that every other call of the head computes. The gradient's three
-// products run in chunks of 2048: 128 MMA steps of the tensor core's
-// accumulation before a round-to-nearest fp32 add, which leaves at most about
-// 128 half-ulps of fp32 (8e-6) per chunk, far below the 16-bit rounding of dz
-// and of what comes out; one sixteenth of the drains.
+// K chunks, each accumulated from zero in a tensor-memory slot and added in
+// fp32 (round to nearest, ascending order) by the epilogue: 512 elements for
+// the scores (kScoreChunkK); 2048 for the gradient's three products -- 128 MMA
+// steps of the tensor core's accumulation, at most about 128 half-ulps of
+// fp32 (8e-6) per chunk, far below the 16-bit rounding of dz and of what comes
+// out; 1024 for OP_SCALED, whose chunk sums are integers of magnitude at most
+// 1024 * 2^14 = 2^24, exact in fp32, added in int32. Longer chunks mean fewer
+// drains of tensor memory, which at 128 elements take longer than the MMAs.
 //
 // Operands with the free axis contiguous ("MN-major") are loaded as boxes of
 // 64 free x 64 contracted elements, 128-byte swizzle: 64 rows of 128 bytes,
@@ -50,18 +57,36 @@
 // unit's first chunks.
 #pragma once
 #include "head_kernels.cuh"
-#include "pair_kernels.cuh"
+#include "int8_kernels.cuh"
 #include "rows_kernels.cuh"
 
 namespace detlm {
 
-enum : int { OP_SCORE = 0, OP_SELECT = 1, OP_DZ = 2, OP_DH = 3, OP_DW = 4 };
+enum : int { OP_SCORE = 0, OP_SCOREZ = 1, OP_SELECT = 2, OP_DZ = 3, OP_DH = 4, OP_DW = 5,
+             OP_SCALED = 6, OP_SCALED1 = 7 };
+__host__ __device__ constexpr bool op_scaled(int op) { return op == OP_SCALED || op == OP_SCALED1; }
 
 constexpr int kGradChunkBoxes = 32;      // 64-element K boxes per gradient chunk (2048)
+constexpr int kScaledChunkBoxes = 16;    // OP_SCALED: 1024
 constexpr int kSegChunks = 8;            // gradient chunks per vocabulary segment (16384)
 constexpr int kCandFloats = 20;          // a candidate block: 16 logits, its index, padding
+constexpr int kShortRun = 2;             // OP_DW: hidden rows of one target added one by one
 constexpr int kRowWords = 4;             // words of a row before its slots
 enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
+
+// Two fp32 values rounded to bf16 or fp16, the first in the low half; and back.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  if (fp16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
 
 __host__ __device__ constexpr int row_words(int K) { return kRowWords + ((K + 3) & ~3); }
 
@@ -85,7 +110,7 @@ struct ScoreArgs {
   const int32_t* targets;   // optional [B]
   int32_t* words;           // [B][row_words(K)]: candidate count, ..., K slot maxima
   float* cand;              // [B][C][kCandFloats]
-  const int32_t* tile_over; // OP_SELECT: [n_rt] tiles to compute
+  const int32_t* tile_over; // OP_SELECT: whether any tile is marked, then [n_rt] marks
 };
 struct GradArgs {
   const float* lse;         // [B]
@@ -97,11 +122,18 @@ struct GradArgs {
 };
 
 struct DwArgs {
-  const int32_t* tiles;     // [n_vt][2]: where a tile's targets start in the list, how many
-  const int2* list;         // (row of h, entry within the tile), by tile, then by row
+  const int32_t* starts;    // [256 n_vt + 1] where a vocabulary entry's run in the list starts
+  const int32_t* list;      // rows of h by their target (those of this pass), then ascending
+  const float* sums;        // [list position][d] sums of the runs longer than kShortRun
   const void* h;            // [B][d]
-  const void* unused[2];
+  const void* unused;
   const float* scale;       // as above
+};
+struct ScaledArgs {
+  const float* x_scale;     // [B]
+  const float* w_scale;     // [V]
+  void* out;                // [B][V], for rows that the tensor map cannot store
+  int32_t type, tma;        // OUT_*; 1: D leaves through the tensor map
 };
 
 // 128 bytes or less (see HeadParams).
@@ -111,7 +143,7 @@ struct PairOpParams {
   int32_t nk;               // K boxes of 64
   int32_t seg;              // K boxes per unit (OP_DH; else nk)
   int32_t units;
-  uint16_t stages, stall;
+  uint8_t stages, stall, a_rows, pad; // a_rows: rows of A's box (K-major A; 128 or fewer)
   uint32_t idesc;
   int32_t K, C;             // score: alternatives wanted, candidate blocks a row can hold;
                             // OP_DH, OP_DW: K is the number of columns of D (d);
@@ -128,6 +160,7 @@ struct PairOpParams {
     ScoreArgs s;
     GradArgs g;
     DwArgs w;
+    ScaledArgs q;
   };
 };
 static_assert(sizeof(PairOpParams) <= 128, "kernel parameter struct above 128 bytes");
@@ -165,52 +198,70 @@ __device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, int u) {
 // Staging of D: per epilogue warp two buffers of 32 rows x 128 bytes (whole
 // cache lines leave; 128-byte swizzle: 16-byte chunk c of row r sits at chunk
 // c ^ (r & 7)), each stored by the tensor map's box while the warp goes on.
+// (Four buffers and fewer stages measured the same on the shortest K loops.)
 constexpr uint32_t kOpStageBuf = 32 * 128;
 constexpr uint32_t kOpXsBytes = 2 * kOpStageBuf;
 constexpr int kOpMaxStages = 7;
 
+__host__ __device__ constexpr bool op_stores(int op) { return op != OP_SCORE && op != OP_SELECT; }
+// Words kept beside the stages: the half-row records [3][128] of the score
+// products, each epilogue warp's column scales [8][128] of OP_SCALED.
+__host__ __device__ constexpr uint32_t op_words(int op) {
+  return op == OP_SCORE || op == OP_SCOREZ ? 384u : op_scaled(op) ? 1024u : 0u;
+}
+
 struct OpLayout {
-  uint32_t a_bytes, stage_bytes, ctrl_off, red_off, xs_off, store_total, score_total;
+  uint32_t a_bytes, stage_bytes, ctrl_off, red_off, xs_off, total;
 };
 // Stage s: this CTA's 128 rows of A, then its 128 of B (128 bytes of K each,
 // or two MN-major boxes of 8 KB each); then the barriers (full[S], empty[S],
 // slot_full[2], slot_empty[2], never, drain), the TMEM address holder and the
-// abort flag; then the staging buffers, or the score products' half-row
-// records [3][128].
-__host__ __device__ inline OpLayout op_layout(int stages) {
+// abort flag; the op's words; the staging buffers.
+__host__ __device__ inline OpLayout op_layout(int op, int stages) {
   OpLayout L;
   L.a_bytes = kRowsHalf * kRowBytes;
   L.stage_bytes = 2 * L.a_bytes;
   L.ctrl_off = static_cast<uint32_t>(stages) * L.stage_bytes;
   L.red_off = L.ctrl_off + (2u * stages + 6u) * 8u + 16u;
-  L.score_total = L.red_off + 3u * 128u * 4u;
-  L.xs_off = (L.red_off + 1023u) & ~1023u;
-  L.store_total = L.xs_off + 8u * kOpXsBytes;
+  L.xs_off = L.red_off + 4u * op_words(op);
+  if (op_stores(op)) L.xs_off = (L.xs_off + 1023u) & ~1023u;
+  L.total = L.xs_off + (op_stores(op) ? 8u * kOpXsBytes : 0u);
   return L;
 }
 
-// 32 rows x 128 bytes of a warp (lane = row) to the tensor map's box at
-// (c0, row0); asynchronous.
-__device__ __forceinline__ void stage_store(const void* tmap, uint8_t* xs, uint32_t xs_u32,
-                                            uint32_t& nbuf, const uint4 (&w)[8], int lane, int c0,
-                                            int row0) {
-  const uint32_t buf = nbuf & 1u;
-  if (nbuf >= 2) {
-    if (lane == 0) bulk_wait_group_read<1>();   // this buffer's previous store has read it
-    __syncwarp();
+// A warp's staging buffers, in turn.
+struct Staging {
+  uint8_t* xs;
+  uint32_t xs_u32, used;
+  // the next buffer, once its previous store has read it
+  __device__ __forceinline__ uint32_t next(int lane) {
+    const uint32_t buf = used & 1u;
+    if (used >= 2) {
+      if (lane == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+    }
+    ++used;
+    return buf * kOpStageBuf;
   }
-  uint8_t* sb = xs + buf * kOpStageBuf;
+  // 32 rows x 128 bytes (lane = row) into the buffer at `off`
+  __device__ __forceinline__ void put(uint32_t off, const uint4 (&w)[8], int lane) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *reinterpret_cast<uint4*>(sb + lane * 128 + 16 * (k ^ (lane & 7))) = w[k];
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(tmap, xs_u32 + buf * kOpStageBuf, c0, row0);
-    bulk_commit_group();
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint4*>(xs + off + lane * 128 + 16 * (k ^ (lane & 7))) = w[k];
   }
-  ++nbuf;
-}
+  // and out to the tensor map's box at (c0, row0); asynchronous
+  __device__ __forceinline__ void store(const void* tmap, const uint4 (&w)[8], int lane, int c0,
+                                        int row0) {
+    const uint32_t off = next(lane);
+    put(off, w, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tmap, xs_u32 + off, c0, row0);
+      bulk_commit_group();
+    }
+  }
+};
 
 // The score call's epilogue of one half-unit: this thread's row n, 128
 // entries from vb (nv of them exist).
@@ -224,7 +275,7 @@ __device__ __forceinline__ void stage_store(const void* tmap, uint8_t* xs, uint3
 // timing, the set of entries above the final threshold does not). About
 // K H_K entries stay above the final threshold (H_K the harmonic number), so
 // of V / 16 blocks some K H_K log(n_vt) are appended.
-template <bool RAGGED>
+template <bool RAGGED, bool CAND>
 __device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&acc)[8][16], int n,
                                            int vb, int nv, float thr, bool records) {
   float bm[8];
@@ -237,8 +288,9 @@ __device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&
   }
   uint32_t mask = 0;
   int base = 0;
-  int32_t* w = p.s.words + static_cast<size_t>(n) * row_words(p.K);
-  if (p.K > 0) {
+  int32_t* w = nullptr;
+  if constexpr (CAND) w = p.s.words + static_cast<size_t>(n) * row_words(p.K);
+  if (CAND && p.K > 0) {
 #pragma unroll
     for (int b = 0; b < 8; ++b)
       if (bm[b] >= thr && (!RAGGED || b * 16 < nv)) mask |= 1u << b;
@@ -270,7 +322,7 @@ __device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&
     }
     st = stat_merge(stat_merge(g[0], g[1], p.c), stat_merge(g[2], g[3], p.c), p.c);
   }
-  if (mask != 0) {
+  if (CAND && mask != 0) {
     float* cd = p.s.cand + static_cast<size_t>(n) * p.C * kCandFloats;
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
@@ -291,40 +343,187 @@ __device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&
   return st;
 }
 
-// OP_DW: the targets' entries of this warp's 32 vocabulary rows (from row0 of
-// the tile on): each hidden row whose target is one of them adds its entry
-// times itself, in ascending order of the rows. A tile's list is short (B / n_vt
-// entries on average); the lane that owns the row adds 128 columns.
-__device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[8][16], int tile,
-                                            int row0, int col0, int lane, bool f16) {
-  const int2 range = *reinterpret_cast<const int2*>(p.w.tiles + 2 * tile);
-  for (int i0 = 0; i0 < range.y; i0 += 32) {
-    const int2 e = i0 + lane < range.y ? p.w.list[range.x + i0 + lane] : make_int2(0, -1);
-    uint32_t hits = __ballot_sync(0xffffffffu, e.y >= row0 && e.y < row0 + 32);
-    while (hits != 0) {
-      const int src = __ffs(hits) - 1;
-      hits &= hits - 1;
-      const int n = __shfl_sync(0xffffffffu, e.x, src);
-      const int row = __shfl_sync(0xffffffffu, e.y, src) - row0;
-      if (lane != row) continue;
-      const float g = p.coef[n];
-      const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
-                                                      static_cast<size_t>(n) * p.K + col0);
+// OP_DW: the hidden rows whose target is this thread's vocabulary row; fetched
+// one unit ahead of their use (three dependent loads would otherwise stand at
+// the end of every unit that has one).
+struct TargetRun {
+  int first, count, n;      // run in the list; its first row
+  float g;                  // and that row's entry
+  __device__ __forceinline__ void fetch(const PairOpParams& p, int v) {
+    first = p.w.starts[v];
+    count = p.w.starts[v + 1] - first;
+    n = 0;
+    g = 0.0f;
+    if (count > 0) {
+      n = p.w.list[first];
+      g = p.coef[n];
+    }
+  }
+};
+
+// OP_DW: the targets' entries of this thread's vocabulary row: each hidden row
+// whose target it is adds its entry times itself, in ascending order of the
+// rows -- one by one, or as the sum that target_sum_kernel has made of a long
+// run (a frequent token), so that no thread walks one.
+__device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[8][16],
+                                            const TargetRun& run, int col0, bool f16) {
+  if (run.count > kShortRun) {
+    const float4* x =
+        reinterpret_cast<const float4*>(p.w.sums + static_cast<size_t>(run.first) * p.K + col0);
 #pragma unroll
-      for (int b = 0; b < 16; ++b) {
-        if (col0 + 8 * b >= p.K) break;      // d is a multiple of 8
-        const uint4 w = __ldg(h + b);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int b = 0; b < 32; ++b) {
+      if (col0 + 4 * b >= p.K) break;        // d is a multiple of 8
+      const float4 v = x[b];
+      float* a = &acc[b >> 2][4 * (b & 3)];
+      a[0] += v.x;
+      a[1] += v.y;
+      a[2] += v.z;
+      a[3] += v.w;
+    }
+    return;
+  }
+  for (int i = 0; i < run.count; ++i) {
+    const int n = i == 0 ? run.n : p.w.list[run.first + i];
+    const float g = i == 0 ? run.g : p.coef[n];
+    const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
+                                                    static_cast<size_t>(n) * p.K + col0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = unpack16(x[k], f16);
-          float* a = &acc[b >> 1][(b & 1) * 8 + 2 * k];
-          a[0] = fmaf(g, v.x, a[0]);
-          a[1] = fmaf(g, v.y, a[1]);
-        }
+    for (int b = 0; b < 16; ++b) {
+      if (col0 + 8 * b >= p.K) break;
+      const uint4 w = __ldg(h + b);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack16(x[k], f16);
+        float* a = &acc[b >> 1][(b & 1) * 8 + 2 * k];
+        a[0] = fmaf(g, v.x, a[0]);
+        a[1] = fmaf(g, v.y, a[1]);
       }
     }
-    __syncwarp();
+  }
+}
+
+// OP_SCALED: this thread's row n, columns vb .. (lim of them exist): the exact
+// int32 sum rounded once to fp32, one rounded product of the two scales, one
+// rounded product, and the output's own rounding. Rows that do not start on
+// 16-byte boundaries are written from the staging buffer one row at a time, a
+// 4-byte word a lane: 16-bit rows of odd origin pair elements (2 l - 1, 2 l).
+// acc: the int32 sums, or (OP_SCALED1) the fp32 integers that the tensor core
+// left; sw: the warp's 128 column scales in shared memory.
+template <typename Acc>
+__device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* tmO,
+                                            const Acc (&acc)[8][16], const float* sw, Staging& sg,
+                                            int lane, int n, int nw0, int vb, int lim) {
+  const int type = p.q.type;
+  const float sx = n < p.B ? p.q.x_scale[n] : 0.0f;
+  const int rows = min(32, p.B - nw0);
+  // fp32 rows that the tensor map cannot store: 32 columns of a row at a time
+  auto rows32 = [&](uint32_t off, int c0) {
+    const uint8_t* sb = sg.xs + off;
+    float* out = static_cast<float*>(p.q.out) + static_cast<size_t>(nw0) * p.V + c0 + lane;
+    if (c0 + lane < p.V) {
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r)
+        out[static_cast<size_t>(r) * p.V] = *reinterpret_cast<const float*>(
+            sb + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3));
+    }
+  };
+  // 16-bit rows that it cannot store: 16 lanes a row, each a 16-byte word of
+  // the row's aligned middle, put together from two chunks of the staged row;
+  // the ends (at most 7 elements each) one element a lane
+  auto rows16 = [&]() {
+    const int half = lane >> 4, l = lane & 15;
+    const int cols = min(128, lim);
+    auto chunk = [&](int r, int c) {           // elements 8 c .. 8 c + 7 of row r
+      return *reinterpret_cast<const uint4*>(sg.xs + (c >> 3) * kOpStageBuf + r * 128 +
+                                             16 * ((c & 7) ^ (r & 7)));
+    };
+#pragma unroll 2
+    for (int r0 = 0; r0 < rows; r0 += 2) {
+      const int r = r0 + half;
+      if (r >= rows) break;                    // (no exchange between lanes below)
+      uint16_t* o = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(nw0 + r) * p.V + vb;
+      // elements before the first 16-byte boundary, whole words behind it
+      const int head = min(cols, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(o) & 15)) & 15) >> 1);
+      const int words = (cols - head) >> 3;
+      const uint4 a = chunk(r, l), b = chunk(r, min(l + 1, 15));
+      const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      if (l < words) {
+        const int s2 = head >> 1;              // whole 4-byte steps of the shift
+        uint32_t y[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+          y[k] = x[k];
+#pragma unroll
+          for (int j = 1; j < 4; ++j)
+            if (k + j < 8) y[k] = s2 == j ? x[k + j] : y[k];
+        }
+        uint4 v = make_uint4(y[0], y[1], y[2], y[3]);
+        if (head & 1)
+          v = make_uint4(__funnelshift_r(y[0], y[1], 16), __funnelshift_r(y[1], y[2], 16),
+                         __funnelshift_r(y[2], y[3], 16), __funnelshift_r(y[3], y[4], 16));
+        *reinterpret_cast<uint4*>(o + head + 8 * l) = v;
+      }
+      // lanes 0..7: the head, 8..15: what the words leave over
+      const int e = l < 8 ? l : head + 8 * words + l - 8;
+      if (l < 8 ? e < head : e < cols)
+        o[e] = *reinterpret_cast<const uint16_t*>(sg.xs + (e >> 6) * kOpStageBuf + r * 128 +
+                                                  16 * (((e >> 3) & 7) ^ (r & 7)) + 2 * (e & 7));
+    }
+  };
+  // columns j .. j + 3
+  auto values = [&](int j, float (&y)[4]) {
+    const float4 w = *reinterpret_cast<const float4*>(sw + j);
+    const float s[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = __fmul_rn(static_cast<float>(acc[(j + i) >> 4][(j + i) & 15]), __fmul_rn(sx, s[i]));
+    }
+  };
+  uint4 w[8];
+  float x[4], y[4];
+  if (type == OUT_F32) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (32 * b >= lim) break;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        values(32 * b + 4 * k, x);
+        w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+      }
+      if (p.q.tma) {
+        sg.store(tmO, w, lane, vb + 32 * b, nw0);
+      } else {
+        __syncwarp();                          // the previous box's reads are done
+        sg.put(0, w, lane);
+        __syncwarp();
+        rows32(0, vb + 32 * b);
+      }
+    }
+  } else {
+    const bool f16 = type == OUT_FP16;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (64 * b >= lim) break;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        values(64 * b + 8 * k, x);
+        values(64 * b + 8 * k + 4, y);
+        w[k] = make_uint4(pack16(x[0], x[1], f16), pack16(x[2], x[3], f16), pack16(y[0], y[1], f16),
+                          pack16(y[2], y[3], f16));
+      }
+      if (p.q.tma) {
+        sg.store(tmO, w, lane, vb + 64 * b, nw0);
+      } else {
+        if (b == 0) __syncwarp();              // the previous tail's reads are done
+        sg.put(b * kOpStageBuf, w, lane);
+      }
+    }
+    if (!p.q.tma) {
+      __syncwarp();
+      rows16();
+    }
   }
 }
 
@@ -332,18 +531,19 @@ template <int OP>
 __global__ void __launch_bounds__(kRowsThreads, 1)
 pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const PairOpParams p) {
-  constexpr bool kScore = OP == OP_SCORE || OP == OP_SELECT;
-  constexpr bool kLogits = kScore || OP == OP_DZ;      // D = h W^T
-  constexpr bool kStore = !kScore;                     // D leaves through staging and tmO
+  constexpr bool kScore = OP == OP_SCORE || OP == OP_SCOREZ || OP == OP_SELECT;
+  constexpr bool kLogits = kScore || OP == OP_DZ || op_scaled(OP);     // D = h W^T
+  constexpr bool kStore = op_stores(OP);               // D leaves through staging and tmO
+  constexpr bool kInt = OP == OP_SCALED;               // integer sums, int32
   constexpr bool kMnA = OP == OP_DW, kMnB = OP == OP_DH || OP == OP_DW;
-  constexpr int kBoxes = kScore ? kScoreChunkK / 64 : kGradChunkBoxes;
+  constexpr int kBoxes = kScore ? kScoreChunkK / 64 : op_scaled(OP) ? kScaledChunkBoxes : kGradChunkBoxes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int S = p.stages;
-  const OpLayout L = op_layout(S);
+  const OpLayout L = op_layout(OP, S);
   const uint32_t rank = cluster_rank();            // 0: leader, 1: peer
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int n_pairs = static_cast<int>(gridDim.x >> 1);
@@ -358,9 +558,6 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 6) * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  // after the control words: staging buffers (1024-byte aligned), or the
-  // half-row records [3][128]
-  uint8_t* tail = smem + (kStore ? L.xs_off : L.red_off);
   const uint32_t smem_base = smem_u32(smem);
   auto sA = [&](int s) { return smem_base + static_cast<uint32_t>(s) * L.stage_bytes; };
   auto sB = [&](int s) { return sA(s) + L.a_bytes; };
@@ -398,9 +595,14 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   // OP_SELECT computes the units of the marked hidden-row tiles alone (the
   // marks are the previous kernel's, read after the wait by every role)
   auto skip = [&](int u) {
-    if constexpr (OP == OP_SELECT) return p.s.tile_over[u % p.n1] == 0;
+    if constexpr (OP == OP_SELECT) return p.s.tile_over[1 + u % p.n1] == 0;
     return false;
   };
+  int units = p.units;
+  if constexpr (OP == OP_SELECT) {
+    grid_dep_wait();
+    if (p.s.tile_over[0] == 0) units = 0;   // the usual case: no row overflowed
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -414,9 +616,15 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             tma_load_2d_pair(sA(s) + i * 8192, &tmA, t.a0 + half + i * 64, kb * 64, fb, pol_n);
-        } else {
+        } else if (t.a0 + half < p.B) {
           tma_load_2d_pair(sA(s), &tmA, kb * 64, t.a0 + half, fb, kLogits ? pol_l : pol_n);
         }
+      };
+      // bytes of a stage over both CTAs: boxes of rows that do not exist are
+      // not loaded (their rows of D are not read)
+      auto bytes = [&](const PairUnit& t) {
+        if constexpr (kMnA) return 2u * L.stage_bytes;
+        return 2u * L.a_bytes + (t.a0 + kRowsHalf < p.B ? 2u : 1u) * p.a_rows * 128u;
       };
       auto load_b = [&](int s, const PairUnit& t, int kb, uint32_t fb) {
         if constexpr (kMnB) {
@@ -432,13 +640,13 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       grid_dep_wait();
       uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
       bool ok = true;
-      for (int u = pair; u < p.units && ok; u += n_pairs) {
+      for (int u = pair; u < units && ok; u += n_pairs) {
         if (skip(u)) continue;
         const PairUnit t = unit_of<OP>(p, u);
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb) {
           const uint32_t fb = cluster_addr(full_bar(stage), 0);
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), 2u * L.stage_bytes);
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes(t));
           load_b(stage, t, kb, fb);
           load_a(stage, t, kb, fb);
           outstanding |= 1u << stage;
@@ -467,11 +675,10 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     // ------------------------------------------------------- MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
     if (lane == 0 && rank == 0) {
-      if constexpr (OP == OP_SELECT) grid_dep_wait();
       uint32_t stage = 0, phase = 0, slot = 0, sph = 0;
       bool ok = true;
       if (p.stall) ok = mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
-      for (int u = pair; u < p.units && ok; u += n_pairs) {
+      for (int u = pair; u < units && ok; u += n_pairs) {
         if (skip(u)) continue;
         const int nkb = unit_of<OP>(p, u).nkb;
         for (int c0 = 0; c0 < nkb && ok; c0 += kBoxes) {
@@ -518,21 +725,46 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int g = (warp - 4) >> 2;             // column half of the unit
     const int r = q * 32 + lane;               // row within this CTA's half
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    uint8_t* xs = tail + (warp - 4) * kOpXsBytes;
-    const uint32_t xs_u32 = smem_u32(xs);
-    float* red = reinterpret_cast<float*>(tail);              // [3][128]
-    uint32_t nbuf = 0;                         // staging buffers used so far
+    Staging sg;
+    sg.used = 0;
+    sg.xs = smem + L.xs_off + (warp - 4) * kOpXsBytes;
+    sg.xs_u32 = smem_u32(sg.xs);
+    float* red = reinterpret_cast<float*>(smem + L.red_off);  // the op's words
+    using Acc = typename std::conditional<kInt, int32_t, float>::type;
     uint32_t slot = 0, sph = 0;
     bool failed = false;
-    for (int u = pair; u < p.units; u += n_pairs) {
+    TargetRun ahead{};
+    if constexpr (OP == OP_DW) {
+      if (pair < units) ahead.fetch(p, unit_of<OP>(p, pair).a0 + half + q * 32 + lane);
+    }
+    for (int u = pair; u < units; u += n_pairs) {
       if (skip(u)) continue;
       const PairUnit t = unit_of<OP>(p, u);
       const int nw0 = t.a0 + half + q * 32;    // the warp's first row of D
       const int n = nw0 + lane;                // this thread's row
       const int rows = OP == OP_DW ? p.V : p.B;
       const int vb = t.b0 + g * 128;           // first column of this half
-      float acc[8][16];
+      Acc acc[8][16];
       float thr = -INFINITY;
+      if constexpr (op_scaled(OP)) {
+        // the unit's column scales, for the warp's own tail
+        float* sw = red + (warp - 4) * 128;
+        __syncwarp();                          // the previous tail's reads are done
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = vb + 32 * k + lane;
+          sw[32 * k + lane] = v < p.V ? __ldg(p.q.w_scale + v) : 0.0f;
+        }
+        __syncwarp();
+      }
+      TargetRun run{};                         // OP_DW: this row's targets
+      if constexpr (OP == OP_DW) {
+        run = ahead;
+        if (u + n_pairs < units) {
+          const PairUnit t2 = unit_of<OP>(p, u + n_pairs);
+          ahead.fetch(p, t2.a0 + half + q * 32 + lane);
+        }
+      }
       const int n_chunks = (t.nkb + kBoxes - 1) / kBoxes;
       for (int c = 0; c < n_chunks; ++c) {
         const uint32_t cur = slot, cph = sph;
@@ -556,7 +788,13 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             for (int b4 = 0; b4 < 4; ++b4) {
               const int bb = h4 * 4 + b4;
               const uint32_t* rr = &rw[b4 >> 1][(b4 & 1) * 16];   // this block's 16 columns
-              if (c == 0) {
+              if constexpr (kInt) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const int32_t x = __float2int_rn(__uint_as_float(rr[i]));
+                  acc[bb][i] = c == 0 ? x : acc[bb][i] + x;
+                }
+              } else if (c == 0) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[bb][i] = __uint_as_float(rr[i]);
               } else {
@@ -592,8 +830,15 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           }
         }
       }
-      if (epi_bar_or<256>(failed || *abort_flag)) {
-        if (threadIdx.x == 128) { *abort_flag = 1; atomicOr(p.err, ERR_TIMEOUT); }
+      if constexpr (kScore) {
+        if (epi_bar_or<256>(failed || *abort_flag)) {
+          if (threadIdx.x == 128) { *abort_flag = 1; atomicOr(p.err, ERR_TIMEOUT); }
+          break;
+        }
+      } else if (__any_sync(0xffffffffu, failed || *abort_flag)) {
+        // (the other products' warps share nothing: no barrier)
+        *abort_flag = 1;
+        if (lane == 0) atomicOr(p.err, ERR_TIMEOUT);
         break;
       }
       if constexpr (kScore) {
@@ -603,11 +848,27 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const bool row_ok = n < p.B;
         const size_t o = static_cast<size_t>(n) * n_vt + vt;   // records [B][n_vt]
         Stat st{-INFINITY, 0.0f, 0.0f};
-        if constexpr (OP == OP_SCORE) {
+        if constexpr (OP == OP_SCORE || OP == OP_SCOREZ) {
+          if constexpr (OP == OP_SCOREZ) {
+            if (nw0 < p.B) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                uint4 w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float* x = &acc[2 * b + (k >> 2)][4 * (k & 3)];
+                  w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                    __float_as_uint(x[2]), __float_as_uint(x[3]));
+                }
+                if (vb + 32 * b < p.V) sg.store(&tmO, w, lane, vb + 32 * b, nw0);
+              }
+            }
+          }
           if (row_ok && nv > 0) {
             // the target's logit, if it lies in this half: a select chain
             // over the 16-entry blocks, then over the block
-            const int tl = p.s.targets != nullptr ? p.s.targets[n] - vb : -1;
+            // (OP_SCOREZ: the merge reads it from the logits)
+            const int tl = OP == OP_SCORE && p.s.targets != nullptr ? p.s.targets[n] - vb : -1;
             if (tl >= 0 && tl < 128) {
               const int tb = tl >> 4, ti = tl & 15;
               float sel[16];
@@ -622,8 +883,9 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
               for (int i = 1; i < 16; ++i) z = i == ti ? sel[i] : z;
               p.s.zt[n] = z;
             }
-            st = nv == 128 ? score_tail<false>(p, acc, n, vb, nv, thr, true)
-                           : score_tail<true>(p, acc, n, vb, nv, thr, true);
+            constexpr bool cand = OP == OP_SCORE;
+            st = nv == 128 ? score_tail<false, cand>(p, acc, n, vb, nv, thr, true)
+                           : score_tail<true, cand>(p, acc, n, vb, nv, thr, true);
           }
           // the two halves of a row: the second hands its record to the first
           if (g == 1) {
@@ -646,10 +908,14 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const float sm = __int_as_float(w[RW_SEL_M]);
             const float m = p.s.rec[o];
             if (w[RW_OVER] != 0 && (m > sm || (m == sm && vt <= w[RW_SEL_T]))) {
-              if (nv == 128) score_tail<false>(p, acc, n, vb, nv, sm, false);
-              else score_tail<true>(p, acc, n, vb, nv, sm, false);
+              if (nv == 128) score_tail<false, true>(p, acc, n, vb, nv, sm, false);
+              else score_tail<true, true>(p, acc, n, vb, nv, sm, false);
             }
           }
+        }
+      } else if constexpr (op_scaled(OP)) {
+        if (vb < p.V && nw0 < p.B) {
+          scaled_tail(p, &tmO, acc, red + (warp - 4) * 128, sg, lane, n, nw0, vb, min(128, p.V - vb));
         }
       } else if constexpr (OP == OP_DZ) {
         // dz - (1/T) g_l 1[v = t] = -(1/T) p (g_l + g_H (log p + H)),
@@ -703,7 +969,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     pack16(x[8 * k], x[8 * k + 1], f16), pack16(x[8 * k + 2], x[8 * k + 3], f16),
                     pack16(x[8 * k + 4], x[8 * k + 5], f16), pack16(x[8 * k + 6], x[8 * k + 7], f16));
             }
-            if (vb + 64 * b < p.V) stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 64 * b, nw0);
+            if (vb + 64 * b < p.V) sg.store(&tmO, w, lane, vb + 64 * b, nw0);
           }
         }
       } else if constexpr (OP == OP_DH) {
@@ -719,11 +985,12 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                               __float_as_uint(x[3]));
           }
           if (vb + 32 * b < p.K && nw0 < p.B)
-            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 32 * b, row0);
+            sg.store(&tmO, w, lane, vb + 32 * b, row0);
         }
       } else {
         const bool f16 = (p.idesc & (7u << 7)) == 0;
-        if (nw0 < p.V) add_targets(p, acc, t.a0 >> 8, half + q * 32, vb, lane, f16);
+        if (run.count > 0) add_targets(p, acc, run, vb, f16);
+        __syncwarp();
         const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -735,7 +1002,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                               pack16(x[4] * s, x[5] * s, f16), pack16(x[6] * s, x[7] * s, f16));
           }
           if (vb + 64 * b < p.K && nw0 < p.V)
-            stage_store(&tmO, xs, xs_u32, nbuf, w, lane, vb + 64 * b, nw0);
+            sg.store(&tmO, w, lane, vb + 64 * b, nw0);
         }
       }
     }

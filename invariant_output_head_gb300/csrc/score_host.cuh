@@ -10,6 +10,10 @@ namespace {
 // the int8-streaming kernel converts W again for every 64.
 constexpr int64_t kI8ScaledWideB = 65;
 constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
+// Up to this many rows the wide projection writes its logits (OP_SCOREZ):
+// with few row tiles most of the vocabulary is under way before a threshold
+// can thin the candidates out.
+constexpr int64_t kLogitRows = 1024;
 constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
 
 // 2-D tensor map of 16-bit or 32-bit elements: `inner` contiguous, rows of
@@ -50,11 +54,11 @@ int ensure_buffer(void** buf, size_t* have, size_t need, cudaStream_t stream) {
 }
 
 template <typename Kern, typename Params>
-cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned block, const Params& p,
+cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned block, const Params& p,
                              cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -93,19 +97,17 @@ cudaError_t op_pairs(detlm_head* h, int* pairs) {
   return cudaSuccess;
 }
 
-// The shared memory and stages of a product: as many stages as fit beside
-// the staging buffers, or beside the score products' records.
-template <int OP>
-uint32_t op_smem(int stages) {
-  const OpLayout L = op_layout(stages);
-  return (OP == OP_SCORE || OP == OP_SELECT ? L.score_total : L.store_total) + 1024u;
-}
+// The stages of a product: as many as fit beside its staging buffers and
+// words.
 template <int OP>
 int op_stages() {
   int s = kOpMaxStages;
-  while (s > 2 && op_smem<OP>(s) > kSmemLimit) --s;
+  while (s > 2 && op_layout(OP, s).total + 1024u > kSmemLimit) --s;
   return s;
 }
+// Rows of the box of a K-major operand of B rows: with fewer than 128 no more
+// than there are (whole 8-row swizzle atoms).
+uint32_t a_box_rows(int64_t B) { return B < kRowsHalf ? static_cast<uint32_t>((B + 7) / 8 * 8) : kRowsHalf; }
 
 template <int OP>
 cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap& b,
@@ -115,14 +117,15 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
   int pairs = 0;
   e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return e;
-  p.stages = static_cast<uint16_t>(op_stages<OP>());
-  p.stall = static_cast<uint16_t>(h->stall);
+  p.stages = static_cast<uint8_t>(op_stages<OP>());
+  p.a_rows = static_cast<uint8_t>(a_box_rows(p.B));
+  p.stall = static_cast<uint8_t>(h->stall);
   p.err = h->d_err;
   p.timeout_ns = h->timeout_ns;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.blockDim = dim3(kRowsThreads);
-  cfg.dynamicSmemBytes = op_smem<OP>(p.stages);
+  cfg.dynamicSmemBytes = op_layout(OP, p.stages).total + 1024u;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.units < pairs ? p.units : pairs)));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -142,6 +145,15 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
 // starts when everything before it is complete and visible.
 __global__ void weights_fence_kernel() {}
 
+bool is_device_memory(const void* p) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();   // clear the error the query recorded
+    return false;
+  }
+  return a.type == cudaMemoryTypeDevice;
+}
+
 void time_start(detlm_head* h, cudaStream_t stream) {
   if (h->t_start) cudaEventRecord(h->t_start, stream);
 }
@@ -160,10 +172,14 @@ int cand_blocks(int pairs, int64_t n_rt, int K) {
 }
 
 struct ScoreLayout {
+  int64_t n_vt, ld;
   size_t logits, rec, rec_part, zt, words, words_bytes, tiles, cand, total;
 };
-// Narrow: logits [B][V], records [3][B][n_vt]. Wide: records, target logits,
-// row words and tile marks (cleared together), candidates.
+// Up to kLogitRows rows: logits [B][ld] and records [3][B][n_vt] (without
+// alternatives only the narrow ones need logits). More: records, target
+// logits, row words and tile marks (cleared together), candidates.
+bool score_has_logits(int64_t B, int K) { return B <= kNarrowRows || (K > 0 && B <= kLogitRows); }
+
 ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
   ScoreLayout L;
   std::memset(&L, 0, sizeof(L));
@@ -174,14 +190,16 @@ ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
     at += round256(bytes);
     return a;
   };
-  const int64_t n_vt = narrow ? h->n_vt : tiles256(h->V);
-  if (narrow) L.logits = part(static_cast<size_t>(B) * h->V * 4);
-  L.rec_part = round256(static_cast<size_t>(B) * n_vt * 4) / 4;
+  L.n_vt = narrow ? h->n_vt : tiles256(h->V);
+  L.rec_part = round256(static_cast<size_t>(B) * L.n_vt * 4) / 4;
   L.rec = part(3 * L.rec_part * 4);
-  if (!narrow) {
+  if (score_has_logits(B, K)) {
+    L.ld = narrow ? h->V : (h->V + 31) / 32 * 32;
+    L.logits = part(static_cast<size_t>(B) * L.ld * 4);
+  } else {
     const int64_t n_rt = (B + kRowsM - 1) / kRowsM;
     L.zt = part(static_cast<size_t>(B) * 4);
-    L.words_bytes = (static_cast<size_t>(B) * row_words(K) + n_rt) * 4;
+    L.words_bytes = (static_cast<size_t>(B) * row_words(K) + 1 + n_rt) * 4;
     L.words = part(L.words_bytes);
     L.tiles = L.words + static_cast<size_t>(B) * row_words(K) * 4;
     // an upper bound of B * cand_blocks that grows with B, so that a
@@ -207,6 +225,9 @@ void score_merge_params(ScoreMergeParams* mp, const detlm_head* h, const ScoreLa
   std::memset(mp, 0, sizeof(*mp));
   float* rec = reinterpret_cast<float*>(static_cast<uint8_t*>(h->sws) + L.rec);
   mp->V = static_cast<int32_t>(h->V);
+  mp->n_vt = static_cast<int32_t>(L.n_vt);
+  mp->logits = reinterpret_cast<const float*>(static_cast<uint8_t*>(h->sws) + L.logits);
+  mp->ld = L.ld;
   mp->B = static_cast<int32_t>(B);
   mp->K = K;
   mp->c = kLog2eScore * inv_t;
@@ -264,9 +285,7 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
   if (e != cudaSuccess) return status_from_cuda(e);
   ScoreMergeParams mp;
   score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
-  mp.n_vt = p.n_vt;
-  mp.logits = p.logits;
-  return status_from_cuda(launch_dependent(score_narrow_kernel, static_cast<unsigned>(B),
+  return status_from_cuda(launch_dependent(score_logits_kernel<kBM>, static_cast<unsigned>(B),
                                            kScoreThreads, mp, stream));
 }
 
@@ -282,7 +301,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   const int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
   if (st != DETLM_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(h->sws);
-  const int64_t n_vt = tiles256(h->V), n_rt = (B + kRowsM - 1) / kRowsM;
+  const int64_t n_vt = L.n_vt, n_rt = (B + kRowsM - 1) / kRowsM;
   if (n_vt * n_rt >= (int64_t{1} << 31)) return DETLM_EINVAL;
   PairOpParams p;
   std::memset(&p, 0, sizeof(p));
@@ -302,6 +321,20 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   p.s.zt = reinterpret_cast<float*>(ws + L.zt);
   p.s.targets = targets;
   p.s.words = reinterpret_cast<int32_t*>(ws + L.words);
+  ScoreMergeParams mp;
+  score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
+  if (score_has_logits(B, K)) {
+    CUtensorMap zOut;
+    if (!encode_box(&zOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.logits, L.ld, B, L.ld * 4, 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_128B, false))
+      return DETLM_EINVAL;
+    time_start(h, stream);
+    e = launch_pairop<OP_SCOREZ>(h, tmH, h->tmW, zOut, p, stream);
+    time_stop(h, stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    return status_from_cuda(launch_dependent(score_logits_kernel<kRowsN>, static_cast<unsigned>(B),
+                                             kScoreThreads, mp, stream));
+  }
   p.s.cand = reinterpret_cast<float*>(ws + L.cand);
   p.s.tile_over = reinterpret_cast<const int32_t*>(ws + L.tiles);
   if (K > 0) {
@@ -312,9 +345,6 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   e = launch_pairop<OP_SCORE>(h, tmH, h->tmW, tmH, p, stream);
   time_stop(h, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
-  ScoreMergeParams mp;
-  score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
-  mp.n_vt = static_cast<int32_t>(n_vt);
   mp.C = p.C;
   mp.zt = p.s.zt;
   mp.cand = p.s.cand;
@@ -338,7 +368,7 @@ struct GradLayout {
   int64_t pass;             // vocabulary entries of a pass
   int64_t ld;               // dz row stride, elements
   int64_t rows_pad, n_rt, n_dt;
-  size_t scale, coef, tiles, list, dz, part, acc, total;
+  size_t scale, coef, starts, list, sums, dz, part, acc, total;
 };
 GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   GradLayout L;
@@ -360,8 +390,9 @@ GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   };
   L.scale = part(8);
   L.coef = part(static_cast<size_t>(B) * 4);
-  L.tiles = part(static_cast<size_t>((entries + 255) / 256) * 8);
-  L.list = part(static_cast<size_t>(B) * 8);
+  L.starts = part(static_cast<size_t>((entries + 255) / 256 * 256 + 1) * 4);
+  L.list = part(static_cast<size_t>(B) * 4);
+  L.sums = part(static_cast<size_t>(B) * h->d * 4);
   L.dz = part(static_cast<size_t>(B) * L.ld * 2);
   // split (few units) or whole segments, whichever is used
   const bool split = per * L.n_rt * L.n_dt < 2 * pairs;
@@ -412,7 +443,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
     const int64_t n_vt = (vc + 255) / 256;
     const int64_t vboxes = (vc + 63) / 64;
     CUtensorMap hK, wK, zOut, zK, wN, pOut, zN, hN, dwOut;
-    if (!encode_box(&hK, t16, in.h, h->d, B, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+    if (!encode_box(&hK, t16, in.h, h->d, B, row, 64, a_box_rows(B), CU_TENSOR_MAP_SWIZZLE_128B, true) ||
         !encode_box(&wK, t16, W, h->d, vc, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
         !encode_box(&zOut, t16, dz, vc, B, L.ld * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
       return DETLM_EINVAL;
@@ -446,7 +477,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       const bool split = (L.pass * L.n_rt * L.n_dt) / (seg_boxes * 64) < 2 * pairs;
       const int64_t per_part = split ? kGradChunkBoxes : seg_boxes;
       const int64_t parts = split ? (vboxes + per_part - 1) / per_part : segs;
-      if (!encode_box(&zK, t16, dz, vc, B, L.ld * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+      if (!encode_box(&zK, t16, dz, vc, B, L.ld * 2, 64, a_box_rows(B), CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&wN, t16, W, h->d, vc, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&pOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, h->d, parts * L.rows_pad,
                       h->d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
@@ -466,7 +497,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       f.part = part;
       f.rows_pad = L.rows_pad;
       f.B = static_cast<int32_t>(B);
-      f.d8 = static_cast<int32_t>(h->d / 8);
+      f.d4 = static_cast<int32_t>(h->d / 4);
       f.n_part = static_cast<int32_t>(parts);
       f.per_seg = split ? kSegChunks : 1;
       f.acc = reinterpret_cast<float*>(ws + L.acc);
@@ -479,7 +510,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       f.W = h->W;
       f.V = static_cast<int32_t>(h->V);
       f.out = static_cast<uint32_t*>(dh);
-      const int64_t blocks = (B * f.d8 + 255) / 256;
+      const int64_t blocks = (B * f.d4 + 255) / 256;
       e = launch_dependent(grad_fold_kernel, static_cast<unsigned>(blocks), 256, f, stream);
       if (e != cudaSuccess) return status_from_cuda(e);
     }
@@ -501,12 +532,30 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       tl.B = p.B;
       tl.v0 = p.t_off;
       tl.vc = p.V;
-      tl.tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
-      tl.list = reinterpret_cast<int2*>(ws + L.list);
+      tl.starts = reinterpret_cast<int32_t*>(ws + L.starts);
+      tl.list = reinterpret_cast<int32_t*>(ws + L.list);
       e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, tl, stream);
       if (e != cudaSuccess) return status_from_cuda(e);
-      q.w.tiles = tl.tiles;
+      TargetSumParams ts;
+      ts.targets = in.targets;
+      ts.starts = tl.starts;
+      ts.list = tl.list;
+      ts.coef = p.coef;
+      ts.h = static_cast<const uint4*>(in.h);
+      ts.sums = reinterpret_cast<float*>(ws + L.sums);
+      ts.n_vt = static_cast<int32_t>(n_vt);
+      ts.v0 = p.t_off;
+      ts.d8 = static_cast<int32_t>(h->d / 8);
+      ts.fp16 = h->dtype == DETLM_FP16;
+      if (B > kShortRun) {
+        e = launch_dependent(target_sum_kernel,
+                             dim3(static_cast<unsigned>(B), static_cast<unsigned>((ts.d8 + 127) / 128)),
+                             128, ts, stream);
+        if (e != cudaSuccess) return status_from_cuda(e);
+      }
+      q.w.starts = tl.starts;
       q.w.list = tl.list;
+      q.w.sums = ts.sums;
       q.w.h = in.h;
       q.w.scale = scale;
       e = launch_pairop<OP_DW>(h, zN, hN, dwOut, q, stream);
@@ -534,14 +583,14 @@ int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
   if (h == nullptr || bad_B(max_B) || top_k < 0 || top_k > kTopMax) return DETLM_EINVAL;
   if (h->P > 1 || h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
   if (max_B == 0) return DETLM_OK;
-  const int64_t narrow = max_B < kNarrowRows ? max_B : kNarrowRows;
-  size_t need = score_layout(h, narrow, top_k, 0).total;
-  if (max_B > kNarrowRows) {
-    int pairs = 0;
-    const cudaError_t e = op_pairs(h, &pairs);
-    if (e != cudaSuccess) return status_from_cuda(e);
-    const size_t wide = score_layout(h, max_B, top_k, pairs).total;
-    if (wide > need) need = wide;
+  int pairs = 0;
+  const cudaError_t e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  // each kind of call's workspace grows with its rows
+  size_t need = 0;
+  for (const int64_t most : {static_cast<int64_t>(kNarrowRows), kLogitRows, max_B}) {
+    const size_t n = score_layout(h, most < max_B ? most : max_B, top_k, pairs).total;
+    if (n > need) need = n;
   }
   return ensure_buffer(&h->sws, &h->sws_bytes, need, nullptr);
 }
@@ -651,22 +700,36 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   e = i8_to_f16(q_dev, h->h16, static_cast<size_t>(B) * h->d, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
   CUtensorMap tmH;
-  if (!encode_2d(&tmH, DETLM_FP16, h->h16, h->d, B, static_cast<uint32_t>(kRowsHalf)))
-    return DETLM_EINVAL;
-  HeadParams p;
-  int8_wide_params(h, B, &p);
-  p.logits = static_cast<float*>(out_dev);
-  p.x_scale = x_scale_dev;
-  p.w_scale = w_scale_dev;
-  CUtensorMap tmL = tmH;   // not read unless the map is valid
+  if (!encode_2d(&tmH, DETLM_FP16, h->h16, h->d, B, a_box_rows(B))) return DETLM_EINVAL;
+  int pairs = 0;
+  e = op_pairs(h, &pairs);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  const int64_t n_vt = tiles256(h->V), n_rt = (B + kRowsM - 1) / kRowsM;
+  if (n_vt * n_rt >= (int64_t{1} << 31)) return DETLM_EINVAL;
+  PairOpParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.B = static_cast<int32_t>(B);
+  p.V = static_cast<int32_t>(h->V);
+  p.n1 = static_cast<int32_t>(n_rt);
+  p.nk = static_cast<int32_t>((h->d + 63) / 64);
+  p.seg = p.nk;
+  p.units = static_cast<int32_t>(n_vt * n_rt);
+  p.idesc = idesc_f16(0u, kRowsM, kRowsN);
+  p.q.x_scale = x_scale_dev;
+  p.q.w_scale = w_scale_dev;
+  p.q.out = out_dev;
+  p.q.type = type;
+  // whole 16-byte rows of device memory leave by the tensor map
   const CUtensorMapDataType t = type == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : type == OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  p.tma_logits = (encode_logits(&tmL, out_dev, h->V, B, t, size) ? 1 : 0) | (type << 1);
-  const int64_t units = static_cast<int64_t>((p.n_vt + 1) / 2) * p.n_nt;
+  CUtensorMap tmO = tmH;   // not read unless it is valid
+  p.q.tma = (h->V * size) % 16 == 0 && aligned(out_dev, 16) && is_device_memory(out_dev) &&
+            encode_box(&tmO, t, out_dev, h->V, B, h->V * size, 128u / size, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B, false);
   time_start(h, stream);
-  e = launch_pair_kernel<MODE_SCALED>(h, h->tmW16, tmH, tmL, p, units,
-                                      pair_layout(p.stages).total + 1024, stream);
+  e = p.nk <= kScaledChunkBoxes ? launch_pairop<OP_SCALED1>(h, tmH, h->tmW16, tmO, p, stream)
+                                : launch_pairop<OP_SCALED>(h, tmH, h->tmW16, tmO, p, stream);
   time_stop(h, stream);
   return status_from_cuda(e);
 }

@@ -34,11 +34,12 @@ struct ScoreMergeParams {
   const float* rec_m;       // [B][n_vt]
   const float* rec_s;
   const float* rec_u;
-  const float* logits;      // narrow: [B][V]
+  const float* logits;      // in a workspace: [B][ld]
+  int64_t ld;
   const float* zt;          // wide: [B] target logits
   const float* cand;        // wide: [B][C][kCandFloats]
   int32_t* words;           // wide: [B][row_words(K)]
-  int32_t* tile_over;       // wide: [ceil(B / 256)]
+  int32_t* tile_over;       // wide: any mark, then [ceil(B / 256)] marks
   const int32_t* targets;   // optional
   float* logp;              // with targets
   float* entropy;           // optional
@@ -178,14 +179,17 @@ __device__ __forceinline__ void write_stats(const ScoreMergeParams& p, ScoreShar
   }
 }
 
-// Up to 128 rows: logits [B][V] and 128-entry records.
-__global__ void __launch_bounds__(kScoreThreads) score_narrow_kernel(const ScoreMergeParams p) {
+// Logits in a workspace, with records of TILE entries: 128 (the one-CTA
+// projection) or 256 (OP_SCOREZ).
+template <int TILE>
+__global__ void __launch_bounds__(kScoreThreads) score_logits_kernel(const ScoreMergeParams p) {
+  constexpr int kPer = TILE / 32;
   __shared__ ScoreShared sh;
   grid_dep_launch();   // the next call's projection may start (it prefetches only W)
   const int n = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t base = static_cast<size_t>(n) * p.n_vt;
-  const float* z = p.logits + static_cast<size_t>(n) * p.V;
+  const float* z = p.logits + static_cast<size_t>(n) * p.ld;
   const int g = static_cast<int>(threadIdx.x) - 128;
   if (g >= 0 && g < kTopMax) sh.slots[g] = 0;
   if (g == 0) sh.n_tiles = sh.n_entries = 0;
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_narrow_kernel(const Score
     if (tg >= 0 && tg < p.V) zt = z[tg];
   }
   if (warp < 4) {
-    Stat x = row_stat<true>(p, base, threadIdx.x);
+    Stat x = row_stat<TILE == kBM>(p, base, threadIdx.x);
 #pragma unroll
     for (int b = 1; b < 32; b <<= 1) x = stat_merge(x, shfl_xor(x, b), p.c);
     if (lane == 0) sh.part[warp] = x;
@@ -219,21 +223,22 @@ __global__ void __launch_bounds__(kScoreThreads) score_narrow_kernel(const Score
     if (nt > kTileCap) {
       if (g == 0) sh.n_entries = kEntryCap + 1;   // rescans below
     } else {
-      // four tiles at a time per warp: 16 loads in flight a lane
-      for (int i0 = (warp - 4) * 4; i0 < nt; i0 += 16) {
-        float x[4][4];
-        int v0[4];
+      // several tiles at a time per warp: 16 loads in flight a lane
+      constexpr int kT = 16 / kPer;
+      for (int i0 = (warp - 4) * kT; i0 < nt; i0 += 4 * kT) {
+        float x[kT][kPer];
+        int v0[kT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v0[i] = i0 + i < nt ? sh.tiles[i0 + i] * kBM + lane : p.V;
+        for (int i = 0; i < kT; ++i) {
+          v0[i] = i0 + i < nt ? sh.tiles[i0 + i] * TILE + lane : p.V;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < kPer; ++j)
             x[i][j] = v0[i] + 32 * j < p.V ? z[v0[i] + 32 * j] : __int_as_float(0x7fc00000);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) push_entry(sh, x[i][j], v0[i] + 32 * j, thr);
+          for (int j = 0; j < kPer; ++j) push_entry(sh, x[i][j], v0[i] + 32 * j, thr);
       }
     }
   }
@@ -337,7 +342,8 @@ __global__ void __launch_bounds__(kScoreThreads) score_wide_kernel(const ScoreMe
     w[RW_SEL_M] = __float_as_int(score_unkey(static_cast<uint32_t>(last >> 32)));
     w[RW_SEL_T] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(last));
     w[RW_OVER] = 1;
-    p.tile_over[n >> 8] = 1;
+    p.tile_over[0] = 1;
+    p.tile_over[1 + (n >> 8)] = 1;
   }
 }
 
@@ -347,8 +353,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const Score
   __shared__ ScoreShared sh;
   grid_dep_launch();
   grid_dep_wait();
+  if (p.tile_over[0] == 0) return;
   for (int n = blockIdx.x; n < p.B; n += gridDim.x) {
-    if (p.tile_over[n >> 8] == 0) continue;
+    if (p.tile_over[1 + (n >> 8)] == 0) continue;
     const int32_t* w = p.words + static_cast<size_t>(n) * row_words(p.K);
     if (w[RW_OVER] == 0) continue;
     const size_t base = static_cast<size_t>(n) * p.n_vt;
@@ -406,69 +413,148 @@ grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targ
   }
 }
 
-// The hidden rows by the vocabulary tile of their target, ascending within a
-// tile: block t counts the targets of lower tiles (its start) and then writes
-// its own rows in order. Targets outside [v0, v0 + vc) take no part. Every
-// block reads all B targets (from L2); no sums depend on an order.
+// The hidden rows by their target: list holds the rows whose target lies in
+// [v0, v0 + vc), by target, then ascending; starts[v] is where entry v's run
+// begins. Block t does the 256 entries of tile t: it counts the targets of
+// lower tiles and of each of its own entries, then places its rows in order.
+// Every block reads all B targets (from L2).
 struct TargetListParams {
   const int32_t* targets;
   int32_t B, v0, vc;
-  int32_t* tiles;           // [n_vt][2]
-  int2* list;               // [B]
+  int32_t* starts;          // [256 n_vt + 1]
+  int32_t* list;            // [B]
 };
 
 __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams p) {
-  __shared__ int sums[8][2];
-  __shared__ int counts[8];
+  __shared__ int sums[8];
+  __shared__ int at[256];   // counts of the tile's entries, then their next places
   grid_dep_launch();
   grid_dep_wait();
   const int tile = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int less = 0, mine = 0;
+  at[threadIdx.x] = 0;
+  __syncthreads();
+  // the entry of row n's target within this pass, or -1
+  auto entry = [&](int n) {
+    const int32_t t = n < p.B ? p.targets[n] : -1;
+    return t >= p.v0 && t - p.v0 < p.vc ? t - p.v0 : -1;
+  };
+  int less = 0;
+#pragma unroll 4
   for (int n = threadIdx.x; n < p.B; n += 256) {
-    const int64_t t = static_cast<int64_t>(p.targets[n]) - p.v0;
-    if (p.targets[n] < 0 || t < 0 || t >= p.vc) continue;
-    less += (t >> 8) < tile;
-    mine += (t >> 8) == tile;
+    const int v = entry(n);
+    if (v < 0) continue;
+    if ((v >> 8) < tile) ++less;
+    else if ((v >> 8) == tile) atomicAdd(&at[v & 255], 1);
   }
   less = __reduce_add_sync(0xffffffffu, less);
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) {
-    sums[warp][0] = less;
-    sums[warp][1] = mine;
+  if (lane == 0) sums[warp] = less;
+  __syncthreads();
+  less = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) less += sums[w];
+  // exclusive scan of the 256 counts
+  const int mine = at[threadIdx.x];
+  int scan = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, scan, s);
+    if (lane >= s) scan += x;
   }
   __syncthreads();
-  less = mine = 0;
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  int before = less, all = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    less += sums[w][0];
-    mine += sums[w][1];
+    before += w < warp ? sums[w] : 0;
+    all += sums[w];
   }
-  if (threadIdx.x == 0) {
-    p.tiles[2 * tile] = less;
-    p.tiles[2 * tile + 1] = mine;
-  }
-  int at = less;
-  const int end = less + mine;
-  for (int n0 = 0; n0 < p.B && at < end; n0 += 256) {
+  const int start = before + scan - mine;
+  p.starts[tile * 256 + threadIdx.x] = start;
+  if (tile == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 255) p.starts[tile * 256 + 256] = less + all;
+  if (all == 0) return;
+  at[threadIdx.x] = start;
+  __syncthreads();
+  // place the rows in ascending order: one warp's 32 rows after another's
+  for (int n0 = 0; n0 < p.B; n0 += 256) {
     const int n = n0 + threadIdx.x;
-    int64_t t = -1;
-    if (n < p.B && p.targets[n] >= 0) t = static_cast<int64_t>(p.targets[n]) - p.v0;
-    const bool hit = t >= 0 && t < p.vc && (t >> 8) == tile;
-    const uint32_t m = __ballot_sync(0xffffffffu, hit);
-    if (lane == 0) counts[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
+    const int v = entry(n);
+    const bool hit = v >= 0 && (v >> 8) == tile;
+    const int any = __syncthreads_or(hit);
+    if (!any) continue;
     for (int w = 0; w < 8; ++w) {
-      before += w < warp ? counts[w] : 0;
-      all += counts[w];
+      if (w == warp) {
+        const uint32_t same = __match_any_sync(0xffffffffu, hit ? (v & 255) : -1);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int place = 0;
+        if (hit) place = at[v & 255];
+        __syncwarp();
+        if (hit) {
+          p.list[place + rank] = n;
+          if (rank == 0) at[v & 255] = place + __popc(same);
+        }
+      }
+      __syncthreads();
     }
-    if (hit)
-      p.list[at + before + __popc(m & ((1u << lane) - 1))] = make_int2(n, static_cast<int>(t & 255));
-    at += all;
-    __syncthreads();
   }
+}
+
+// The sums of the long runs of the list (a target of more than kShortRun
+// rows): sums[first][k] = sum coef_n h[n][k], fp32, rows in ascending order.
+// Block (i, j): the run that starts at list position i, if one does, columns
+// 1024 j on, eight a thread.
+struct TargetSumParams {
+  const int32_t* targets;
+  const int32_t* starts;
+  const int32_t* list;
+  const float* coef;
+  const uint4* h;           // [B][d8]
+  float* sums;              // [B][d]
+  int32_t n_vt, v0, d8, fp16;
+};
+
+__global__ void __launch_bounds__(128) target_sum_kernel(const TargetSumParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int i = blockIdx.x;
+  if (i >= p.starts[p.n_vt * 256]) return;
+  const int v = p.targets[p.list[i]] - p.v0;
+  const int first = p.starts[v], end = p.starts[v + 1];
+  if (first != i || end - first <= kShortRun) return;
+  const int c = blockIdx.y * 128 + threadIdx.x;
+  if (c >= p.d8) return;
+  float a[8] = {};
+  const bool f16 = p.fp16 != 0;
+  constexpr int kU = 8;                       // rows in flight
+  for (int e0 = first; e0 < end; e0 += kU) {
+    uint4 w[kU];
+    float g[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      g[j] = 0.0f;
+      w[j] = make_uint4(0, 0, 0, 0);
+      if (e0 + j < end) {
+        const int n = p.list[e0 + j];
+        g[j] = p.coef[n];
+        w[j] = __ldg(p.h + static_cast<size_t>(n) * p.d8 + c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      if (e0 + j >= end) break;
+      const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 t = unpack16(x[k], f16);
+        a[2 * k] = fmaf(g[j], t.x, a[2 * k]);
+        a[2 * k + 1] = fmaf(g[j], t.y, a[2 * k + 1]);
+      }
+    }
+  }
+  float4* o = reinterpret_cast<float4*>(p.sums) + (static_cast<size_t>(first) * p.d8 + c) * 2;
+  o[0] = make_float4(a[0], a[1], a[2], a[3]);
+  o[1] = make_float4(a[4], a[5], a[6], a[7]);
 }
 
 // dh from the partial sums [n_part][rows_pad][d] (fp32): partials of a segment
@@ -476,12 +562,12 @@ __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams
 // whole segment), the segments' sums in ascending order onto the running
 // sum -- the same additions however the segments were split over units or
 // passes -- and last the target's entry of dz times its row of W.
-// Eight columns a thread; bound by reading the partials.
+// Four columns a thread; bound by reading the partials.
 struct FoldParams {
   const float* part;
   int64_t rows_pad;
-  int32_t B, d8;            // d / 8
-  int32_t n_part, per_seg;
+  int32_t B, d4;            // d / 4
+  int32_t n_part, per_seg;  // per_seg: 1 or kSegChunks
   float* acc;               // running sum [B][d] between passes
   int32_t first, last;      // first pass: start from zero; last: write dh
   int32_t fp16;
@@ -497,55 +583,53 @@ __global__ void __launch_bounds__(256) grad_fold_kernel(const FoldParams p) {
   grid_dep_launch();
   grid_dep_wait();
   const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= static_cast<int64_t>(p.B) * p.d8) return;
-  const int64_t step = p.rows_pad * p.d8 * 2;           // float4 per partial
-  const float4* src = reinterpret_cast<const float4*>(p.part) + i * 2;
-  float a[8];
-  float4* run = reinterpret_cast<float4*>(p.acc) + i * 2;
-  if (p.first) {
+  if (i >= static_cast<int64_t>(p.B) * p.d4) return;
+  const int64_t step = p.rows_pad * p.d4;               // float4 per partial
+  const float4* src = reinterpret_cast<const float4*>(p.part) + i;
+  float4* run = reinterpret_cast<float4*>(p.acc) + i;
+  float4 a = p.first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *run;
+  auto add = [](float4& x, const float4& y) {
+    x.x = __fadd_rn(x.x, y.x);
+    x.y = __fadd_rn(x.y, y.y);
+    x.z = __fadd_rn(x.z, y.z);
+    x.w = __fadd_rn(x.w, y.w);
+  };
+  constexpr int kU = kSegChunks;                        // loads in flight
+  for (int s = 0; s < p.n_part; s += kU) {
+    float4 v[kU];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = 0.0f;
-  } else {
-    const float4 x = run[0], y = run[1];
-    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-    a[4] = y.x; a[5] = y.y; a[6] = y.z; a[7] = y.w;
-  }
-  for (int s = 0; s < p.n_part; s += p.per_seg) {
-    float t[8];
-    const int e = min(s + p.per_seg, p.n_part);
-#pragma unroll 4
-    for (int j = s; j < e; ++j) {
-      const float4 x = __ldcs(src + j * step), y = __ldcs(src + j * step + 1);
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    for (int j = 0; j < kU; ++j)
+      if (s + j < p.n_part) v[j] = __ldcs(src + (s + j) * step);
+    if (p.per_seg == 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) t[k] = j == s ? v[k] : __fadd_rn(t[k], v[k]);
+      for (int j = 0; j < kU; ++j)
+        if (s + j < p.n_part) add(a, v[j]);
+    } else {
+#pragma unroll
+      for (int j = 1; j < kU; ++j)
+        if (s + j < p.n_part) add(v[0], v[j]);
+      add(a, v[0]);
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = __fadd_rn(a[k], t[k]);
   }
   if (!p.last) {
-    run[0] = make_float4(a[0], a[1], a[2], a[3]);
-    run[1] = make_float4(a[4], a[5], a[6], a[7]);
+    *run = a;
     return;
   }
   const float s = p.scale != nullptr ? p.scale[1] : 1.0f;
   const bool f16 = p.fp16 != 0;
-  const int n = static_cast<int>(i / p.d8), c8 = static_cast<int>(i - static_cast<int64_t>(n) * p.d8);
+  const int n = static_cast<int>(i / p.d4), c = static_cast<int>(i - static_cast<int64_t>(n) * p.d4);
   const int tg = p.targets[n];
   if (tg >= 0 && tg < p.V) {
     const float g = p.coef[n];
-    const uint4 w = reinterpret_cast<const uint4*>(p.W)[static_cast<size_t>(tg) * p.d8 + c8];
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 v = unpack16(x[k], f16);
-      a[2 * k] = fmaf(g, v.x, a[2 * k]);
-      a[2 * k + 1] = fmaf(g, v.y, a[2 * k + 1]);
-    }
+    const uint2 w = reinterpret_cast<const uint2*>(p.W)[static_cast<size_t>(tg) * p.d4 + c];
+    const float2 lo = unpack16(w.x, f16), hi = unpack16(w.y, f16);
+    a.x = fmaf(g, lo.x, a.x);
+    a.y = fmaf(g, lo.y, a.y);
+    a.z = fmaf(g, hi.x, a.z);
+    a.w = fmaf(g, hi.y, a.w);
   }
-  reinterpret_cast<uint4*>(p.out)[i] =
-      make_uint4(pack16(a[0] * s, a[1] * s, f16), pack16(a[2] * s, a[3] * s, f16),
-                 pack16(a[4] * s, a[5] * s, f16), pack16(a[6] * s, a[7] * s, f16));
+  reinterpret_cast<uint2*>(p.out)[i] =
+      make_uint2(pack16(a.x * s, a.y * s, f16), pack16(a.z * s, a.w * s, f16));
 }
 
 }  // namespace detlm
