@@ -172,25 +172,43 @@ static_assert(sizeof(PairOpParams) <= 128, "kernel parameter struct above 128 by
 //   OP_DH: n1 tiles of d, fastest, then n0 hidden-row tiles, then segments
 //   OP_DW: n1 tiles of d, fastest, then vocabulary tiles
 struct PairUnit { int a0, b0, kb0, nkb, seg; };
+
+// The units of one pair: u = pair, pair + n_pairs, ..., as (q, r) = (u / n1,
+// u % n1) without a division per unit.
+struct UnitWalk {
+  int u, q, r, du, dq, dr, n1;
+  __device__ __forceinline__ UnitWalk(int pair, int n_pairs, int n1_)
+      : u(pair), q(pair / n1_), r(pair - (pair / n1_) * n1_), du(n_pairs), dq(n_pairs / n1_),
+        dr(n_pairs - (n_pairs / n1_) * n1_), n1(n1_) {}
+  __device__ __forceinline__ void next() {
+    u += du;
+    q += dq;
+    r += dr;
+    if (r >= n1) {
+      r -= n1;
+      ++q;
+    }
+  }
+};
+
 template <int OP>
-__device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, int u) {
+__device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, const UnitWalk& w) {
   PairUnit t;
-  const int q = u / p.n1, r = u - q * p.n1;
   t.kb0 = 0;
   t.nkb = p.nk;
   t.seg = 0;
   if constexpr (OP == OP_DH) {
-    t.seg = q / p.n0;
-    t.a0 = (q - t.seg * p.n0) * 256;
-    t.b0 = r * 256;
+    t.seg = w.q / p.n0;
+    t.a0 = (w.q - t.seg * p.n0) * 256;
+    t.b0 = w.r * 256;
     t.kb0 = t.seg * p.seg;
     t.nkb = min(p.seg, p.nk - t.kb0);
   } else if constexpr (OP == OP_DW) {
-    t.a0 = q * 256;
-    t.b0 = r * 256;
+    t.a0 = w.q * 256;
+    t.b0 = w.r * 256;
   } else {
-    t.a0 = r * 256;
-    t.b0 = q * 256;
+    t.a0 = w.r * 256;
+    t.b0 = w.q * 256;
   }
   return t;
 }
@@ -201,7 +219,12 @@ __device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, int u) {
 // (Four buffers and fewer stages measured the same on the shortest K loops.)
 constexpr uint32_t kOpStageBuf = 32 * 128;
 constexpr uint32_t kOpXsBytes = 2 * kOpStageBuf;
-constexpr int kOpMaxStages = 7;
+// registers: the producer and the MMA issuer walk the units, which 40 (the
+// other pair kernels' share) do not hold
+constexpr int kOpRegsWg0 = 56, kOpRegsEpi = 224;
+static_assert(128 * kOpRegsWg0 + 256 * kOpRegsEpi == 384 * kRegsLaunchWide,
+              "register split must equal the launch budget");
+constexpr int kOpMaxStages = 12;
 
 __host__ __device__ constexpr bool op_stores(int op) { return op != OP_SCORE && op != OP_SELECT; }
 // Words kept beside the stages: the half-row records [3][128] of the score
@@ -213,14 +236,15 @@ __host__ __device__ constexpr uint32_t op_words(int op) {
 struct OpLayout {
   uint32_t a_bytes, stage_bytes, ctrl_off, red_off, xs_off, total;
 };
-// Stage s: this CTA's 128 rows of A, then its 128 of B (128 bytes of K each,
-// or two MN-major boxes of 8 KB each); then the barriers (full[S], empty[S],
+// Stage s: this CTA's rows of A (128, or as many as its box has), then its 128
+// rows of B (128 bytes of K each, or two MN-major boxes of 8 KB each); then
+// the barriers (full[S], empty[S],
 // slot_full[2], slot_empty[2], never, drain), the TMEM address holder and the
 // abort flag; the op's words; the staging buffers.
-__host__ __device__ inline OpLayout op_layout(int op, int stages) {
+__host__ __device__ inline OpLayout op_layout(int op, int stages, int a_rows) {
   OpLayout L;
-  L.a_bytes = kRowsHalf * kRowBytes;
-  L.stage_bytes = 2 * L.a_bytes;
+  L.a_bytes = static_cast<uint32_t>(a_rows) * kRowBytes;
+  L.stage_bytes = L.a_bytes + kRowsHalf * kRowBytes;
   L.ctrl_off = static_cast<uint32_t>(stages) * L.stage_bytes;
   L.red_off = L.ctrl_off + (2u * stages + 6u) * 8u + 16u;
   L.xs_off = L.red_off + 4u * op_words(op);
@@ -229,39 +253,56 @@ __host__ __device__ inline OpLayout op_layout(int op, int stages) {
   return L;
 }
 
-// A warp's staging buffers, in turn.
+// A warp's two staging buffers.
 struct Staging {
   uint8_t* xs;
-  uint32_t xs_u32, used;
-  // the next buffer, once its previous store has read it
-  __device__ __forceinline__ uint32_t next(int lane) {
-    const uint32_t buf = used & 1u;
-    if (used >= 2) {
-      if (lane == 0) bulk_wait_group_read<1>();
-      __syncwarp();
-    }
-    ++used;
-    return buf * kOpStageBuf;
+  uint32_t xs_u32;
+  // both buffers may be written: their previous stores have read them
+  __device__ __forceinline__ void claim(int lane) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
   }
-  // 32 rows x 128 bytes (lane = row) into the buffer at `off`
-  __device__ __forceinline__ void put(uint32_t off, const uint4 (&w)[8], int lane) {
+  // 32 rows x 128 bytes (lane = row) into buffer b
+  __device__ __forceinline__ void put(int b, const uint4 (&w)[8], int lane) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<uint4*>(xs + off + lane * 128 + 16 * (k ^ (lane & 7))) = w[k];
+      *reinterpret_cast<uint4*>(xs + b * kOpStageBuf + lane * 128 + 16 * (k ^ (lane & 7))) = w[k];
   }
-  // and out to the tensor map's box at (c0, row0); asynchronous
-  __device__ __forceinline__ void store(const void* tmap, const uint4 (&w)[8], int lane, int c0,
-                                        int row0) {
-    const uint32_t off = next(lane);
-    put(off, w, lane);
+  // out to the tensor map's boxes at (c0, row0) and, where two, (c1, row0);
+  // asynchronous
+  __device__ __forceinline__ void store(const void* tmap, int lane, int c0, int c1, bool two, int row0) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(tmap, xs_u32 + off, c0, row0);
+      tma_store_2d(tmap, xs_u32, c0, row0);
+      if (two) tma_store_2d(tmap, xs_u32 + kOpStageBuf, c1, row0);
       bulk_commit_group();
     }
   }
 };
+
+// 128 fp32 columns of a warp's rows through the staging buffers: columns c0
+// on, `cols` of them in the tensor.
+__device__ __forceinline__ void store_f32(const float (&acc)[8][16], Staging& sg, const void* tmap,
+                                          int lane, int c0, int cols, int row0) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (c0 + 64 * h >= cols) break;
+    sg.claim(lane);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint4 w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float* x = &acc[4 * h + 2 * b + (k >> 2)][4 * (k & 3)];
+        w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+      }
+      sg.put(b, w, lane);
+    }
+    sg.store(tmap, lane, c0 + 64 * h, c0 + 64 * h + 32, c0 + 64 * h + 32 < cols, row0);
+  }
+}
 
 // The score call's epilogue of one half-unit: this thread's row n, 128
 // entries from vb (nv of them exist).
@@ -486,26 +527,30 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (32 * b >= lim) break;
+      if ((b & 1) == 0) sg.claim(lane);        // (and the previous rows' reads are done)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         values(32 * b + 4 * k, x);
         w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                           __float_as_uint(x[3]));
       }
+      sg.put(b & 1, w, lane);
+      const bool more = (b & 1) == 0 && 32 * (b + 1) < lim;   // the pair's second box follows
+      if (more) continue;
+      const int c0 = vb + 32 * (b & ~1);
       if (p.q.tma) {
-        sg.store(tmO, w, lane, vb + 32 * b, nw0);
+        sg.store(tmO, lane, c0, c0 + 32, (b & 1) != 0, nw0);
       } else {
-        __syncwarp();                          // the previous box's reads are done
-        sg.put(0, w, lane);
         __syncwarp();
-        rows32(0, vb + 32 * b);
+        rows32(0, c0);
+        if ((b & 1) != 0) rows32(kOpStageBuf, c0 + 32);
       }
     }
   } else {
     const bool f16 = type == OUT_FP16;
+    sg.claim(lane);                            // (and the previous rows' reads are done)
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      if (64 * b >= lim) break;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         values(64 * b + 8 * k, x);
@@ -513,14 +558,11 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
         w[k] = make_uint4(pack16(x[0], x[1], f16), pack16(x[2], x[3], f16), pack16(y[0], y[1], f16),
                           pack16(y[2], y[3], f16));
       }
-      if (p.q.tma) {
-        sg.store(tmO, w, lane, vb + 64 * b, nw0);
-      } else {
-        if (b == 0) __syncwarp();              // the previous tail's reads are done
-        sg.put(b * kOpStageBuf, w, lane);
-      }
+      sg.put(b, w, lane);
     }
-    if (!p.q.tma) {
+    if (p.q.tma) {
+      sg.store(tmO, lane, vb, vb + 64, lim > 64, nw0);
+    } else {
       __syncwarp();
       rows16();
     }
@@ -543,7 +585,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int S = p.stages;
-  const OpLayout L = op_layout(OP, S);
+  const OpLayout L = op_layout(OP, S, p.a_rows);
   const uint32_t rank = cluster_rank();            // 0: leader, 1: peer
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int n_pairs = static_cast<int>(gridDim.x >> 1);
@@ -594,10 +636,11 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const int half = static_cast<int>(rank) * kRowsHalf;
   // OP_SELECT computes the units of the marked hidden-row tiles alone (the
   // marks are the previous kernel's, read after the wait by every role)
-  auto skip = [&](int u) {
-    if constexpr (OP == OP_SELECT) return p.s.tile_over[1 + u % p.n1] == 0;
+  auto skip = [&](const UnitWalk& w) {
+    if constexpr (OP == OP_SELECT) return p.s.tile_over[1 + w.r] == 0;
     return false;
   };
+  const UnitWalk first(pair, n_pairs, p.n1);
   int units = p.units;
   if constexpr (OP == OP_SELECT) {
     grid_dep_wait();
@@ -606,7 +649,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
     if (lane == 0) {
       const uint64_t pol_n = policy_evict_normal();
       const uint64_t pol_l = policy_evict_last();
@@ -624,7 +667,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       // not loaded (their rows of D are not read)
       auto bytes = [&](const PairUnit& t) {
         if constexpr (kMnA) return 2u * L.stage_bytes;
-        return 2u * L.a_bytes + (t.a0 + kRowsHalf < p.B ? 2u : 1u) * p.a_rows * 128u;
+        return 2u * kRowsHalf * kRowBytes + (t.a0 + kRowsHalf < p.B ? 2u : 1u) * L.a_bytes;
       };
       auto load_b = [&](int s, const PairUnit& t, int kb, uint32_t fb) {
         if constexpr (kMnB) {
@@ -640,9 +683,9 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       grid_dep_wait();
       uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
       bool ok = true;
-      for (int u = pair; u < units && ok; u += n_pairs) {
-        if (skip(u)) continue;
-        const PairUnit t = unit_of<OP>(p, u);
+      for (UnitWalk w = first; w.u < units && ok; w.next()) {
+        if (skip(w)) continue;
+        const PairUnit t = unit_of<OP>(p, w);
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; ++kb) {
           const uint32_t fb = cluster_addr(full_bar(stage), 0);
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
@@ -673,14 +716,14 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
     if (lane == 0 && rank == 0) {
       uint32_t stage = 0, phase = 0, slot = 0, sph = 0;
       bool ok = true;
       if (p.stall) ok = mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
-      for (int u = pair; u < units && ok; u += n_pairs) {
-        if (skip(u)) continue;
-        const int nkb = unit_of<OP>(p, u).nkb;
+      for (UnitWalk w = first; w.u < units && ok; w.next()) {
+        if (skip(w)) continue;
+        const int nkb = unit_of<OP>(p, w).nkb;
         for (int c0 = 0; c0 < nkb && ok; c0 += kBoxes) {
           if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
@@ -716,17 +759,16 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     __syncwarp();
   } else if (warp < 4) {
     // warps 2 and 3: no role, fewer registers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
   } else {
     // --------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsEpiWide));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kOpRegsEpi));
     grid_dep_wait();          // outputs and records: only after the previous kernels
     const int q = warp & 3;                    // TMEM lane quarter
     const int g = (warp - 4) >> 2;             // column half of the unit
     const int r = q * 32 + lane;               // row within this CTA's half
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
     Staging sg;
-    sg.used = 0;
     sg.xs = smem + L.xs_off + (warp - 4) * kOpXsBytes;
     sg.xs_u32 = smem_u32(sg.xs);
     float* red = reinterpret_cast<float*>(smem + L.red_off);  // the op's words
@@ -735,11 +777,11 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     bool failed = false;
     TargetRun ahead{};
     if constexpr (OP == OP_DW) {
-      if (pair < units) ahead.fetch(p, unit_of<OP>(p, pair).a0 + half + q * 32 + lane);
+      if (pair < units) ahead.fetch(p, unit_of<OP>(p, first).a0 + half + q * 32 + lane);
     }
-    for (int u = pair; u < units; u += n_pairs) {
-      if (skip(u)) continue;
-      const PairUnit t = unit_of<OP>(p, u);
+    for (UnitWalk walk = first; walk.u < units; walk.next()) {
+      if (skip(walk)) continue;
+      const PairUnit t = unit_of<OP>(p, walk);
       const int nw0 = t.a0 + half + q * 32;    // the warp's first row of D
       const int n = nw0 + lane;                // this thread's row
       const int rows = OP == OP_DW ? p.V : p.B;
@@ -760,10 +802,9 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       TargetRun run{};                         // OP_DW: this row's targets
       if constexpr (OP == OP_DW) {
         run = ahead;
-        if (u + n_pairs < units) {
-          const PairUnit t2 = unit_of<OP>(p, u + n_pairs);
-          ahead.fetch(p, t2.a0 + half + q * 32 + lane);
-        }
+        UnitWalk w2 = walk;
+        w2.next();
+        if (w2.u < units) ahead.fetch(p, unit_of<OP>(p, w2).a0 + half + q * 32 + lane);
       }
       const int n_chunks = (t.nkb + kBoxes - 1) / kBoxes;
       for (int c = 0; c < n_chunks; ++c) {
@@ -850,19 +891,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         Stat st{-INFINITY, 0.0f, 0.0f};
         if constexpr (OP == OP_SCORE || OP == OP_SCOREZ) {
           if constexpr (OP == OP_SCOREZ) {
-            if (nw0 < p.B) {
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                uint4 w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float* x = &acc[2 * b + (k >> 2)][4 * (k & 3)];
-                  w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                    __float_as_uint(x[2]), __float_as_uint(x[3]));
-                }
-                if (vb + 32 * b < p.V) sg.store(&tmO, w, lane, vb + 32 * b, nw0);
-              }
-            }
+            if (nw0 < p.B) store_f32(acc, sg, &tmO, lane, vb, p.V, nw0);
           }
           if (row_ok && nv > 0) {
             // the target's logit, if it lies in this half: a select chain
@@ -941,6 +970,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         }
         if (vb < p.V && nw0 < p.B) {
           const bool f16 = (p.idesc & (7u << 7)) == 0;   // the head's format
+          sg.claim(lane);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint4 w[8];
@@ -969,40 +999,33 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     pack16(x[8 * k], x[8 * k + 1], f16), pack16(x[8 * k + 2], x[8 * k + 3], f16),
                     pack16(x[8 * k + 4], x[8 * k + 5], f16), pack16(x[8 * k + 6], x[8 * k + 7], f16));
             }
-            if (vb + 64 * b < p.V) sg.store(&tmO, w, lane, vb + 64 * b, nw0);
+            sg.put(b, w, lane);
           }
+          sg.store(&tmO, lane, vb, vb + 64, vb + 64 < p.V, nw0);
         }
       } else if constexpr (OP == OP_DH) {
         // fp32 partial sums of the segment, rows padded to whole tiles
         const int row0 = t.seg * (p.n0 * 256) + nw0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint4 w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* x = &acc[2 * b + (k >> 2)][4 * (k & 3)];
-            w[k] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                              __float_as_uint(x[3]));
-          }
-          if (vb + 32 * b < p.K && nw0 < p.B)
-            sg.store(&tmO, w, lane, vb + 32 * b, row0);
-        }
+        if (nw0 < p.B) store_f32(acc, sg, &tmO, lane, vb, p.K, row0);
       } else {
         const bool f16 = (p.idesc & (7u << 7)) == 0;
         if (run.count > 0) add_targets(p, acc, run, vb, f16);
         __syncwarp();
         const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;
+        if (vb < p.K && nw0 < p.V) {
+          sg.claim(lane);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint4 w[8];
+          for (int b = 0; b < 2; ++b) {
+            uint4 w[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* x = &acc[4 * b + (k >> 1)][(k & 1) * 8];
-            w[k] = make_uint4(pack16(x[0] * s, x[1] * s, f16), pack16(x[2] * s, x[3] * s, f16),
-                              pack16(x[4] * s, x[5] * s, f16), pack16(x[6] * s, x[7] * s, f16));
+            for (int k = 0; k < 8; ++k) {
+              const float* x = &acc[4 * b + (k >> 1)][(k & 1) * 8];
+              w[k] = make_uint4(pack16(x[0] * s, x[1] * s, f16), pack16(x[2] * s, x[3] * s, f16),
+                                pack16(x[4] * s, x[5] * s, f16), pack16(x[6] * s, x[7] * s, f16));
+            }
+            sg.put(b, w, lane);
           }
-          if (vb + 64 * b < p.K && nw0 < p.V)
-            sg.store(&tmO, w, lane, vb + 64 * b, nw0);
+          sg.store(&tmO, lane, vb, vb + 64, vb + 64 < p.K, nw0);
         }
       }
     }

@@ -98,11 +98,12 @@ cudaError_t op_pairs(detlm_head* h, int* pairs) {
 }
 
 // The stages of a product: as many as fit beside its staging buffers and
-// words.
+// words (with few rows a stage is small, and more of them keep as much of B
+// in flight).
 template <int OP>
-int op_stages() {
+int op_stages(int a_rows) {
   int s = kOpMaxStages;
-  while (s > 2 && op_layout(OP, s).total + 1024u > kSmemLimit) --s;
+  while (s > 2 && op_layout(OP, s, a_rows).total + 1024u > kSmemLimit) --s;
   return s;
 }
 // Rows of the box of a K-major operand of B rows: with fewer than 128 no more
@@ -117,15 +118,15 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
   int pairs = 0;
   e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return e;
-  p.stages = static_cast<uint8_t>(op_stages<OP>());
-  p.a_rows = static_cast<uint8_t>(a_box_rows(p.B));
+  p.a_rows = static_cast<uint8_t>(OP == OP_DW ? kRowsHalf : a_box_rows(p.B));
+  p.stages = static_cast<uint8_t>(op_stages<OP>(p.a_rows));
   p.stall = static_cast<uint8_t>(h->stall);
   p.err = h->d_err;
   p.timeout_ns = h->timeout_ns;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.blockDim = dim3(kRowsThreads);
-  cfg.dynamicSmemBytes = op_layout(OP, p.stages).total + 1024u;
+  cfg.dynamicSmemBytes = op_layout(OP, p.stages, p.a_rows).total + 1024u;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.units < pairs ? p.units : pairs)));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
