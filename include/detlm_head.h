@@ -331,10 +331,11 @@ int detlm_head_score_backward(detlm_head_t* head, const void* h_dev,
 int detlm_head_reserve_backward(detlm_head_t* head, int64_t max_B);
 
 /* To be called after W was changed in place on `stream` (by an optimizer,
- * say), before the next call of this head: the calls request parts of W before
- * the stream's earlier kernels have finished, and an INT8 head keeps a
- * converted copy. Score calls of more than 128 rows and gradient calls of
- * BF16/FP16 heads read W in stream order and do not need it. */
+ * say), before the next call of this head: calls request parts of W before
+ * the stream's earlier kernels have finished, an INT8 head keeps an fp16 copy
+ * for its wide calls, and a BF16/FP16 head with d % 16 == 8 keeps a copy of W
+ * with padded rows for score and gradient calls (2 V d bytes or a little more;
+ * made by the first such call or reserve). */
 int detlm_head_weights_changed(detlm_head_t* head, cudaStream_t stream);
 
 /* Scaled logits of an INT8 head ("Eliminating Nondeterminism in LLM Inference

@@ -79,6 +79,10 @@ struct detlm_head {
   // integer front end: the quantized rows and their multipliers and shifts
   void* q8 = nullptr;
   size_t q8_bytes = 0;
+  // score and gradient calls, rows of W that do not start on 32-byte sectors
+  // (d % 16 == 8): a copy with rows on cache lines (see padded_weights)
+  void* Wp = nullptr;
+  bool wp_stale = false;
   // score and gradient calls: one buffer each, laid out per call
   void* sws = nullptr;
   size_t sws_bytes = 0;
@@ -1591,6 +1595,7 @@ void detlm_head_destroy(detlm_head_t* h) {
   if (h->W16) cudaFree(h->W16);
   if (h->h16) cudaFree(h->h16);
   if (h->stage) cudaFree(h->stage);
+  if (h->Wp) cudaFree(h->Wp);
   if (h->sws) cudaFree(h->sws);
   if (h->gws) cudaFree(h->gws);
   if (h->err_mapped) cudaFreeHost(h->err_mapped);

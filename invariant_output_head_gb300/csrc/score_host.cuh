@@ -69,6 +69,71 @@ cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned block, const Params&
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// An ordinary (not programmatic) launch between a change of W on the stream
+// and a call whose kernels request W boxes before waiting for the stream: it
+// starts when everything before it is complete and visible.
+__global__ void weights_fence_kernel() {}
+
+// Rows of 16-bit operands whose length is an odd multiple of 16 bytes start
+// in the middle of a 32-byte sector every other time, and a TMA box of them
+// moves half as fast (1024 x 50001 x 1000 scored: 105 us, x 1008: 76 us). Such
+// heads keep a copy of W with rows on cache lines, made by the first call (or
+// reserve) that wants it and again after detlm_head_weights_changed, and the
+// pair products copy their hidden rows likewise.
+bool needs_padding(const detlm_head* h) { return h->d % 16 != 0; }
+int64_t padded_d(const detlm_head* h) { return needs_padding(h) ? (h->d + 63) / 64 * 64 : h->d; }
+
+int pad_rows(const detlm_head* h, const void* in, void* out, int64_t rows, cudaStream_t stream) {
+  const int d8 = static_cast<int>(h->d / 8), ld8 = static_cast<int>(padded_d(h) / 8);
+  const int64_t want = (rows * d8 + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(want < 16 * h->num_sms ? want : 16 * h->num_sms);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return status_from_cuda(cudaLaunchKernelEx(&cfg, pad_rows_kernel, static_cast<const uint4*>(in),
+                                             static_cast<uint4*>(out), rows, d8, ld8));
+}
+
+// W for the score and gradient calls: itself, or its copy with padded rows.
+int padded_weights(detlm_head* h, cudaStream_t stream, const void** W) {
+  *W = h->W;
+  if (!needs_padding(h)) return DETLM_OK;
+  if (h->Wp == nullptr) {
+    void* p = nullptr;
+    const cudaError_t e = cudaMalloc(&p, static_cast<size_t>(h->V) * padded_d(h) * 2);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return status_from_cuda(e);
+    }
+    h->Wp = p;
+    h->wp_stale = true;
+  }
+  if (h->wp_stale) {
+    const int st = pad_rows(h, h->W, h->Wp, h->V, stream);
+    if (st != DETLM_OK) return st;
+    weights_fence_kernel<<<1, 32, 0, stream>>>();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return status_from_cuda(e);
+    h->wp_stale = false;
+  }
+  *W = h->Wp;
+  return DETLM_OK;
+}
+
+int reserve_weights(detlm_head* h) {
+  const void* W = nullptr;
+  const int st = padded_weights(h, nullptr, &W);
+  if (st != DETLM_OK || W == h->W) return st;
+  return status_from_cuda(cudaStreamSynchronize(nullptr));
+}
+
 // CTA pairs of the pair-product kernels that fit on the GPU at once (they all
 // have one shape: 384 threads, the full shared memory).
 cudaError_t op_pairs(detlm_head* h, int* pairs) {
@@ -141,11 +206,6 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
   return cudaLaunchKernelEx(&cfg, pairop_kernel<OP>, a, b, o, p);
 }
 
-// An ordinary (not programmatic) launch between a change of W on the stream
-// and a call whose kernels request W boxes before waiting for the stream: it
-// starts when everything before it is complete and visible.
-__global__ void weights_fence_kernel() {}
-
 bool is_device_memory(const void* p) {
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
@@ -174,7 +234,7 @@ int cand_blocks(int pairs, int64_t n_rt, int K) {
 
 struct ScoreLayout {
   int64_t n_vt, ld;
-  size_t logits, rec, rec_part, zt, words, words_bytes, tiles, cand, total;
+  size_t rows, logits, rec, rec_part, zt, words, words_bytes, tiles, cand, total;
 };
 // Up to kLogitRows rows: logits [B][ld] and records [3][B][n_vt] (without
 // alternatives only the narrow ones need logits). More: records, target
@@ -194,6 +254,7 @@ ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
   L.n_vt = narrow ? h->n_vt : tiles256(h->V);
   L.rec_part = round256(static_cast<size_t>(B) * L.n_vt * 4) / 4;
   L.rec = part(3 * L.rec_part * 4);
+  if (!narrow && needs_padding(h)) L.rows = part(static_cast<size_t>(B) * padded_d(h) * 2);
   if (score_has_logits(B, K)) {
     L.ld = narrow ? h->V : (h->V + 31) / 32 * 32;
     L.logits = part(static_cast<size_t>(B) * L.ld * 4);
@@ -251,8 +312,15 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
   CUtensorMap tmH;
   if (!encode_2d(&tmH, h->dtype, h_dev, h->d, B, static_cast<uint32_t>(N))) return DETLM_EINVAL;
   const ScoreLayout L = score_layout(h, B, K, 0);
-  const int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
+  int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
   if (st != DETLM_OK) return st;
+  const void* W = nullptr;
+  st = padded_weights(h, stream, &W);
+  if (st != DETLM_OK) return st;
+  CUtensorMap tmW;
+  if (!encode_box(&tmW, map_type(h->dtype), W, h->d, h->V, padded_d(h) * 2, 64, kBM,
+                  CU_TENSOR_MAP_SWIZZLE_128B, true))
+    return DETLM_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(h->sws);
   float* rec = reinterpret_cast<float*>(ws + L.rec);
   HeadParams p;
@@ -280,7 +348,7 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
   p.temperature = kLog2eScore * inv_t;
   const int grid = p.n_vt < h->num_sms ? p.n_vt : h->num_sms;
   time_start(h, stream);
-  cudaError_t e = launch_gemm<MODE_SCORE>(h->tmW, tmH, p, grid, smem_layout(N, p.stages).total + 1024,
+  cudaError_t e = launch_gemm<MODE_SCORE>(tmW, tmH, p, grid, smem_layout(N, p.stages).total + 1024,
                                           stream);
   time_stop(h, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
@@ -292,16 +360,29 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
 
 int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t B, int K,
                float inv_t, const ScoreOut& out, cudaStream_t stream) {
-  CUtensorMap tmH;
-  if (!encode_2d(&tmH, h->dtype, h_dev, h->d, B, static_cast<uint32_t>(kRowsHalf)))
-    return DETLM_EINVAL;
   int pairs = 0;
   cudaError_t e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return status_from_cuda(e);
   const ScoreLayout L = score_layout(h, B, K, pairs);
-  const int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
+  int st = ensure_buffer(&h->sws, &h->sws_bytes, L.total, stream);
   if (st != DETLM_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(h->sws);
+  const void* W = nullptr;
+  st = padded_weights(h, stream, &W);
+  if (st != DETLM_OK) return st;
+  const void* rows = h_dev;
+  if (needs_padding(h)) {
+    rows = ws + L.rows;
+    st = pad_rows(h, h_dev, ws + L.rows, B, stream);
+    if (st != DETLM_OK) return st;
+  }
+  CUtensorMap tmH, tmW;
+  const CUtensorMapDataType t16 = map_type(h->dtype);
+  if (!encode_box(&tmH, t16, rows, h->d, B, padded_d(h) * 2, 64, kRowsHalf, CU_TENSOR_MAP_SWIZZLE_128B,
+                  true) ||
+      !encode_box(&tmW, t16, W, h->d, h->V, padded_d(h) * 2, 64, kRowsHalf, CU_TENSOR_MAP_SWIZZLE_128B,
+                  true))
+    return DETLM_EINVAL;
   const int64_t n_vt = L.n_vt, n_rt = (B + kRowsM - 1) / kRowsM;
   if (n_vt * n_rt >= (int64_t{1} << 31)) return DETLM_EINVAL;
   PairOpParams p;
@@ -330,7 +411,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
                     CU_TENSOR_MAP_SWIZZLE_128B, false))
       return DETLM_EINVAL;
     time_start(h, stream);
-    e = launch_pairop<OP_SCOREZ>(h, tmH, h->tmW, zOut, p, stream);
+    e = launch_pairop<OP_SCOREZ>(h, tmH, tmW, zOut, p, stream);
     time_stop(h, stream);
     if (e != cudaSuccess) return status_from_cuda(e);
     return status_from_cuda(launch_dependent(score_logits_kernel<kRowsN>, static_cast<unsigned>(B),
@@ -343,7 +424,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
     if (e != cudaSuccess) return status_from_cuda(e);
   }
   time_start(h, stream);
-  e = launch_pairop<OP_SCORE>(h, tmH, h->tmW, tmH, p, stream);
+  e = launch_pairop<OP_SCORE>(h, tmH, tmW, tmH, p, stream);
   time_stop(h, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
   mp.C = p.C;
@@ -355,7 +436,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   if (e != cudaSuccess) return status_from_cuda(e);
   // a row's list can overflow only where it is shorter than all its blocks
   if (K == 0 || 16 * n_vt <= p.C) return DETLM_OK;
-  e = launch_pairop<OP_SELECT>(h, tmH, h->tmW, tmH, p, stream);
+  e = launch_pairop<OP_SELECT>(h, tmH, tmW, tmH, p, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
   const int64_t blocks = (B + 15) / 16 < 2 * h->num_sms ? (B + 15) / 16 : 2 * h->num_sms;
   return status_from_cuda(launch_dependent(score_select_kernel, static_cast<unsigned>(blocks),
@@ -369,7 +450,7 @@ struct GradLayout {
   int64_t pass;             // vocabulary entries of a pass
   int64_t ld;               // dz row stride, elements
   int64_t rows_pad, n_rt, n_dt;
-  size_t scale, coef, starts, list, sums, dz, part, acc, total;
+  size_t scale, coef, rows, starts, list, sums, dz, part, acc, total;
 };
 GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   GradLayout L;
@@ -391,6 +472,7 @@ GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   };
   L.scale = part(8);
   L.coef = part(static_cast<size_t>(B) * 4);
+  if (needs_padding(h)) L.rows = part(static_cast<size_t>(B) * padded_d(h) * 2);
   L.starts = part(static_cast<size_t>((entries + 255) / 256 * 256 + 1) * 4);
   L.list = part(static_cast<size_t>(B) * 4);
   L.sums = part(static_cast<size_t>(B) * h->d * 4);
@@ -416,15 +498,24 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
   cudaError_t e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return status_from_cuda(e);
   const GradLayout L = grad_layout(h, B, pairs);
-  const int st = ensure_buffer(&h->gws, &h->gws_bytes, L.total, stream);
+  int st = ensure_buffer(&h->gws, &h->gws_bytes, L.total, stream);
   if (st != DETLM_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(h->gws);
+  const void* Wrows = nullptr;
+  st = padded_weights(h, stream, &Wrows);
+  if (st != DETLM_OK) return st;
+  const void* hrows = in.h;
+  if (needs_padding(h)) {
+    hrows = ws + L.rows;
+    st = pad_rows(h, in.h, ws + L.rows, B, stream);
+    if (st != DETLM_OK) return st;
+  }
   float* scale = h->dtype == DETLM_FP16 ? reinterpret_cast<float*>(ws + L.scale) : nullptr;
   void* dz = ws + L.dz;
   float* part = reinterpret_cast<float*>(ws + L.part);
   const CUtensorMapDataType t16 = map_type(h->dtype);
   const uint32_t idesc = idesc_f16(h->dtype == DETLM_BF16 ? 1u : 0u, 256, 256);
-  const int64_t row = h->d * 2;
+  const int64_t row = h->d * 2, prow = padded_d(h) * 2;   // bytes of a row, and of one loaded
 
   if (scale != nullptr) {
     cudaLaunchConfig_t cfg;
@@ -440,12 +531,12 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
   time_start(h, stream);
   for (int64_t v0 = 0; v0 < h->V; v0 += L.pass) {
     const int64_t vc = h->V - v0 < L.pass ? h->V - v0 : L.pass;
-    const uint8_t* W = static_cast<const uint8_t*>(h->W) + v0 * row;
+    const uint8_t* W = static_cast<const uint8_t*>(Wrows) + v0 * prow;
     const int64_t n_vt = (vc + 255) / 256;
     const int64_t vboxes = (vc + 63) / 64;
     CUtensorMap hK, wK, zOut, zK, wN, pOut, zN, hN, dwOut;
-    if (!encode_box(&hK, t16, in.h, h->d, B, row, 64, a_box_rows(B), CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-        !encode_box(&wK, t16, W, h->d, vc, row, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+    if (!encode_box(&hK, t16, hrows, h->d, B, prow, 64, a_box_rows(B), CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+        !encode_box(&wK, t16, W, h->d, vc, prow, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
         !encode_box(&zOut, t16, dz, vc, B, L.ld * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
       return DETLM_EINVAL;
     PairOpParams p;
@@ -479,7 +570,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       const int64_t per_part = split ? kGradChunkBoxes : seg_boxes;
       const int64_t parts = split ? (vboxes + per_part - 1) / per_part : segs;
       if (!encode_box(&zK, t16, dz, vc, B, L.ld * 2, 64, a_box_rows(B), CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-          !encode_box(&wN, t16, W, h->d, vc, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&wN, t16, W, h->d, vc, prow, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&pOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, h->d, parts * L.rows_pad,
                       h->d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
         return DETLM_EINVAL;
@@ -518,7 +609,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
     if (dW != nullptr) {
       uint8_t* out = static_cast<uint8_t*>(dW) + v0 * row;
       if (!encode_box(&zN, t16, dz, vc, B, L.ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
-          !encode_box(&hN, t16, in.h, h->d, B, row, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
+          !encode_box(&hN, t16, hrows, h->d, B, prow, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, true) ||
           !encode_box(&dwOut, t16, out, h->d, vc, row, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B, false))
         return DETLM_EINVAL;
       PairOpParams q = p;
@@ -576,6 +667,7 @@ extern "C" {
 int detlm_head_weights_changed(detlm_head_t* h, cudaStream_t stream) {
   if (h == nullptr) return DETLM_EINVAL;
   h->w16_stale = true;
+  h->wp_stale = true;
   weights_fence_kernel<<<1, 32, 0, stream>>>();
   return status_from_cuda(cudaGetLastError());
 }
@@ -593,7 +685,8 @@ int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
     const size_t n = score_layout(h, most < max_B ? most : max_B, top_k, pairs).total;
     if (n > need) need = n;
   }
-  return ensure_buffer(&h->sws, &h->sws_bytes, need, nullptr);
+  const int st = ensure_buffer(&h->sws, &h->sws_bytes, need, nullptr);
+  return st == DETLM_OK ? reserve_weights(h) : st;
 }
 
 int detlm_head_score(detlm_head_t* h, const void* h_dev, const int32_t* targets_dev, int64_t B,
@@ -633,7 +726,8 @@ int detlm_head_reserve_backward(detlm_head_t* h, int64_t max_B) {
     const size_t n = grad_layout(h, b, pairs).total;
     if (n > need) need = n;
   }
-  return ensure_buffer(&h->gws, &h->gws_bytes, need, nullptr);
+  const int st = ensure_buffer(&h->gws, &h->gws_bytes, need, nullptr);
+  return st == DETLM_OK ? reserve_weights(h) : st;
 }
 
 int detlm_head_score_backward(detlm_head_t* h, const void* h_dev, const int32_t* targets_dev,

@@ -378,6 +378,20 @@ __global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const Score
   }
 }
 
+// Rows of d8 16-byte words into rows of ld8 (the words behind them are left:
+// the tensor maps end at d).
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint4* __restrict__ in,
+                                                       uint4* __restrict__ out, int64_t rows, int d8,
+                                                       int ld8) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int64_t n = rows * d8;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const int64_t r = i / d8;
+    out[r * ld8 + (i - r * d8)] = in[i];
+  }
+}
+
 // ------------------------------------------------------- gradient helpers
 // The power of two that dz of an fp16 head is held in: |dz| is at most
 // (|g_l| + |g_H| (1 + log V)) / T, whose largest value over the rows goes just
