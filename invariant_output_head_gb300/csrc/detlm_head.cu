@@ -23,6 +23,7 @@
 #include "rows_kernels.cuh"
 #include "pair_kernels.cuh"
 #include "shard_kernels.cuh"
+#include "int8_rows_kernel.cuh"
 #include "pairop_kernels.cuh"
 #include "score_kernels.cuh"
 

@@ -658,6 +658,25 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
   return DETLM_OK;
 }
 
+template <int NB>
+cudaError_t launch_int8_rows(const detlm_head* h, const Int8RowsParams& p, cudaStream_t stream) {
+  cudaError_t e = prepare_kernel<int8_rows_kernel<NB>>(0);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  const int64_t groups = (h->V + kI8RowsGroup - 1) / kI8RowsGroup;
+  cfg.gridDim = dim3(static_cast<unsigned>(groups < 2 * h->num_sms ? groups : 2 * h->num_sms));
+  cfg.blockDim = dim3(kI8RowsThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(NB) * h->d;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, int8_rows_kernel<NB>, p);
+}
+
 bool bad_temperature(float t) { return !(t > 0.0f) || !std::isfinite(t) || !std::isfinite(1.0f / t); }
 
 }  // namespace
@@ -773,6 +792,24 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   if (w_scale_dev == nullptr || !aligned(w_scale_dev, 4)) return DETLM_EINVAL;
   if (out_dev == nullptr || !aligned(out_dev, static_cast<size_t>(size))) return DETLM_EINVAL;
   cudaError_t e;
+  if (B <= kI8RowsMax) {
+    Int8RowsParams p;
+    p.W = static_cast<const int8_t*>(h->W);
+    p.q = q_dev;
+    p.x_scale = x_scale_dev;
+    p.w_scale = w_scale_dev;
+    p.out = out_dev;
+    p.V = static_cast<int32_t>(h->V);
+    p.d = static_cast<int32_t>(h->d);
+    p.B = static_cast<int32_t>(B);
+    p.type = type;
+    time_start(h, stream);
+    e = B == 1   ? launch_int8_rows<1>(h, p, stream)
+        : B == 2 ? launch_int8_rows<2>(h, p, stream)
+                 : launch_int8_rows<4>(h, p, stream);
+    time_stop(h, stream);
+    return status_from_cuda(e);
+  }
   if (B < kI8ScaledWideB) {
     const int N = int8_cols_for(B, h->d);
     CUtensorMap tmH;
