@@ -53,9 +53,9 @@ int ensure_buffer(void** buf, size_t* have, size_t need, cudaStream_t stream) {
   return DETLM_OK;
 }
 
-template <typename Kern, typename Params>
-cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned block, const Params& p,
-                             cudaStream_t stream) {
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, unsigned block, cudaStream_t stream,
+                             Args... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
@@ -66,7 +66,7 @@ cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned block, const Params&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // An ordinary (not programmatic) launch between a change of W on the stream
@@ -83,22 +83,15 @@ __global__ void weights_fence_kernel() {}
 bool needs_padding(const detlm_head* h) { return h->d % 16 != 0; }
 int64_t padded_d(const detlm_head* h) { return needs_padding(h) ? (h->d + 63) / 64 * 64 : h->d; }
 
+unsigned copy_grid(const detlm_head* h, int64_t words) {
+  const int64_t want = (words + 255) / 256;
+  return static_cast<unsigned>(want < 16 * h->num_sms ? want : 16 * h->num_sms);
+}
 int pad_rows(const detlm_head* h, const void* in, void* out, int64_t rows, cudaStream_t stream) {
   const int d8 = static_cast<int>(h->d / 8), ld8 = static_cast<int>(padded_d(h) / 8);
-  const int64_t want = (rows * d8 + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(want < 16 * h->num_sms ? want : 16 * h->num_sms);
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return status_from_cuda(cudaLaunchKernelEx(&cfg, pad_rows_kernel, static_cast<const uint4*>(in),
-                                             static_cast<uint4*>(out), rows, d8, ld8));
+  return status_from_cuda(launch_dependent(pad_rows_kernel, copy_grid(h, rows * d8), 256, stream,
+                                           static_cast<const uint4*>(in), static_cast<uint4*>(out),
+                                           rows, d8, ld8));
 }
 
 // W for the score and gradient calls: itself, or its copy with padded rows.
@@ -355,7 +348,7 @@ int score_narrow(detlm_head* h, const void* h_dev, const int32_t* targets, int64
   ScoreMergeParams mp;
   score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
   return status_from_cuda(launch_dependent(score_logits_kernel<kBM>, static_cast<unsigned>(B),
-                                           kScoreThreads, mp, stream));
+                                           kScoreThreads, stream, mp));
 }
 
 int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t B, int K,
@@ -415,7 +408,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
     time_stop(h, stream);
     if (e != cudaSuccess) return status_from_cuda(e);
     return status_from_cuda(launch_dependent(score_logits_kernel<kRowsN>, static_cast<unsigned>(B),
-                                             kScoreThreads, mp, stream));
+                                             kScoreThreads, stream, mp));
   }
   p.s.cand = reinterpret_cast<float*>(ws + L.cand);
   p.s.tile_over = reinterpret_cast<const int32_t*>(ws + L.tiles);
@@ -432,7 +425,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   mp.cand = p.s.cand;
   mp.words = p.s.words;
   mp.tile_over = reinterpret_cast<int32_t*>(ws + L.tiles);
-  e = launch_dependent(score_wide_kernel, static_cast<unsigned>(B), kScoreThreads, mp, stream);
+  e = launch_dependent(score_wide_kernel, static_cast<unsigned>(B), kScoreThreads, stream, mp);
   if (e != cudaSuccess) return status_from_cuda(e);
   // a row's list can overflow only where it is shorter than all its blocks
   if (K == 0 || 16 * n_vt <= p.C) return DETLM_OK;
@@ -440,7 +433,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   if (e != cudaSuccess) return status_from_cuda(e);
   const int64_t blocks = (B + 15) / 16 < 2 * h->num_sms ? (B + 15) / 16 : 2 * h->num_sms;
   return status_from_cuda(launch_dependent(score_select_kernel, static_cast<unsigned>(blocks),
-                                           kScoreThreads, mp, stream));
+                                           kScoreThreads, stream, mp));
 }
 
 // ---------------------------------------------------------------- gradient
@@ -518,14 +511,9 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
   const int64_t row = h->d * 2, prow = padded_d(h) * 2;   // bytes of a row, and of one loaded
 
   if (scale != nullptr) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = stream;
     const float h_max = 1.0f + std::log(static_cast<float>(h->V));
-    e = cudaLaunchKernelEx(&cfg, grad_scale_kernel, in.dlogp, in.dentropy, in.targets,
-                           static_cast<int>(B), inv_t, h_max, scale);
+    e = launch_dependent(grad_scale_kernel, 1, 1024, stream, in.dlogp, in.dentropy, in.targets,
+                         static_cast<int>(B), inv_t, h_max, scale);
     if (e != cudaSuccess) return status_from_cuda(e);
   }
   time_start(h, stream);
@@ -603,7 +591,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       f.V = static_cast<int32_t>(h->V);
       f.out = static_cast<uint32_t*>(dh);
       const int64_t blocks = (B * f.d4 + 255) / 256;
-      e = launch_dependent(grad_fold_kernel, static_cast<unsigned>(blocks), 256, f, stream);
+      e = launch_dependent(grad_fold_kernel, static_cast<unsigned>(blocks), 256, stream, f);
       if (e != cudaSuccess) return status_from_cuda(e);
     }
     if (dW != nullptr) {
@@ -626,7 +614,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       tl.vc = p.V;
       tl.starts = reinterpret_cast<int32_t*>(ws + L.starts);
       tl.list = reinterpret_cast<int32_t*>(ws + L.list);
-      e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, tl, stream);
+      e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, stream, tl);
       if (e != cudaSuccess) return status_from_cuda(e);
       TargetSumParams ts;
       ts.targets = in.targets;
@@ -642,7 +630,7 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       if (B > kShortRun) {
         e = launch_dependent(target_sum_kernel,
                              dim3(static_cast<unsigned>(B), static_cast<unsigned>((ts.d8 + 127) / 128)),
-                             128, ts, stream);
+                             128, stream, ts);
         if (e != cudaSuccess) return status_from_cuda(e);
       }
       q.w.starts = tl.starts;
@@ -829,7 +817,9 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   }
   const int st = ensure_wide(h, B, stream);
   if (st != DETLM_OK) return st;
-  e = i8_to_f16(q_dev, h->h16, static_cast<size_t>(B) * h->d, stream);
+  const size_t words = static_cast<size_t>(B) * h->d / 16;
+  e = launch_dependent(rows_to_f16_kernel, copy_grid(h, static_cast<int64_t>(words)), 256, stream,
+                       reinterpret_cast<const uint4*>(q_dev), static_cast<uint4*>(h->h16), words);
   if (e != cudaSuccess) return status_from_cuda(e);
   CUtensorMap tmH;
   if (!encode_2d(&tmH, DETLM_FP16, h->h16, h->d, B, a_box_rows(B))) return DETLM_EINVAL;

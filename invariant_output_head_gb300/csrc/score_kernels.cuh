@@ -55,8 +55,7 @@ struct ScoreShared {
   uint32_t slots[kTopMax];
   int n_tiles, n_entries;
   int32_t tiles[kTileCap];
-  uint32_t key[kEntryCap];
-  int32_t id[kEntryCap];
+  unsigned long long entry[kEntryCap];   // order words
   unsigned long long best[kScoreThreads / 32];
 };
 
@@ -113,19 +112,20 @@ __device__ __forceinline__ void write_top(const ScoreMergeParams& p, ScoreShared
                                           Visit visit) {
   const Stat tot = sh.tot;
   const float log_s = logf(tot.S);
-  auto put = [&](int k, uint32_t key, int32_t id) {
+  auto put = [&](int k, unsigned long long word) {
     const size_t o = static_cast<size_t>(n) * p.K + k;
-    p.top_token[o] = id;
-    p.top_logp[o] = (score_unkey(key) - tot.m) * p.inv_t - log_s;
+    p.top_token[o] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(word));
+    p.top_logp[o] = (score_unkey(static_cast<uint32_t>(word >> 32)) - tot.m) * p.inv_t - log_s;
   };
   const int ne = sh.n_entries;
   int found = min(ne, p.K);
   if (ne <= kEntryCap) {
     for (int e = threadIdx.x; e < ne; e += kScoreThreads) {
-      const unsigned long long me = order_word(sh.key[e], sh.id[e]);
+      const unsigned long long me = sh.entry[e];
       int rank = 0;
-      for (int j = 0; j < ne; ++j) rank += order_word(sh.key[j], sh.id[j]) > me;
-      if (rank < p.K) put(rank, sh.key[e], sh.id[e]);
+#pragma unroll 4
+      for (int j = 0; j < ne; ++j) rank += sh.entry[j] > me;
+      if (rank < p.K) put(rank, me);
     }
   } else {
     unsigned long long last = ~0ull;
@@ -134,9 +134,7 @@ __device__ __forceinline__ void write_top(const ScoreMergeParams& p, ScoreShared
       last = next_best(sh, last, visit);
       if (last == 0) break;
       found = k + 1;
-      if (threadIdx.x == 0)
-        put(k, static_cast<uint32_t>(last >> 32),
-            static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(last)));
+      if (threadIdx.x == 0) put(k, last);
     }
   }
   // fewer logits than alternatives that are numbers
@@ -149,10 +147,7 @@ __device__ __forceinline__ void write_top(const ScoreMergeParams& p, ScoreShared
 __device__ __forceinline__ void push_entry(ScoreShared& sh, float z, int32_t id, float thr) {
   if (z >= thr) {
     const int at = atomicAdd(&sh.n_entries, 1);
-    if (at < kEntryCap) {
-      sh.key[at] = score_key(z);
-      sh.id[at] = id;
-    }
+    if (at < kEntryCap) sh.entry[at] = order_word(score_key(z), id);
   }
 }
 
@@ -206,25 +201,41 @@ __global__ void __launch_bounds__(kScoreThreads) score_logits_kernel(const Score
     for (int b = 1; b < 32; b <<= 1) x = stat_merge(x, shfl_xor(x, b), p.c);
     if (lane == 0) sh.part[warp] = x;
   } else if (p.K > 0) {
+    // the tiles' maxima, kept in registers up to 1024 tiles (further ones are
+    // read again)
+    constexpr int kKeep = 8;
+    float keep[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int t = g + 128 * i;
+      keep[i] = t < p.n_vt ? p.rec_m[base + t] : __int_as_float(0x7fc00000);
+    }
     named_bar_sync(1, 128);                       // slots are zero
-    for (int t = g; t < p.n_vt; t += 128)
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (g + 128 * i < p.n_vt) atomicMax(&sh.slots[(g + 128 * i) % p.K], score_key(keep[i]));
+    for (int t = g + 128 * kKeep; t < p.n_vt; t += 128)
       atomicMax(&sh.slots[t % p.K], score_key(p.rec_m[base + t]));
     named_bar_sync(1, 128);
     uint32_t lo = lane < p.K ? sh.slots[lane] : 0xFFFFFFFFu;
     lo = __reduce_min_sync(0xffffffffu, lo);
     const float thr = score_unkey(lo);
-    for (int t = g; t < p.n_vt; t += 128)
-      if (p.rec_m[base + t] >= thr) {
+    auto want = [&](float m, int t) {
+      if (m >= thr) {
         const int at = atomicAdd(&sh.n_tiles, 1);
         if (at < kTileCap) sh.tiles[at] = t;
       }
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) want(keep[i], g + 128 * i);
+    for (int t = g + 128 * kKeep; t < p.n_vt; t += 128) want(p.rec_m[base + t], t);
     named_bar_sync(1, 128);
     const int nt = sh.n_tiles;
     if (nt > kTileCap) {
       if (g == 0) sh.n_entries = kEntryCap + 1;   // rescans below
     } else {
-      // several tiles at a time per warp: 16 loads in flight a lane
-      constexpr int kT = 16 / kPer;
+      // several tiles at a time per warp: 32 loads in flight a lane
+      constexpr int kT = 32 / kPer;
       for (int i0 = (warp - 4) * kT; i0 < nt; i0 += 4 * kT) {
         float x[kT][kPer];
         int v0[kT];
@@ -375,6 +386,24 @@ __global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const Score
     gather_blocks(p, sh, n, nb, __int_as_float(w[RW_SEL_M]), threadIdx.x, kScoreThreads);
     __syncthreads();
     write_top(p, sh, n, [&](auto f) { visit_blocks(p, n, nb, f); });
+  }
+}
+
+// int8 -> fp16 (exact) of the hidden rows, n16 16-byte words, as a dependent
+// of the previous kernel on the stream.
+__global__ void __launch_bounds__(256) rows_to_f16_kernel(const uint4* __restrict__ in,
+                                                          uint4* __restrict__ out, size_t n16) {
+  grid_dep_launch();
+  grid_dep_wait();
+  for (size_t i = blockIdx.x * size_t{256} + threadIdx.x; i < n16; i += size_t{256} * gridDim.x) {
+    const uint4 w = in[i];
+    uint4 o0, o1;
+    i8x4_to_h2x2(w.x, o0.x, o0.y);
+    i8x4_to_h2x2(w.y, o0.z, o0.w);
+    i8x4_to_h2x2(w.z, o1.x, o1.y);
+    i8x4_to_h2x2(w.w, o1.z, o1.w);
+    out[2 * i] = o0;
+    out[2 * i + 1] = o1;
   }
 }
 
