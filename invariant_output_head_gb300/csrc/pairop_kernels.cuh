@@ -27,8 +27,9 @@
 //   OP_DW      D[v, k] = sum_n dz[n, v] h[n, k]: both operands with the free
 //              axis contiguous.
 //   OP_SCALED  D[n, v] = q W^T of int8 values held as fp16, written times a
-//              scale of the row and one of the column; OP_SCALED1 where d is
-//              at most one chunk (no integer conversions).
+//              scale of the row and one of the column; OP_SCALED2 where d is
+//              at most two chunks (no integer conversions: the rounded sum of
+//              two exact integers is the rounding of their exact sum).
 //
 // The target's entry (g_l (1 - p) - ...) / T of the gradient never passes
 // through 16 bits: it is by far the largest of its row, and its rounding would
@@ -63,8 +64,8 @@
 namespace detlm {
 
 enum : int { OP_SCORE = 0, OP_SCOREZ = 1, OP_SELECT = 2, OP_DZ = 3, OP_DH = 4, OP_DW = 5,
-             OP_SCALED = 6, OP_SCALED1 = 7 };
-__host__ __device__ constexpr bool op_scaled(int op) { return op == OP_SCALED || op == OP_SCALED1; }
+             OP_SCALED = 6, OP_SCALED2 = 7 };
+__host__ __device__ constexpr bool op_scaled(int op) { return op == OP_SCALED || op == OP_SCALED2; }
 
 constexpr int kGradChunkBoxes = 32;      // 64-element K boxes per gradient chunk (2048)
 constexpr int kScaledChunkBoxes = 16;    // OP_SCALED: 1024
@@ -449,7 +450,7 @@ __device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[
 // rounded product, and the output's own rounding. Rows that do not start on
 // 16-byte boundaries are written from the staging buffer one row at a time, a
 // 4-byte word a lane: 16-bit rows of odd origin pair elements (2 l - 1, 2 l).
-// acc: the int32 sums, or (OP_SCALED1) the fp32 integers that the tensor core
+// acc: the int32 sums, or (OP_SCALED2) the fp32 integers that the tensor core
 // left; sw: the warp's 128 column scales in shared memory.
 template <typename Acc>
 __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* tmO,
@@ -469,47 +470,35 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
             sb + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3));
     }
   };
-  // 16-bit rows that it cannot store: 16 lanes a row, each a 16-byte word of
-  // the row's aligned middle, put together from two chunks of the staged row;
-  // the ends (at most 7 elements each) one element a lane
+  // 16-bit rows that it cannot store. Their owners have staged them as 4-byte
+  // words of the row's own alignment (rows at odd elements: elements 2 k - 1
+  // and 2 k in word k), so a warp writes a row's words 32 at a time; what
+  // shares a word with a neighbour goes element by element.
   auto rows16 = [&]() {
-    const int half = lane >> 4, l = lane & 15;
-    const int cols = min(128, lim);
-    auto chunk = [&](int r, int c) {           // elements 8 c .. 8 c + 7 of row r
-      return *reinterpret_cast<const uint4*>(sg.xs + (c >> 3) * kOpStageBuf + r * 128 +
-                                             16 * ((c & 7) ^ (r & 7)));
-    };
-#pragma unroll 2
-    for (int r0 = 0; r0 < rows; r0 += 2) {
-      const int r = r0 + half;
-      if (r >= rows) break;                    // (no exchange between lanes below)
-      uint16_t* o = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(nw0 + r) * p.V + vb;
-      // elements before the first 16-byte boundary, whole words behind it
-      const int head = min(cols, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(o) & 15)) & 15) >> 1);
-      const int words = (cols - head) >> 3;
-      const uint4 a = chunk(r, l), b = chunk(r, min(l + 1, 15));
-      const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (l < words) {
-        const int s2 = head >> 1;              // whole 4-byte steps of the shift
-        uint32_t y[5];
-#pragma unroll
-        for (int k = 0; k < 5; ++k) {
-          y[k] = x[k];
-#pragma unroll
-          for (int j = 1; j < 4; ++j)
-            if (k + j < 8) y[k] = s2 == j ? x[k + j] : y[k];
-        }
-        uint4 v = make_uint4(y[0], y[1], y[2], y[3]);
-        if (head & 1)
-          v = make_uint4(__funnelshift_r(y[0], y[1], 16), __funnelshift_r(y[1], y[2], 16),
-                         __funnelshift_r(y[2], y[3], 16), __funnelshift_r(y[3], y[4], 16));
-        *reinterpret_cast<uint4*>(o + head + 8 * l) = v;
+    const uint8_t* sb = sg.xs + 4 * (lane & 3);
+    uint16_t* o = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(nw0) * p.V + vb;
+    if (lim >= 128) {
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r, o += p.V) {
+        const uint32_t at = r * 128 + 16 * ((lane >> 2) ^ (r & 7));
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(sb + at);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(sb + kOpStageBuf + at);
+        const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(o) >> 1) & 1);
+        uint32_t* x = reinterpret_cast<uint32_t*>(o - odd) + lane;
+        if (odd && lane == 0) o[0] = static_cast<uint16_t>(w0 >> 16);
+        else x[0] = w0;
+        x[32] = w1;
       }
-      // lanes 0..7: the head, 8..15: what the words leave over
-      const int e = l < 8 ? l : head + 8 * words + l - 8;
-      if (l < 8 ? e < head : e < cols)
-        o[e] = *reinterpret_cast<const uint16_t*>(sg.xs + (e >> 6) * kOpStageBuf + r * 128 +
-                                                  16 * (((e >> 3) & 7) ^ (r & 7)) + 2 * (e & 7));
+    } else {
+      for (int r = 0; r < rows; ++r, o += p.V) {
+        const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(o) >> 1) & 1);
+        for (int e = lane; e < lim; e += 32) {
+          const int k = (e + odd) >> 1;
+          o[e] = *reinterpret_cast<const uint16_t*>(sg.xs + (k >> 5) * kOpStageBuf + r * 128 +
+                                                    16 * (((k >> 2) & 7) ^ (r & 7)) + 4 * (k & 3) +
+                                                    2 * ((e + odd) & 1));
+        }
+      }
     }
   };
   // columns j .. j + 3
@@ -548,6 +537,11 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
     }
   } else {
     const bool f16 = type == OUT_FP16;
+    // this row's origin is an odd element (and not the tensor map's to store)
+    uint16_t* mine = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(n) * p.V + vb;
+    const uint32_t shift =
+        !p.q.tma ? static_cast<uint32_t>((reinterpret_cast<uintptr_t>(mine) >> 1) & 1) * 16u : 0u;
+    uint32_t last = 0;
     sg.claim(lane);                            // (and the previous rows' reads are done)
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -555,14 +549,19 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
       for (int k = 0; k < 8; ++k) {
         values(64 * b + 8 * k, x);
         values(64 * b + 8 * k + 4, y);
-        w[k] = make_uint4(pack16(x[0], x[1], f16), pack16(x[2], x[3], f16), pack16(y[0], y[1], f16),
-                          pack16(y[2], y[3], f16));
+        const uint32_t e[4] = {pack16(x[0], x[1], f16), pack16(x[2], x[3], f16),
+                               pack16(y[0], y[1], f16), pack16(y[2], y[3], f16)};
+        w[k] = make_uint4(__funnelshift_l(last, e[0], shift), __funnelshift_l(e[0], e[1], shift),
+                          __funnelshift_l(e[1], e[2], shift), __funnelshift_l(e[2], e[3], shift));
+        last = e[3];
       }
       sg.put(b, w, lane);
     }
     if (p.q.tma) {
       sg.store(tmO, lane, vb, vb + 64, lim > 64, nw0);
     } else {
+      // (the 128th element of a shifted row has no word)
+      if (shift != 0 && lim >= 128 && n < p.B) mine[127] = static_cast<uint16_t>(last >> 16);
       __syncwarp();
       rows16();
     }

@@ -850,7 +850,7 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
             encode_box(&tmO, t, out_dev, h->V, B, h->V * size, 128u / size, 32,
                        CU_TENSOR_MAP_SWIZZLE_128B, false);
   time_start(h, stream);
-  e = p.nk <= kScaledChunkBoxes ? launch_pairop<OP_SCALED1>(h, tmH, h->tmW16, tmO, p, stream)
+  e = p.nk <= 2 * kScaledChunkBoxes ? launch_pairop<OP_SCALED2>(h, tmH, h->tmW16, tmO, p, stream)
                                 : launch_pairop<OP_SCALED>(h, tmH, h->tmW16, tmO, p, stream);
   time_stop(h, stream);
   return status_from_cuda(e);
