@@ -1,7 +1,7 @@
 // pairop_kernels.cuh -- the matrix products of the score call and of its
 // gradient, on CTA pairs.
 //
-// One kernel body, eight products. A unit is a 256 x 256 tile of
+// One kernel body, nine products. A unit is a 256 x 256 tile of
 // D = A * B^T, computed by a cluster of two CTAs with tcgen05.mma.cta_group::2
 // (each CTA holds 128 rows of A and 128 of B per stage and finds its own 128
 // rows of D in its tensor memory), with the pair protocol of
@@ -25,7 +25,7 @@
 //   OP_DH      D[n, k] = sum_v dz[n, v] W[v, k]: A = dz with the contracted
 //              axis contiguous, B = W with the free axis contiguous.
 //   OP_DW      D[v, k] = sum_n dz[n, v] h[n, k]: both operands with the free
-//              axis contiguous.
+//              axis contiguous. OP_DW_FEW: of at most kFewRows rows.
 //   OP_SCALED  D[n, v] = q W^T of int8 values held as fp16, written times a
 //              scale of the row and one of the column; OP_SCALED2 where d is
 //              at most two chunks (no integer conversions: the rounded sum of
@@ -64,13 +64,15 @@
 namespace detlm {
 
 enum : int { OP_SCORE = 0, OP_SCOREZ = 1, OP_SELECT = 2, OP_DZ = 3, OP_DH = 4, OP_DW = 5,
-             OP_SCALED = 6, OP_SCALED2 = 7 };
+             OP_SCALED = 6, OP_SCALED2 = 7, OP_DW_FEW = 8 };
+__host__ __device__ constexpr bool op_dw(int op) { return op == OP_DW || op == OP_DW_FEW; }
 __host__ __device__ constexpr bool op_scaled(int op) { return op == OP_SCALED || op == OP_SCALED2; }
 
 constexpr int kGradChunkBoxes = 32;      // 64-element K boxes per gradient chunk (2048)
 constexpr int kScaledChunkBoxes = 16;    // OP_SCALED: 1024
 constexpr int kSegChunks = 8;            // gradient chunks per vocabulary segment (16384)
 constexpr int kCandFloats = 20;          // a candidate block: 16 logits, its index, padding
+constexpr int kFewRows = 128;            // OP_DW: rows whose targets a warp holds in registers
 constexpr int kShortRun = 2;             // OP_DW: hidden rows of one target added one by one
 constexpr int kRowWords = 4;             // words of a row before its slots
 enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
@@ -123,11 +125,11 @@ struct GradArgs {
 };
 
 struct DwArgs {
+  const int32_t* targets;   // OP_DW_FEW: [B] (and no list)
   const int32_t* starts;    // [256 n_vt + 1] where a vocabulary entry's run in the list starts
   const int32_t* list;      // rows of h by their target (those of this pass), then ascending
   const float* sums;        // [list position][d] sums of the runs longer than kShortRun
   const void* h;            // [B][d]
-  const void* unused;
   const float* scale;       // as above
 };
 struct ScaledArgs {
@@ -204,7 +206,7 @@ __device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, const UnitWal
     t.b0 = w.r * 256;
     t.kb0 = t.seg * p.seg;
     t.nkb = min(p.seg, p.nk - t.kb0);
-  } else if constexpr (OP == OP_DW) {
+  } else if constexpr (op_dw(OP)) {
     t.a0 = w.q * 256;
     t.b0 = w.r * 256;
   } else {
@@ -403,6 +405,26 @@ struct TargetRun {
   }
 };
 
+// acc += g h[n][col0 ..], 128 columns or up to d (a multiple of 8).
+__device__ __forceinline__ void add_row(const PairOpParams& p, float (&acc)[8][16], int n, float g,
+                                        int col0, bool f16) {
+  const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
+                                                  static_cast<size_t>(n) * p.K + col0);
+#pragma unroll
+  for (int b = 0; b < 16; ++b) {
+    if (col0 + 8 * b >= p.K) break;
+    const uint4 w = __ldg(h + b);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = unpack16(x[k], f16);
+      float* a = &acc[b >> 1][(b & 1) * 8 + 2 * k];
+      a[0] = fmaf(g, v.x, a[0]);
+      a[1] = fmaf(g, v.y, a[1]);
+    }
+  }
+}
+
 // OP_DW: the targets' entries of this thread's vocabulary row: each hidden row
 // whose target it is adds its entry times itself, in ascending order of the
 // rows -- one by one, or as the sum that target_sum_kernel has made of a long
@@ -426,22 +448,7 @@ __device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[
   }
   for (int i = 0; i < run.count; ++i) {
     const int n = i == 0 ? run.n : p.w.list[run.first + i];
-    const float g = i == 0 ? run.g : p.coef[n];
-    const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
-                                                    static_cast<size_t>(n) * p.K + col0);
-#pragma unroll
-    for (int b = 0; b < 16; ++b) {
-      if (col0 + 8 * b >= p.K) break;
-      const uint4 w = __ldg(h + b);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = unpack16(x[k], f16);
-        float* a = &acc[b >> 1][(b & 1) * 8 + 2 * k];
-        a[0] = fmaf(g, v.x, a[0]);
-        a[1] = fmaf(g, v.y, a[1]);
-      }
-    }
+    add_row(p, acc, n, i == 0 ? run.g : p.coef[n], col0, f16);
   }
 }
 
@@ -576,7 +583,7 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   constexpr bool kLogits = kScore || OP == OP_DZ || op_scaled(OP);     // D = h W^T
   constexpr bool kStore = op_stores(OP);               // D leaves through staging and tmO
   constexpr bool kInt = OP == OP_SCALED;               // integer sums, int32
-  constexpr bool kMnA = OP == OP_DW, kMnB = OP == OP_DH || OP == OP_DW;
+  constexpr bool kMnA = op_dw(OP), kMnB = OP == OP_DH || op_dw(OP);
   constexpr int kBoxes = kScore ? kScoreChunkK / 64 : op_scaled(OP) ? kScaledChunkBoxes : kGradChunkBoxes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -774,16 +781,29 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     using Acc = typename std::conditional<kInt, int32_t, float>::type;
     uint32_t slot = 0, sph = 0;
     bool failed = false;
+    // OP_DW: the run of the unit's targets in the list, one unit ahead.
+    // OP_DW_FEW: lane l of every warp holds the targets of rows l, l + 32, ...
     TargetRun ahead{};
+    int few[kFewRows / 32];
     if constexpr (OP == OP_DW) {
       if (pair < units) ahead.fetch(p, unit_of<OP>(p, first).a0 + half + q * 32 + lane);
+    }
+    if constexpr (OP == OP_DW_FEW) {
+#pragma unroll
+      for (int k = 0; k < kFewRows / 32; ++k) {
+        few[k] = -1;
+        if (32 * k + lane < p.B) {
+          const int v = p.w.targets[32 * k + lane];
+          if (v >= p.t_off && v - p.t_off < p.V) few[k] = v - p.t_off;
+        }
+      }
     }
     for (UnitWalk walk = first; walk.u < units; walk.next()) {
       if (skip(walk)) continue;
       const PairUnit t = unit_of<OP>(p, walk);
       const int nw0 = t.a0 + half + q * 32;    // the warp's first row of D
       const int n = nw0 + lane;                // this thread's row
-      const int rows = OP == OP_DW ? p.V : p.B;
+      const int rows = op_dw(OP) ? p.V : p.B;
       const int vb = t.b0 + g * 128;           // first column of this half
       Acc acc[8][16];
       float thr = -INFINITY;
@@ -1008,7 +1028,21 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         if (nw0 < p.B) store_f32(acc, sg, &tmO, lane, vb, p.K, row0);
       } else {
         const bool f16 = (p.idesc & (7u << 7)) == 0;
-        if (run.count > 0) add_targets(p, acc, run, vb, f16);
+        if constexpr (OP == OP_DW_FEW) {
+#pragma unroll
+          for (int k = 0; k < kFewRows / 32; ++k) {
+            const int rel = few[k] >= 0 ? few[k] - nw0 : -1;      // the warp's row it is
+            uint32_t hits = __ballot_sync(0xffffffffu, rel >= 0 && rel < 32);
+            while (hits != 0) {
+              const int src = __ffs(hits) - 1;
+              hits &= hits - 1;
+              const int row = __shfl_sync(0xffffffffu, rel, src);
+              if (lane == row) add_row(p, acc, 32 * k + src, p.coef[32 * k + src], vb, f16);
+            }
+          }
+        } else if (run.count > 0) {
+          add_targets(p, acc, run, vb, f16);
+        }
         __syncwarp();
         const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;
         if (vb < p.K && nw0 < p.V) {

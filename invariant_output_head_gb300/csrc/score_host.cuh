@@ -176,7 +176,7 @@ cudaError_t launch_pairop(detlm_head* h, const CUtensorMap& a, const CUtensorMap
   int pairs = 0;
   e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return e;
-  p.a_rows = static_cast<uint8_t>(OP == OP_DW ? kRowsHalf : a_box_rows(p.B));
+  p.a_rows = static_cast<uint8_t>(op_dw(OP) ? kRowsHalf : a_box_rows(p.B));
   p.stages = static_cast<uint8_t>(op_stages<OP>(p.a_rows));
   p.stall = static_cast<uint8_t>(h->stall);
   p.err = h->d_err;
@@ -607,38 +607,43 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       q.units = static_cast<int32_t>(n_vt * L.n_dt);
       q.K = static_cast<int32_t>(h->d);
       q.idesc = idesc | kIdescMnA | kIdescMnB;
-      TargetListParams tl;
-      tl.targets = in.targets;
-      tl.B = p.B;
-      tl.v0 = p.t_off;
-      tl.vc = p.V;
-      tl.starts = reinterpret_cast<int32_t*>(ws + L.starts);
-      tl.list = reinterpret_cast<int32_t*>(ws + L.list);
-      e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, stream, tl);
-      if (e != cudaSuccess) return status_from_cuda(e);
-      TargetSumParams ts;
-      ts.targets = in.targets;
-      ts.starts = tl.starts;
-      ts.list = tl.list;
-      ts.coef = p.coef;
-      ts.h = static_cast<const uint4*>(in.h);
-      ts.sums = reinterpret_cast<float*>(ws + L.sums);
-      ts.n_vt = static_cast<int32_t>(n_vt);
-      ts.v0 = p.t_off;
-      ts.d8 = static_cast<int32_t>(h->d / 8);
-      ts.fp16 = h->dtype == DETLM_FP16;
-      if (B > kShortRun) {
+      q.w.targets = in.targets;
+      q.w.starts = nullptr;
+      q.w.list = nullptr;
+      q.w.sums = nullptr;
+      if (B > kFewRows) {
+        TargetListParams tl;
+        tl.targets = in.targets;
+        tl.B = p.B;
+        tl.v0 = p.t_off;
+        tl.vc = p.V;
+        tl.starts = reinterpret_cast<int32_t*>(ws + L.starts);
+        tl.list = reinterpret_cast<int32_t*>(ws + L.list);
+        e = launch_dependent(target_list_kernel, static_cast<unsigned>(n_vt), 256, stream, tl);
+        if (e != cudaSuccess) return status_from_cuda(e);
+        TargetSumParams ts;
+        ts.targets = in.targets;
+        ts.starts = tl.starts;
+        ts.list = tl.list;
+        ts.coef = p.coef;
+        ts.h = static_cast<const uint4*>(in.h);
+        ts.sums = reinterpret_cast<float*>(ws + L.sums);
+        ts.n_vt = static_cast<int32_t>(n_vt);
+        ts.v0 = p.t_off;
+        ts.d8 = static_cast<int32_t>(h->d / 8);
+        ts.fp16 = h->dtype == DETLM_FP16;
         e = launch_dependent(target_sum_kernel,
                              dim3(static_cast<unsigned>(B), static_cast<unsigned>((ts.d8 + 127) / 128)),
                              128, stream, ts);
         if (e != cudaSuccess) return status_from_cuda(e);
+        q.w.starts = tl.starts;
+        q.w.list = tl.list;
+        q.w.sums = ts.sums;
       }
-      q.w.starts = tl.starts;
-      q.w.list = tl.list;
-      q.w.sums = ts.sums;
       q.w.h = in.h;
       q.w.scale = scale;
-      e = launch_pairop<OP_DW>(h, zN, hN, dwOut, q, stream);
+      e = B > kFewRows ? launch_pairop<OP_DW>(h, zN, hN, dwOut, q, stream)
+                       : launch_pairop<OP_DW_FEW>(h, zN, hN, dwOut, q, stream);
       if (e != cudaSuccess) return status_from_cuda(e);
     }
   }
