@@ -1029,16 +1029,34 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       } else {
         const bool f16 = (p.idesc & (7u << 7)) == 0;
         if constexpr (OP == OP_DW_FEW) {
+          // the warp's vocabulary rows that are targets: mostly none, which is
+          // one branch around one copy of the long code
+          constexpr int kW = kFewRows / 32;
+          uint32_t hits[kW], any = 0;
+          int rel[kW];
 #pragma unroll
-          for (int k = 0; k < kFewRows / 32; ++k) {
-            const int rel = few[k] >= 0 ? few[k] - nw0 : -1;      // the warp's row it is
-            uint32_t hits = __ballot_sync(0xffffffffu, rel >= 0 && rel < 32);
-            while (hits != 0) {
-              const int src = __ffs(hits) - 1;
-              hits &= hits - 1;
-              const int row = __shfl_sync(0xffffffffu, rel, src);
-              if (lane == row) add_row(p, acc, 32 * k + src, p.coef[32 * k + src], vb, f16);
+          for (int k = 0; k < kW; ++k) {
+            rel[k] = few[k] >= 0 ? few[k] - nw0 : -1;
+            hits[k] = __ballot_sync(0xffffffffu, rel[k] >= 0 && rel[k] < 32);
+            any |= hits[k];
+          }
+          while (any != 0) {
+            int n = 0, row = 0;
+            bool found = false;
+            any = 0;
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+              const int src = __ffs(hits[k]) - 1;
+              const int at = __shfl_sync(0xffffffffu, rel[k], src < 0 ? 0 : src);
+              if (!found && src >= 0) {          // the same in every lane
+                found = true;
+                n = 32 * k + src;
+                row = at;
+                hits[k] &= hits[k] - 1;
+              }
+              any |= hits[k];
             }
+            if (lane == row) add_row(p, acc, n, p.coef[n], vb, f16);
           }
         } else if (run.count > 0) {
           add_targets(p, acc, run, vb, f16);
