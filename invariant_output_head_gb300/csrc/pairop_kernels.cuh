@@ -73,7 +73,6 @@ constexpr int kScaledChunkBoxes = 16;    // OP_SCALED: 1024
 constexpr int kSegChunks = 8;            // gradient chunks per vocabulary segment (16384)
 constexpr int kCandFloats = 20;          // a candidate block: 16 logits, its index, padding
 constexpr int kFewRows = 128;            // OP_DW: rows whose targets a warp holds in registers
-constexpr int kShortRun = 2;             // OP_DW: hidden rows of one target added one by one
 constexpr int kRowWords = 4;             // words of a row before its slots
 enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
 
@@ -125,10 +124,9 @@ struct GradArgs {
 };
 
 struct DwArgs {
-  const int32_t* targets;   // OP_DW_FEW: [B] (and no list)
+  const int32_t* targets;   // OP_DW_FEW: [B] (and no runs)
   const int32_t* starts;    // [256 n_vt + 1] where a vocabulary entry's run in the list starts
-  const int32_t* list;      // rows of h by their target (those of this pass), then ascending
-  const float* sums;        // [list position][d] sums of the runs longer than kShortRun
+  const float* sums;        // [list position][d]: the sum of the run that starts there
   const void* h;            // [B][d]
   const float* scale;       // as above
 };
@@ -387,25 +385,7 @@ __device__ __forceinline__ Stat score_tail(const PairOpParams& p, const float (&
   return st;
 }
 
-// OP_DW: the hidden rows whose target is this thread's vocabulary row; fetched
-// one unit ahead of their use (three dependent loads would otherwise stand at
-// the end of every unit that has one).
-struct TargetRun {
-  int first, count, n;      // run in the list; its first row
-  float g;                  // and that row's entry
-  __device__ __forceinline__ void fetch(const PairOpParams& p, int v) {
-    first = p.w.starts[v];
-    count = p.w.starts[v + 1] - first;
-    n = 0;
-    g = 0.0f;
-    if (count > 0) {
-      n = p.w.list[first];
-      g = p.coef[n];
-    }
-  }
-};
-
-// acc += g h[n][col0 ..], 128 columns or up to d (a multiple of 8).
+// OP_DW_FEW: acc += g h[n][col0 ..], 128 columns or up to d (a multiple of 8).
 __device__ __forceinline__ void add_row(const PairOpParams& p, float (&acc)[8][16], int n, float g,
                                         int col0, bool f16) {
   const uint4* h = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w.h) +
@@ -425,30 +405,54 @@ __device__ __forceinline__ void add_row(const PairOpParams& p, float (&acc)[8][1
   }
 }
 
-// OP_DW: the targets' entries of this thread's vocabulary row: each hidden row
-// whose target it is adds its entry times itself, in ascending order of the
-// rows -- one by one, or as the sum that target_sum_kernel has made of a long
-// run (a frequent token), so that no thread walks one.
-__device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[8][16],
-                                            const TargetRun& run, int col0, bool f16) {
-  if (run.count > kShortRun) {
-    const float4* x =
-        reinterpret_cast<const float4*>(p.w.sums + static_cast<size_t>(run.first) * p.K + col0);
+// OP_DW: the targets' entries of the warp's 32 vocabulary rows. The hidden rows
+// of one target have been summed (target_sum_kernel: coef_n h[n], ascending,
+// so a frequent token costs no thread a walk); `first` is the sum of this
+// lane's row, or -1. The warp fetches the sums row by row, through the staging
+// buffers (16 rows of 512 bytes, 16-byte chunks swizzled by the row), and
+// every lane adds its own.
+__device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[8][16], Staging& sg,
+                                            int first, int col0, int lane) {
+  const uint32_t hits = __ballot_sync(0xffffffffu, first >= 0);
+  if (hits == 0) return;
+  const bool in = col0 + 4 * lane < p.K;       // d is a multiple of 8
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t left = (hits >> (16 * h)) & 0xFFFFu;
+    if (left == 0) continue;
+    sg.claim(lane);                            // (a warp barrier: earlier reads are done)
+    while (left != 0) {
+      float4 x[4];
+      int row[4];
 #pragma unroll
-    for (int b = 0; b < 32; ++b) {
-      if (col0 + 4 * b >= p.K) break;        // d is a multiple of 8
-      const float4 v = x[b];
-      float* a = &acc[b >> 2][4 * (b & 3)];
-      a[0] += v.x;
-      a[1] += v.y;
-      a[2] += v.z;
-      a[3] += v.w;
+      for (int j = 0; j < 4; ++j) {
+        row[j] = left != 0 ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+        const int f = __shfl_sync(0xffffffffu, first, 16 * h + (row[j] & 15));
+        if (row[j] >= 0 && in)
+          x[j] = __ldg(reinterpret_cast<const float4*>(p.w.sums + static_cast<size_t>(f) * p.K + col0) +
+                       lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (row[j] >= 0 && in)
+          *reinterpret_cast<float4*>(sg.xs + row[j] * 512 + 16 * (lane ^ (row[j] & 7))) = x[j];
     }
-    return;
-  }
-  for (int i = 0; i < run.count; ++i) {
-    const int n = i == 0 ? run.n : p.w.list[run.first + i];
-    add_row(p, acc, n, i == 0 ? run.g : p.coef[n], col0, f16);
+    __syncwarp();
+    if ((lane >> 4) == h && first >= 0) {
+      const int r = lane & 15;
+#pragma unroll
+      for (int b = 0; b < 32; ++b) {
+        if (col0 + 4 * b >= p.K) break;
+        const float4 v = *reinterpret_cast<const float4*>(sg.xs + r * 512 + 16 * (b ^ (r & 7)));
+        float* a = &acc[b >> 2][4 * (b & 3)];
+        a[0] += v.x;
+        a[1] += v.y;
+        a[2] += v.z;
+        a[3] += v.w;
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -781,13 +785,8 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     using Acc = typename std::conditional<kInt, int32_t, float>::type;
     uint32_t slot = 0, sph = 0;
     bool failed = false;
-    // OP_DW: the run of the unit's targets in the list, one unit ahead.
     // OP_DW_FEW: lane l of every warp holds the targets of rows l, l + 32, ...
-    TargetRun ahead{};
     int few[kFewRows / 32];
-    if constexpr (OP == OP_DW) {
-      if (pair < units) ahead.fetch(p, unit_of<OP>(p, first).a0 + half + q * 32 + lane);
-    }
     if constexpr (OP == OP_DW_FEW) {
 #pragma unroll
       for (int k = 0; k < kFewRows / 32; ++k) {
@@ -818,12 +817,10 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         }
         __syncwarp();
       }
-      TargetRun run{};                         // OP_DW: this row's targets
+      int run0 = 0, run1 = 0;                  // OP_DW: this row's run in the list
       if constexpr (OP == OP_DW) {
-        run = ahead;
-        UnitWalk w2 = walk;
-        w2.next();
-        if (w2.u < units) ahead.fetch(p, unit_of<OP>(p, w2).a0 + half + q * 32 + lane);
+        run0 = p.w.starts[n];
+        run1 = p.w.starts[n + 1];
       }
       const int n_chunks = (t.nkb + kBoxes - 1) / kBoxes;
       for (int c = 0; c < n_chunks; ++c) {
@@ -1058,8 +1055,8 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if (lane == row) add_row(p, acc, n, p.coef[n], vb, f16);
           }
-        } else if (run.count > 0) {
-          add_targets(p, acc, run, vb, f16);
+        } else {
+          add_targets(p, acc, sg, run1 > run0 ? run0 : -1, vb, lane);
         }
         __syncwarp();
         const float s = p.w.scale != nullptr ? p.w.scale[1] : 1.0f;

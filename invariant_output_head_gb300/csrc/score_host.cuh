@@ -10,10 +10,13 @@ namespace {
 // the int8-streaming kernel converts W again for every 64.
 constexpr int64_t kI8ScaledWideB = 65;
 constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
-// Up to this many rows the wide projection writes its logits (OP_SCOREZ):
-// with few row tiles most of the vocabulary is under way before a threshold
-// can thin the candidates out.
+// The wide projection writes its logits (OP_SCOREZ) where candidates do not
+// pay: up to kLogitRows rows, or in at most kLogitRounds units a pair -- a large
+// part of the vocabulary is then under way before a threshold can thin the
+// candidates out. (1024 x 151936 x 1536, K = 8: 342 us, with candidates 366;
+// 4098 x 1352 x 384, K = 5: see the table; 2048 x 151936 x 1536: candidates.)
 constexpr int64_t kLogitRows = 1024;
+constexpr int64_t kLogitRounds = 8;
 constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
 
 // 2-D tensor map of 16-bit or 32-bit elements: `inner` contiguous, rows of
@@ -232,7 +235,14 @@ struct ScoreLayout {
 // Up to kLogitRows rows: logits [B][ld] and records [3][B][n_vt] (without
 // alternatives only the narrow ones need logits). More: records, target
 // logits, row words and tile marks (cleared together), candidates.
-bool score_has_logits(int64_t B, int K) { return B <= kNarrowRows || (K > 0 && B <= kLogitRows); }
+// The most rows whose calls do that.
+int64_t logit_rows(const detlm_head* h, int pairs) {
+  const int64_t rows = kLogitRounds * pairs / tiles256(h->V) * kRowsM;
+  return rows > kLogitRows ? rows : kLogitRows;
+}
+bool score_has_logits(const detlm_head* h, int64_t B, int K, int pairs) {
+  return B <= kNarrowRows || (K > 0 && B <= logit_rows(h, pairs));
+}
 
 ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
   ScoreLayout L;
@@ -248,7 +258,7 @@ ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
   L.rec_part = round256(static_cast<size_t>(B) * L.n_vt * 4) / 4;
   L.rec = part(3 * L.rec_part * 4);
   if (!narrow && needs_padding(h)) L.rows = part(static_cast<size_t>(B) * padded_d(h) * 2);
-  if (score_has_logits(B, K)) {
+  if (score_has_logits(h, B, K, pairs)) {
     L.ld = narrow ? h->V : (h->V + 31) / 32 * 32;
     L.logits = part(static_cast<size_t>(B) * L.ld * 4);
   } else {
@@ -398,7 +408,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   p.s.words = reinterpret_cast<int32_t*>(ws + L.words);
   ScoreMergeParams mp;
   score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
-  if (score_has_logits(B, K)) {
+  if (score_has_logits(h, B, K, pairs)) {
     CUtensorMap zOut;
     if (!encode_box(&zOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.logits, L.ld, B, L.ld * 4, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_128B, false))
@@ -609,7 +619,6 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
       q.idesc = idesc | kIdescMnA | kIdescMnB;
       q.w.targets = in.targets;
       q.w.starts = nullptr;
-      q.w.list = nullptr;
       q.w.sums = nullptr;
       if (B > kFewRows) {
         TargetListParams tl;
@@ -637,7 +646,6 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
                              128, stream, ts);
         if (e != cudaSuccess) return status_from_cuda(e);
         q.w.starts = tl.starts;
-        q.w.list = tl.list;
         q.w.sums = ts.sums;
       }
       q.w.h = in.h;
@@ -693,7 +701,7 @@ int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
   if (e != cudaSuccess) return status_from_cuda(e);
   // each kind of call's workspace grows with its rows
   size_t need = 0;
-  for (const int64_t most : {static_cast<int64_t>(kNarrowRows), kLogitRows, max_B}) {
+  for (const int64_t most : {static_cast<int64_t>(kNarrowRows), logit_rows(h, pairs), max_B}) {
     const size_t n = score_layout(h, most < max_B ? most : max_B, top_k, pairs).total;
     if (n > need) need = n;
   }

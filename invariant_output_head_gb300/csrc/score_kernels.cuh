@@ -458,95 +458,118 @@ grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targ
 
 // The hidden rows by their target: list holds the rows whose target lies in
 // [v0, v0 + vc), by target, then ascending; starts[v] is where entry v's run
-// begins. Block t does the 256 entries of tile t: it counts the targets of
-// lower tiles and of each of its own entries, then places its rows in order.
-// Every block reads all B targets (from L2).
+// begins. Block t does the 256 entries of tile t: its threads count, each over
+// an ascending share of the rows, the targets of lower tiles and of each of
+// its own entries; gather its own rows in order; and then thread e picks entry
+// e's rows out of them. Every block reads all B targets (from L2).
 struct TargetListParams {
   const int32_t* targets;
   int32_t B, v0, vc;
   int32_t* starts;          // [256 n_vt + 1]
   int32_t* list;            // [B]
 };
+constexpr int kListWindow = 4096;    // rows of a tile gathered at a time
 
 __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams p) {
-  __shared__ int sums[8];
-  __shared__ int at[256];   // counts of the tile's entries, then their next places
+  __shared__ int sums[2][8];
+  __shared__ int count[256];
+  __shared__ int rows[kListWindow];
+  __shared__ __align__(16) uint8_t entries[kListWindow];
   grid_dep_launch();
-  grid_dep_wait();
   const int tile = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  at[threadIdx.x] = 0;
+  count[threadIdx.x] = 0;
   __syncthreads();
+  grid_dep_wait();
+  const int share = (p.B + 255) / 256;
+  const int n0 = min(p.B, static_cast<int>(threadIdx.x) * share), n1 = min(p.B, n0 + share);
   // the entry of row n's target within this pass, or -1
   auto entry = [&](int n) {
-    const int32_t t = n < p.B ? p.targets[n] : -1;
+    const int32_t t = p.targets[n];
     return t >= p.v0 && t - p.v0 < p.vc ? t - p.v0 : -1;
   };
-  int less = 0;
-#pragma unroll 4
-  for (int n = threadIdx.x; n < p.B; n += 256) {
+  int less = 0, mine = 0;
+#pragma unroll 8
+  for (int n = n0; n < n1; ++n) {
     const int v = entry(n);
-    if (v < 0) continue;
-    if ((v >> 8) < tile) ++less;
-    else if ((v >> 8) == tile) atomicAdd(&at[v & 255], 1);
+    less += v >= 0 && (v >> 8) < tile;
+    if (v >= 0 && (v >> 8) == tile) {
+      ++mine;
+      atomicAdd(&count[v & 255], 1);
+    }
   }
-  less = __reduce_add_sync(0xffffffffu, less);
-  if (lane == 0) sums[warp] = less;
-  __syncthreads();
-  less = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) less += sums[w];
-  // exclusive scan of the 256 counts
-  const int mine = at[threadIdx.x];
+  // exclusive scans over the block: of the shares' rows, of the entries' counts
   int scan = mine;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, scan, s);
     if (lane >= s) scan += x;
   }
+  less = __reduce_add_sync(0xffffffffu, less);
+  if (lane == 31) sums[0][warp] = scan;
+  if (lane == 0) sums[1][warp] = less;
   __syncthreads();
-  if (lane == 31) sums[warp] = scan;
-  __syncthreads();
-  int before = less, all = 0;
+  int before = 0, all = 0;
+  less = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    before += w < warp ? sums[w] : 0;
-    all += sums[w];
+    before += w < warp ? sums[0][w] : 0;
+    all += sums[0][w];
+    less += sums[1][w];
   }
-  const int start = before + scan - mine;
-  p.starts[tile * 256 + threadIdx.x] = start;
-  if (tile == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 255) p.starts[tile * 256 + 256] = less + all;
-  if (all == 0) return;
-  at[threadIdx.x] = start;
+  const int place = before + scan - mine;              // this share's first row in the tile
+  const int own = count[threadIdx.x];
+  scan = own;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, scan, s);
+    if (lane >= s) scan += x;
+  }
   __syncthreads();
-  // place the rows in ascending order: one warp's 32 rows after another's
-  for (int n0 = 0; n0 < p.B; n0 += 256) {
-    const int n = n0 + threadIdx.x;
-    const int v = entry(n);
-    const bool hit = v >= 0 && (v >> 8) == tile;
-    const int any = __syncthreads_or(hit);
-    if (!any) continue;
-    for (int w = 0; w < 8; ++w) {
-      if (w == warp) {
-        const uint32_t same = __match_any_sync(0xffffffffu, hit ? (v & 255) : -1);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        int place = 0;
-        if (hit) place = at[v & 255];
-        __syncwarp();
-        if (hit) {
-          p.list[place + rank] = n;
-          if (rank == 0) at[v & 255] = place + __popc(same);
+  if (lane == 31) sums[0][warp] = scan;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) before += w < warp ? sums[0][w] : 0;
+  int at = less + before + scan - own;
+  p.starts[tile * 256 + threadIdx.x] = at;
+  if (tile == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 255) p.starts[tile * 256 + 256] = less + all;
+  for (int w0 = 0; w0 < all; w0 += kListWindow) {
+    if (mine > 0) {
+      int i = place - w0;
+      for (int n = n0; n < n1; ++n) {
+        const int v = entry(n);
+        if (v < 0 || (v >> 8) != tile) continue;
+        if (i >= 0 && i < kListWindow) {
+          rows[i] = n;
+          entries[i] = static_cast<uint8_t>(v);
+        }
+        ++i;
+      }
+    }
+    __syncthreads();
+    const int here = min(kListWindow, all - w0);
+    const uint32_t me = threadIdx.x * 0x01010101u;
+    for (int i = 0; i < here; i += 16) {               // 16 entries a load
+      const uint4 e = *reinterpret_cast<const uint4*>(entries + i);
+      const uint32_t x[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t eq = __vcmpeq4(x[k], me);
+        while (eq != 0) {
+          const int j = (__ffs(eq) - 1) >> 3;
+          eq &= ~(0xFFu << (8 * j));
+          if (i + 4 * k + j < here) p.list[at++] = rows[i + 4 * k + j];
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
 }
 
-// The sums of the long runs of the list (a target of more than kShortRun
-// rows): sums[first][k] = sum coef_n h[n][k], fp32, rows in ascending order.
-// Block (i, j): the run that starts at list position i, if one does, columns
-// 1024 j on, eight a thread.
+// The sums of the list's runs: sums[first][k] = sum coef_n h[n][k], fp32, rows
+// in ascending order. Block (i, j): the run that starts at list position i, if
+// one does, columns 1024 j on, eight a thread.
 struct TargetSumParams {
   const int32_t* targets;
   const int32_t* starts;
@@ -564,7 +587,7 @@ __global__ void __launch_bounds__(128) target_sum_kernel(const TargetSumParams p
   if (i >= p.starts[p.n_vt * 256]) return;
   const int v = p.targets[p.list[i]] - p.v0;
   const int first = p.starts[v], end = p.starts[v + 1];
-  if (first != i || end - first <= kShortRun) return;
+  if (first != i) return;
   const int c = blockIdx.y * 128 + threadIdx.x;
   if (c >= p.d8) return;
   float a[8] = {};
@@ -630,6 +653,17 @@ __global__ void __launch_bounds__(256) grad_fold_kernel(const FoldParams p) {
   const int64_t step = p.rows_pad * p.d4;               // float4 per partial
   const float4* src = reinterpret_cast<const float4*>(p.part) + i;
   float4* run = reinterpret_cast<float4*>(p.acc) + i;
+  // the target's row of W is on its way while the partials are added
+  const int n = static_cast<int>(i / p.d4), c = static_cast<int>(i - static_cast<int64_t>(n) * p.d4);
+  float g = 0.0f;
+  uint2 w = make_uint2(0, 0);
+  if (p.last) {
+    const int tg = p.targets[n];
+    if (tg >= 0 && tg < p.V) {
+      g = p.coef[n];
+      w = reinterpret_cast<const uint2*>(p.W)[static_cast<size_t>(tg) * p.d4 + c];
+    }
+  }
   float4 a = p.first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *run;
   auto add = [](float4& x, const float4& y) {
     x.x = __fadd_rn(x.x, y.x);
@@ -660,11 +694,7 @@ __global__ void __launch_bounds__(256) grad_fold_kernel(const FoldParams p) {
   }
   const float s = p.scale != nullptr ? p.scale[1] : 1.0f;
   const bool f16 = p.fp16 != 0;
-  const int n = static_cast<int>(i / p.d4), c = static_cast<int>(i - static_cast<int64_t>(n) * p.d4);
-  const int tg = p.targets[n];
-  if (tg >= 0 && tg < p.V) {
-    const float g = p.coef[n];
-    const uint2 w = reinterpret_cast<const uint2*>(p.W)[static_cast<size_t>(tg) * p.d4 + c];
+  if (g != 0.0f) {
     const float2 lo = unpack16(w.x, f16), hi = unpack16(w.y, f16);
     a.x = fmaf(g, lo.x, a.x);
     a.y = fmaf(g, lo.y, a.y);
