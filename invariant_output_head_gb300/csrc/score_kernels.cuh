@@ -460,8 +460,8 @@ grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targ
 // [v0, v0 + vc), by target, then ascending; starts[v] is where entry v's run
 // begins. Block t does the 256 entries of tile t: its threads count, each over
 // an ascending share of the rows, the targets of lower tiles and of each of
-// its own entries; gather its own rows in order; and then thread e picks entry
-// e's rows out of them. Every block reads all B targets (from L2).
+// its own entries; gather its own rows in order; and place them by entry.
+// Every block reads all B targets (from L2).
 struct TargetListParams {
   const int32_t* targets;
   int32_t B, v0, vc;
@@ -472,9 +472,9 @@ constexpr int kListWindow = 4096;    // rows of a tile gathered at a time
 
 __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams p) {
   __shared__ int sums[2][8];
-  __shared__ int count[256];
+  __shared__ int count[256];           // of the tile's entries
   __shared__ int rows[kListWindow];
-  __shared__ __align__(16) uint8_t entries[kListWindow];
+  __shared__ uint8_t entries[kListWindow];
   grid_dep_launch();
   const int tile = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -531,8 +531,9 @@ __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams
   before = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) before += w < warp ? sums[0][w] : 0;
-  int at = less + before + scan - own;
-  p.starts[tile * 256 + threadIdx.x] = at;
+  const int start = less + before + scan - own;
+  p.starts[tile * 256 + threadIdx.x] = start;
+  count[threadIdx.x] = start;                          // from here on: the entry's next place
   if (tile == static_cast<int>(gridDim.x) - 1 && threadIdx.x == 255) p.starts[tile * 256 + 256] = less + all;
   for (int w0 = 0; w0 < all; w0 += kListWindow) {
     if (mine > 0) {
@@ -548,19 +549,23 @@ __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams
       }
     }
     __syncthreads();
+    // one warp places them, 32 at a time in order (a barrier per step would
+    // cost more than the other warps bring)
     const int here = min(kListWindow, all - w0);
-    const uint32_t me = threadIdx.x * 0x01010101u;
-    for (int i = 0; i < here; i += 16) {               // 16 entries a load
-      const uint4 e = *reinterpret_cast<const uint4*>(entries + i);
-      const uint32_t x[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t eq = __vcmpeq4(x[k], me);
-        while (eq != 0) {
-          const int j = (__ffs(eq) - 1) >> 3;
-          eq &= ~(0xFFu << (8 * j));
-          if (i + 4 * k + j < here) p.list[at++] = rows[i + 4 * k + j];
+    if (warp == 0) {
+      for (int i0 = 0; i0 < here; i0 += 32) {
+        const bool in = i0 + lane < here;
+        const int e = in ? entries[i0 + lane] : 256 + lane;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int to = 0;
+        if (in) {
+          to = count[e];
+          p.list[to + rank] = rows[i0 + lane];
         }
+        __syncwarp();
+        if (in && rank == 0) count[e] = to + __popc(same);
+        __syncwarp();
       }
     }
     __syncthreads();
