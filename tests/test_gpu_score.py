@@ -41,6 +41,8 @@ def _check_score(got, want, K, T):
     (5001, 264, 1, 20, 0.7, "bf16"), (5001, 264, 300, 20, 0.7, "fp16"),
     (32000, 128, 3, 32, 1.0, "bf16"), (32000, 128, 513, 32, 1.0, "bf16"),
     (50001, 64, 260, 1, 1.3, "fp16"), (70000, 8, 129, 13, 1.0, "bf16"),
+    (1352, 384, 1300, 5, 1.0, "bf16"), (20000, 64, 1100, 32, 1.0, "bf16"),
+    (60000, 24, 1050, 8, 1.0, "fp16"), (9000, 40, 1500, 0, 0.8, "bf16"),
 ])
 def test_score(V, d, B, K, T, dtype):
     torch = _torch()
@@ -65,15 +67,15 @@ def test_score_without_targets_or_alternatives(B):
 
 def test_row_bits_do_not_depend_on_the_batch():
     torch = _torch()
-    W, h, t = ref.grid_inputs(5, 9001, 328, 700)
+    W, h, t = ref.grid_inputs(5, 9001, 328, 5200)
     head = _head(W, "bf16")
     # off-grid values too: the sums' rounding must not depend on B either
-    noise = torch.randn(700, 328, generator=torch.Generator().manual_seed(1)).cuda()
+    noise = torch.randn(5200, 328, generator=torch.Generator().manual_seed(1)).cuda()
     hd = (ref.to_dev(h, "bf16").float() + noise).bfloat16()
     td = torch.from_numpy(t).cuda()
     full = head.score(hd, td, top_k=9, temperature=0.9)
     for rows in ([0], [5, 699], list(range(100, 117)), list(range(31, 159)),
-                 list(range(300, 429)), list(range(690, 100, -1))):
+                 list(range(300, 429)), list(range(690, 100, -1)), list(range(5000, 900, -2))):
         i = torch.tensor(rows, device="cuda")
         part = head.score(hd[i].contiguous(), td[i].contiguous(), top_k=9, temperature=0.9)
         for a, b in zip(full, part):
@@ -81,7 +83,7 @@ def test_row_bits_do_not_depend_on_the_batch():
     assert head.check() == 0
 
 
-@pytest.mark.parametrize("B", [4, 300])
+@pytest.mark.parametrize("B", [4, 300, 1100])
 def test_equal_and_ordered_logits(B):
     """Rows that admit every block as a candidate: all logits equal (a zero
     row), rising, and falling along the vocabulary."""
@@ -257,6 +259,38 @@ def test_gradient_of_masked_and_shared_targets():
     assert (dh == 0).all() and (dW == 0).all()
     dh, dW = head.score_backward(hd[:0], td[:0], s.lse[:0], s.entropy[:0], dl[:0], de[:0])
     assert dh.shape == (0, d) and (dW == 0).all()
+
+
+def test_gradient_in_several_passes_over_the_vocabulary():
+    """More rows than one pass's dz holds (about 8 GB): a row's dh is the bits
+    of a call of few rows, and dW is that of two half batches added."""
+    torch = _torch()
+    from invariant_output_head_gb300 import Head
+    V, d, B = 140001, 16, 40000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn(V, d, generator=g, device="cuda").bfloat16()
+    h = torch.randn(B, d, generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, V, (B,), generator=g, device="cuda", dtype=torch.int32)
+    t[::7] = 139999                               # a frequent token, in the last pass
+    dl = torch.randn(B, generator=g, device="cuda") / B
+    head = Head(W)
+    s = head.score(h, t)
+    dh, dW = head.score_backward(h, t, s.lse, s.entropy, dl)
+    halves = []
+    for i in (slice(0, B // 2), slice(B // 2, B)):
+        part = head.score_backward(h[i].contiguous(), t[i].contiguous(), s.lse[i].contiguous(),
+                                   s.entropy[i].contiguous(), dl[i].contiguous())
+        assert torch.equal(part[0], dh[i])
+        halves.append(part[1].float())
+    few = head.score_backward(h[:3].contiguous(), t[:3].contiguous(), s.lse[:3].contiguous(),
+                              s.entropy[:3].contiguous(), dl[:3].contiguous())
+    assert torch.equal(few[0], dh[:3])
+    # each half and the whole are rounded once to bf16 (2^-8 of themselves at
+    # most), and their fp32 sums differ by 1e-5 of the halves' magnitudes
+    a, b = halves
+    tol = 2.0 ** -8 * (a.abs() + b.abs() + dW.float().abs()) * 1.01 + 1e-9
+    assert ((dW.float() - (a + b)).abs() <= tol).all()
+    assert head.check() == 0
 
 
 # ------------------------------------------------------------ scaled logits
@@ -440,3 +474,44 @@ def test_weights_changed():
     want = (q.float() @ W8.float().t())
     assert torch.equal(head.scaled_logits(q, sx, sw), want)
     assert torch.equal(head.scaled_logits(q[:4].contiguous(), sx[:4].contiguous(), sw), want[:4])
+    # a 16-bit head whose rows are padded (d % 16 == 8)
+    W, h, t = ref.grid_inputs(41, 900, 24, 200)
+    Wd, hd, td = ref.to_dev(W, "bf16"), ref.to_dev(h, "bf16"), torch.from_numpy(t).cuda()
+    head = Head(Wd)
+    for B in (5, 200):
+        head.score(hd[:B].contiguous(), td[:B].contiguous(), top_k=3)
+    Wd.neg_()
+    head.weights_changed()
+    for B in (5, 200):
+        got = head.score(hd[:B].contiguous(), td[:B].contiguous(), top_k=3)
+        _check_score(got, ref.score(-W, h[:B], t[:B], 3, 1.0), 3, 1.0)
+
+
+def test_differentiable_score():
+    """The autograd function against the call it is made of, and the example
+    that runs the operators together."""
+    torch = _torch()
+    from invariant_output_head_gb300 import Head
+    from invariant_output_head_gb300.training import scored_logprobs
+    W, h, t = ref.grid_inputs(12, 800, 72, 60, masked=0.1)
+    Wd = ref.to_dev(W, "bf16").requires_grad_()
+    hd = ref.to_dev(h, "bf16").requires_grad_()
+    td = torch.from_numpy(t).cuda()
+    head = Head(Wd)
+    logp, entropy = scored_logprobs(head, hd, td, 0.9)
+    a, b = torch.randn(60, device="cuda"), torch.randn(60, device="cuda")
+    ((a * logp).sum() + (b * entropy).sum()).backward()
+    s = head.score(hd.detach(), td, temperature=0.9)
+    assert torch.equal(s.logp, logp.detach()) and torch.equal(s.entropy, entropy.detach())
+    dh, dW = head.score_backward(hd.detach(), td, s.lse, s.entropy, a, b, temperature=0.9)
+    assert torch.equal(hd.grad, dh) and torch.equal(Wd.grad, dW)
+    hd.grad = None
+    logp, _ = scored_logprobs(head, hd, td)                  # only logp, only h
+    (dh_only,) = torch.autograd.grad(logp.sum(), hd)
+    s = head.score(hd.detach(), td)
+    dh, _ = head.score_backward(hd.detach(), td, s.lse, s.entropy, torch.ones(60, device="cuda"),
+                                torch.zeros(60, device="cuda"), need_dW=False)
+    assert torch.equal(dh_only, dh)
+    from examples.policy_step import main
+    band, values = main(rows=200, vocab=3000, dim=256, say=lambda *_: None)
+    assert band <= 0.2 and values[1] > values[0]
