@@ -24,6 +24,7 @@
 #include "pair_kernels.cuh"
 #include "shard_kernels.cuh"
 #include "int8_rows_kernel.cuh"
+#include "int8_regs_kernel.cuh"
 #include "pairop_kernels.cuh"
 #include "score_kernels.cuh"
 

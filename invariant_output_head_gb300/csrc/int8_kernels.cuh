@@ -481,22 +481,28 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       if constexpr (SCALED) {
         // a warp writes 32 consecutive entries of one row at a time; nothing
         // is shared between warps, so the next unit needs no barrier
-        const float sw = vok ? p.w_scale[v] : 0.0f;
-        void* out = p.logits;
+        if (vok) {
+          const float sw = p.w_scale[v];
+          const size_t at = static_cast<size_t>(n0) * p.V + v;
+          const int rows = p.B - n0;             // columns of the unit that exist
+          auto scaled = [&](int c) {
+            return __fmul_rn(__int2float_rn(acc[c >> 4][c & 15]), __fmul_rn(__ldg(p.x_scale + n0 + c), sw));
+          };
+          if (p.out_type == OUT_F32) {
+            float* o = reinterpret_cast<float*>(p.logits) + at;
 #pragma unroll
-        for (int bb = 0; bb < N / 16; ++bb) {
-          if (n0 + bb * 16 >= p.B) break;
-          float sx[16];
+            for (int c = 0; c < N; ++c, o += p.V)
+              if (c < rows) *o = scaled(c);
+          } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(p.logits) + at;
+            const bool f16 = p.out_type == OUT_FP16;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sx[i] = n0 + bb * 16 + i < p.B ? __ldg(p.x_scale + n0 + bb * 16 + i) : 0.0f;
-          if (!vok) continue;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int n = n0 + bb * 16 + i;
-            if (n < p.B)
-              store_scaled(out, static_cast<size_t>(n) * p.V + v,
-                           __fmul_rn(__int2float_rn(acc[bb][i]), __fmul_rn(sx[i], sw)), p.out_type);
+            for (int c = 0; c < N; ++c, o += p.V)
+              if (c < rows) {
+                const float y = scaled(c);
+                *o = f16 ? __half_as_ushort(__float2half_rn(y))
+                         : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+              }
           }
         }
       } else {

@@ -678,6 +678,33 @@ cudaError_t launch_int8_rows(const detlm_head* h, const Int8RowsParams& p, cudaS
   return cudaLaunchKernelEx(&cfg, int8_rows_kernel<NB>, p);
 }
 
+// Shares of K of the register-streaming kernel: at least four steps each (or
+// one share), at most sixteen (exact fp32 sums).
+int int8_regs_shares(int steps) {
+  int wk = 1;
+  while (wk < 16 && steps >= 8 * wk) wk *= 2;
+  return wk;
+}
+
+cudaError_t launch_int8_regs(const detlm_head* h, const Int8RegsParams& p, cudaStream_t stream) {
+  cudaError_t e = prepare_kernel<int8_regs_kernel>(0);
+  if (e != cudaSuccess) return e;
+  const int rows = 32 * (16 / p.wk);
+  const int64_t rounds = (h->V + rows - 1) / rows;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(rounds < h->num_sms ? rounds : h->num_sms));
+  cfg.blockDim = dim3(kI8RegsThreads);
+  cfg.dynamicSmemBytes = int8_regs_smem(p.steps, p.wk);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, int8_regs_kernel, p);
+}
+
 bool bad_temperature(float t) { return !(t > 0.0f) || !std::isfinite(t) || !std::isfinite(1.0f / t); }
 
 }  // namespace
@@ -808,6 +835,24 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
     e = B == 1   ? launch_int8_rows<1>(h, p, stream)
         : B == 2 ? launch_int8_rows<2>(h, p, stream)
                  : launch_int8_rows<4>(h, p, stream);
+    time_stop(h, stream);
+    return status_from_cuda(e);
+  }
+  if (B <= kI8RegsMax) {
+    Int8RegsParams p;
+    p.W = static_cast<const int8_t*>(h->W);
+    p.q = q_dev;
+    p.x_scale = x_scale_dev;
+    p.w_scale = w_scale_dev;
+    p.out = out_dev;
+    p.V = static_cast<int32_t>(h->V);
+    p.d = static_cast<int32_t>(h->d);
+    p.B = static_cast<int32_t>(B);
+    p.type = type;
+    p.steps = static_cast<int32_t>((h->d + 63) / 64);
+    p.wk = int8_regs_shares(p.steps);
+    time_start(h, stream);
+    e = launch_int8_regs(h, p, stream);
     time_stop(h, stream);
     return status_from_cuda(e);
   }

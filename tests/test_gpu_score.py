@@ -294,7 +294,8 @@ def test_gradient_in_several_passes_over_the_vocabulary():
 
 
 # ------------------------------------------------------------ scaled logits
-@pytest.mark.parametrize("V,d,B", [(1, 16, 1), (130, 32, 5), (1000, 1040, 33), (1001, 272, 64),
+@pytest.mark.parametrize("V,d,B", [(1, 16, 1), (130, 32, 5), (3, 2048, 8), (5001, 4112, 7),
+                                   (1000, 16384, 6), (1001, 16384, 4), (257, 528, 3), (2000, 64, 2), (1000, 1040, 33), (1001, 272, 64),
                                    (5001, 512, 200), (5000, 512, 256), (5001, 2064, 300),
                                    (4996, 512, 700)])
 @pytest.mark.parametrize("out", ["float32", "bfloat16", "float16"])
@@ -315,6 +316,22 @@ def test_scaled_logits(V, d, B, out):
     y = acc * (sx[:, None] * sw[None, :])                                      # fp32, one each
     want = torch.from_numpy(y).to(getattr(torch, out))
     assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("B", [1, 3, 8, 20, 70, 300])
+def test_scaled_logits_of_the_largest_sums(B):
+    """All values -128 at the largest d: partial sums reach 2^24 in every
+    kernel's chunks, the whole sum 2^28."""
+    torch = _torch()
+    from invariant_output_head_gb300 import Head
+    V, d = 300, 16384
+    W = torch.full((V, d), -128, dtype=torch.int8, device="cuda")
+    W[1::3] = 127
+    W[2::3, ::2] = 127
+    q = torch.full((B, d), -128, dtype=torch.int8, device="cuda")
+    got = Head(W).scaled_logits(q, torch.ones(B, device="cuda"), torch.ones(V, device="cuda"))
+    want = (q.double() @ W.double().t()).float()
+    assert torch.equal(got, want)
 
 
 def test_scaled_logits_with_the_integer_front_end():
@@ -448,7 +465,8 @@ def test_a_wait_that_runs_out_is_reported():
                      (head, lambda: head.score(hd[:5].contiguous(), td[:5].contiguous(), top_k=4)),
                      (head, lambda: head.score_backward(hd, td, want.lse, want.entropy, dl)),
                      (h8, lambda: h8.scaled_logits(q, sx, sw)),
-                     (h8, lambda: h8.scaled_logits(q[:5].contiguous(), sx[:5].contiguous(), sw))):
+                     # (calls of up to 8 rows have no wait that could run out)
+                     (h8, lambda: h8.scaled_logits(q[:40].contiguous(), sx[:40].contiguous(), sw))):
         detlm_head_debug(hh.handle, DETLM_DEBUG_STALL, 20_000_000)
         call()
         assert hh.check() == DETLM_ETIMEOUT
