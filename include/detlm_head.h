@@ -286,8 +286,11 @@ int detlm_head_logprob_host_async(detlm_head_t* head, const void* h_host,
  *
  * temperature T: finite and > 0. 0 <= top_k <= min(DETLM_MAX_TOP, V).
  * A row of NaN or infinite logits gives NaN.
- * The logits are those of the other calls, and every sum runs in an order set
- * by V alone, so a row's outputs are the same bits for any B and any co-rows.
+ * The logits are accumulated in K chunks of 512 elements (the other calls: of
+ * 128), so they can differ from those in the last bits, and alternatives that
+ * close can rank differently from the greedy call's token. Every sum runs in
+ * an order set by V and d alone: a row's outputs are the same bits for any B
+ * and any co-rows.
  * "batch-logprob-gap": the trainer's per-token log-probability; "Inference
  * and Decoding", section 3, Temperature. B == 0 is a no-op; h_dev 16-byte
  * aligned, the other arrays 4-byte aligned. */
