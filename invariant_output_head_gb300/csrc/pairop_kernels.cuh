@@ -52,10 +52,27 @@
 // atom (the descriptor's stride offset), the next 64 free elements start 8 KB
 // on (its leading offset), and a K = 16 step is 16 rows = 2048 bytes.
 //
-// What bounds them: the tensor pipe. Per chunk of 128 the pair's MMAs take
-// ~0.52 us; the epilogue drains it in about half of that, so the statistics
-// (5 instructions a logit) run while the MMA fills the two slots of the next
-// unit's first chunks.
+// Why 256 x 256 on a pair: an SM then loads 64 KB of operands for every 128
+// x 256 x 128 products, half of what one CTA with the same accumulator loads,
+// and two 256-column slots fill the tensor memory, one drained while the other
+// is multiplied into. The remaining 512 - 2 * 256 columns being none, a unit's
+// statistics (5 instructions a logit) run while the MMA fills the slots with
+// the next unit's first chunks, and chunks must be long enough to hide them.
+//
+// What bounds them: for thousands of rows the tensor pipe, and on calls of
+// milliseconds the power limit under it (products run at the 1.72 to 1.74
+// PFLOP/s that a library product sustains there). Of one launch, with cold
+// caches, the pipe is active (2048 x 50176 x 1536 unless said otherwise):
+//   OP_SCORE   K = 8, 206 us    64 %    OP_DZ      187 us    70 %
+//   OP_DH      183 us           73 %    OP_DW      180 us    74 %
+//   OP_SCALED  2048 x 32000 x 4096, 303 us         74 %
+// the rest being the drains at a unit's end, the partial last round of units
+// and the clock, which drops under this load. With a few hundred rows the
+// operands bound them (units share W tiles and hidden rows through L2, which
+// delivers about 15.5 TB/s to the SMs): 301 x 50001 x 1000 scores in 58 us
+// where the MMAs of its 512 padded rows need 27. Under 128 rows the gradient's
+// products are streams: W read (OP_DZ, OP_DH) or dW written (OP_DW), 28 to 33
+// us each at 48 x 32000 x 2048, 131 MB (20 us at the copy bandwidth).
 #pragma once
 #include "head_kernels.cuh"
 #include "int8_kernels.cuh"
@@ -170,7 +187,10 @@ static_assert(sizeof(PairOpParams) <= 128, "kernel parameter struct above 128 by
 // nkb K boxes from kb0.
 //   OP_SCORE, OP_SELECT, OP_DZ: n1 hidden-row tiles, fastest (they share each
 //     W tile from L2)
-//   OP_DH: n1 tiles of d, fastest, then n0 hidden-row tiles, then segments
+//   OP_DH: n1 tiles of d, fastest, then n0 hidden-row tiles, then segments, the
+//     last one first: OP_DZ has left the end of W and of dz in L2 (777 x 50001
+//     x 1000: gradient 245.6 -> 240.6 us; 48 x 32000 x 2048: 99.4 -> 96.8;
+//     W's loads marked evict-last, without it no gain there)
 //   OP_DW: n1 tiles of d, fastest, then vocabulary tiles
 struct PairUnit { int a0, b0, kb0, nkb, seg; };
 
@@ -199,8 +219,9 @@ __device__ __forceinline__ PairUnit unit_of(const PairOpParams& p, const UnitWal
   t.nkb = p.nk;
   t.seg = 0;
   if constexpr (OP == OP_DH) {
-    t.seg = w.q / p.n0;
-    t.a0 = (w.q - t.seg * p.n0) * 256;
+    const int q = w.q / p.n0;
+    t.seg = (p.nk - 1) / p.seg - q;
+    t.a0 = (w.q - q * p.n0) * 256;
     t.b0 = w.r * 256;
     t.kb0 = t.seg * p.seg;
     t.nkb = min(p.seg, p.nk - t.kb0);

@@ -7,16 +7,22 @@
 namespace {
 
 // Scaled logits of as many rows as this run on the fp16 copies: above 64 rows
-// the int8-streaming kernel converts W again for every 64.
+// the int8-streaming kernel converts W again for every 64 (50001 x 1040, 64 rows:
+// streaming 23.7 us; 67 rows: streaming 38, on the copies 26).
 constexpr int64_t kI8ScaledWideB = 65;
 constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
 // The wide projection writes its logits (OP_SCOREZ) where candidates do not
-// pay: up to kLogitRows rows, or in at most kLogitRounds units a pair -- a large
-// part of the vocabulary is then under way before a threshold can thin the
-// candidates out. (1024 x 151936 x 1536, K = 8: 342 us, with candidates 366;
-// 4098 x 1352 x 384, K = 5: see the table; 2048 x 151936 x 1536: candidates.)
-constexpr int64_t kLogitRows = 1024;
-constexpr int64_t kLogitRounds = 8;
+// pay. Candidates cost some 14 us whatever the size (until a threshold can thin
+// them out, every block of the vocabulary is one); logits cost about 3 ns a
+// row more in the merge and 0.2 ns per thousand of them. They break even near
+// B (15000 + V) = kLogitWork. Logits against candidates, us:
+//   256 x 151936 x 1536, K = 8    118 / 134    512 rows    188 / 181
+//   1024 rows                     342 / 313    1024 x 50001 x 1000    106 / 106
+//   1280 x 32000 x 2048, K = 8    130 / 140    2048 rows   197 / 193
+//   2048 x 8192 x 1024, K = 8      53 /  58    4096 rows    93 /  87
+//   4098 x 1352 x 384, K = 5       40 /  47    6000 rows    52 /  47
+// (The largest exception found: 384 x 151936 x 1536, 181 / 176.)
+constexpr int64_t kLogitWork = 68000000;
 constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
 
 // 2-D tensor map of 16-bit or 32-bit elements: `inner` contiguous, rows of
@@ -228,20 +234,17 @@ int cand_blocks(int pairs, int64_t n_rt, int K) {
   return 64 + 32 * K + 16 * static_cast<int>((pairs + n_rt - 1) / n_rt + 2);
 }
 
+// With logits: logits [B][ld] and records [3][B][n_vt]. Without (many rows, or
+// no alternatives wanted of more than 128): records, target logits, row words and
+// tile marks (cleared together), candidates.
 struct ScoreLayout {
   int64_t n_vt, ld;
   size_t rows, logits, rec, rec_part, zt, words, words_bytes, tiles, cand, total;
 };
-// Up to kLogitRows rows: logits [B][ld] and records [3][B][n_vt] (without
-// alternatives only the narrow ones need logits). More: records, target
-// logits, row words and tile marks (cleared together), candidates.
-// The most rows whose calls do that.
-int64_t logit_rows(const detlm_head* h, int pairs) {
-  const int64_t rows = kLogitRounds * pairs / tiles256(h->V) * kRowsM;
-  return rows > kLogitRows ? rows : kLogitRows;
-}
-bool score_has_logits(const detlm_head* h, int64_t B, int K, int pairs) {
-  return B <= kNarrowRows || (K > 0 && B <= logit_rows(h, pairs));
+// The most rows whose alternatives come from logits in the workspace.
+int64_t logit_rows(const detlm_head* h) { return kLogitWork / (15000 + h->V); }
+bool score_has_logits(const detlm_head* h, int64_t B, int K) {
+  return B <= kNarrowRows || (K > 0 && B <= logit_rows(h));
 }
 
 ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
@@ -258,7 +261,7 @@ ScoreLayout score_layout(const detlm_head* h, int64_t B, int K, int pairs) {
   L.rec_part = round256(static_cast<size_t>(B) * L.n_vt * 4) / 4;
   L.rec = part(3 * L.rec_part * 4);
   if (!narrow && needs_padding(h)) L.rows = part(static_cast<size_t>(B) * padded_d(h) * 2);
-  if (score_has_logits(h, B, K, pairs)) {
+  if (score_has_logits(h, B, K)) {
     L.ld = narrow ? h->V : (h->V + 31) / 32 * 32;
     L.logits = part(static_cast<size_t>(B) * L.ld * 4);
   } else {
@@ -408,7 +411,7 @@ int score_wide(detlm_head* h, const void* h_dev, const int32_t* targets, int64_t
   p.s.words = reinterpret_cast<int32_t*>(ws + L.words);
   ScoreMergeParams mp;
   score_merge_params(&mp, h, L, B, K, inv_t, targets, out);
-  if (score_has_logits(h, B, K, pairs)) {
+  if (score_has_logits(h, B, K)) {
     CUtensorMap zOut;
     if (!encode_box(&zOut, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.logits, L.ld, B, L.ld * 4, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_128B, false))
@@ -728,7 +731,7 @@ int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
   if (e != cudaSuccess) return status_from_cuda(e);
   // each kind of call's workspace grows with its rows
   size_t need = 0;
-  for (const int64_t most : {static_cast<int64_t>(kNarrowRows), logit_rows(h, pairs), max_B}) {
+  for (const int64_t most : {static_cast<int64_t>(kNarrowRows), logit_rows(h), max_B}) {
     const size_t n = score_layout(h, most < max_B ? most : max_B, top_k, pairs).total;
     if (n > need) need = n;
   }

@@ -15,7 +15,9 @@
 //
 // Bound: latency. A block makes four dependent rounds of loads (records,
 // their tree, the candidates' logits, the target), and a launch of up to ~1200
-// rows is one wave of blocks.
+// rows is one wave of blocks: about 4 us after the projection for a few rows
+// (1 x 32000), 19 us for 2048 rows of 50176 with candidates, 30 us for 4098
+// rows of 1352 with logits.
 #pragma once
 #include "head_kernels.cuh"
 #include "pairop_kernels.cuh"
@@ -390,7 +392,8 @@ __global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const Score
 }
 
 // int8 -> fp16 (exact) of the hidden rows, n16 16-byte words, as a dependent
-// of the previous kernel on the stream.
+// of the previous kernel on the stream. A copy of a few MB: a launch's latency
+// (about 3 us) bounds it.
 __global__ void __launch_bounds__(256) rows_to_f16_kernel(const uint4* __restrict__ in,
                                                           uint4* __restrict__ out, size_t n16) {
   grid_dep_launch();

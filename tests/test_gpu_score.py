@@ -43,6 +43,8 @@ def _check_score(got, want, K, T):
     (50001, 64, 260, 1, 1.3, "fp16"), (70000, 8, 129, 13, 1.0, "bf16"),
     (1352, 384, 1300, 5, 1.0, "bf16"), (20000, 64, 1100, 32, 1.0, "bf16"),
     (60000, 24, 1050, 8, 1.0, "fp16"), (9000, 40, 1500, 0, 0.8, "bf16"),
+    (151936, 16, 450, 8, 1.0, "bf16"), (20000, 64, 2100, 32, 1.0, "bf16"),
+    (1352, 64, 4400, 5, 1.0, "fp16"),
 ])
 def test_score(V, d, B, K, T, dtype):
     torch = _torch()
@@ -83,7 +85,7 @@ def test_row_bits_do_not_depend_on_the_batch():
     assert head.check() == 0
 
 
-@pytest.mark.parametrize("B", [4, 300, 1100])
+@pytest.mark.parametrize("B", [4, 300, 1100, 1500])
 def test_equal_and_ordered_logits(B):
     """Rows that admit every block as a candidate: all logits equal (a zero
     row), rising, and falling along the vocabulary."""
