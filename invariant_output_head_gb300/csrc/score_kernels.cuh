@@ -15,9 +15,10 @@
 //
 // Bound: latency. A block makes four dependent rounds of loads (records,
 // their tree, the candidates' logits, the target), and a launch of up to ~1200
-// rows is one wave of blocks: about 4 us after the projection for a few rows
-// (1 x 32000), 19 us for 2048 rows of 50176 with candidates, 30 us for 4098
-// rows of 1352 with logits.
+// rows is one wave of blocks. One launch with cold caches: 1 row of 32000
+// 7.5 us (about 4 behind the projection, whose end it overlaps), 301 rows of
+// 50001 10 us, 2048 rows of 50176 with candidates 17 us, 4098 rows of 1352
+// with logits 30 us.
 #pragma once
 #include "head_kernels.cuh"
 #include "pairop_kernels.cuh"
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_select_kernel(const Score
 
 // int8 -> fp16 (exact) of the hidden rows, n16 16-byte words, as a dependent
 // of the previous kernel on the stream. A copy of a few MB: a launch's latency
-// (about 3 us) bounds it.
+// (2.7 us, 205 x 1040) bounds it.
 __global__ void __launch_bounds__(256) rows_to_f16_kernel(const uint4* __restrict__ in,
                                                           uint4* __restrict__ out, size_t n16) {
   grid_dep_launch();
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(256) rows_to_f16_kernel(const uint4* __restric
 }
 
 // Rows of d8 16-byte words into rows of ld8 (the words behind them are left:
-// the tensor maps end at d).
+// the tensor maps end at d). Bound: for W (once a change of it) the copy, 50001
+// x 1000 in 30 us, 6.7 TB/s; for hidden rows a launch's latency, 3 us.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint4* __restrict__ in,
                                                        uint4* __restrict__ out, int64_t rows, int d8,
                                                        int ld8) {
@@ -429,7 +431,8 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint4* __restrict__
 // (|g_l| + |g_H| (1 + log V)) / T, whose largest value over the rows goes just
 // below 2^14. fp16 then keeps every dz above 2^-38 of that with its full 11
 // bits. (bf16 has fp32's exponents and needs none.) One block; the maximum is
-// exact, so the result does not depend on any order.
+// exact, so the result does not depend on any order. A launch's latency, 3.7
+// us at 777 rows.
 __global__ void __launch_bounds__(1024)
 grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targets, int B,
                   float inv_t, float h_max, float* scale) {
@@ -464,7 +467,8 @@ grad_scale_kernel(const float* dlogp, const float* dentropy, const int32_t* targ
 // begins. Block t does the 256 entries of tile t: its threads count, each over
 // an ascending share of the rows, the targets of lower tiles and of each of
 // its own entries; gather its own rows in order; and place them by entry.
-// Every block reads all B targets (from L2).
+// Every block reads all B targets (from L2). Latency: 196 tiles, 777 rows in 4.2
+// us, 2048 rows in 5.0.
 struct TargetListParams {
   const int32_t* targets;
   int32_t B, v0, vc;
@@ -577,7 +581,8 @@ __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams
 
 // The sums of the list's runs: sums[first][k] = sum coef_n h[n][k], fp32, rows
 // in ascending order. Block (i, j): the run that starts at list position i, if
-// one does, columns 1024 j on, eight a thread.
+// one does, columns 1024 j on, eight a thread. Bound by latency (a run's rows
+// are fetched one after another): 777 x 1000 in 5.3 us, 2048 x 1536 in 9.3.
 struct TargetSumParams {
   const int32_t* targets;
   const int32_t* starts;
@@ -636,7 +641,8 @@ __global__ void __launch_bounds__(128) target_sum_kernel(const TargetSumParams p
 // whole segment), the segments' sums in ascending order onto the running
 // sum -- the same additions however the segments were split over units or
 // passes -- and last the target's entry of dz times its row of W.
-// Four columns a thread; bound by reading the partials.
+// Four columns a thread; bound by reading the partials: 777 x 1000, 25 partials
+// (78 MB) in 17 us; 2048 x 1536, four of them, in 16.
 struct FoldParams {
   const float* part;
   int64_t rows_pad;
