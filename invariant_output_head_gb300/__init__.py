@@ -5,8 +5,12 @@ computes logits = h . W^T on sm_103a tensor cores and fuses the greedy
 decision (lowest-index argmax, top-2 gap in bf16 ulps), the target
 log-probability, the margin-gated decision, seeded sampling or speculative
 verification, bit-identical for a row whatever the batch size; an integer
-front end quantizes float rows for the exact int8 head. This package is the
-thin Python binding; see ``binding.Head``.
+front end quantizes float rows for the exact int8 head. The score call gives
+log-probability, entropy and the most likely alternatives of given tokens, its
+backward call the gradients of the hidden rows and the weight, and the int8
+head's scaled logits apply a scale per token and per channel. This package is
+the thin Python binding; see ``binding.Head``, and ``training`` for the score
+call as a differentiable function.
 """
 from .binding import (  # noqa: F401
     Head, DetlmError, load_library, library_path, status_string,
