@@ -55,9 +55,9 @@
 // Why 256 x 256 on a pair: an SM then loads 64 KB of operands for every 128
 // x 256 x 128 products, half of what one CTA with the same accumulator loads,
 // and two 256-column slots fill the tensor memory, one drained while the other
-// is multiplied into. The remaining 512 - 2 * 256 columns being none, a unit's
-// statistics (5 instructions a logit) run while the MMA fills the slots with
-// the next unit's first chunks, and chunks must be long enough to hide them.
+// is multiplied into. A unit's statistics (5 instructions a logit) run while the
+// MMA fills the slots with the next unit's first chunks, which hide them if they
+// are long enough.
 //
 // What bounds them: for thousands of rows the tensor pipe, and on calls of
 // milliseconds the power limit under it (products run at the 1.72 to 1.74
