@@ -390,6 +390,12 @@ class Head:
     def _check_h(self, h):
         if not h.is_cuda or not h.is_contiguous() or h.dim() != 2 or h.shape[1] != self.d:
             raise ValueError(f"h must be a contiguous CUDA tensor [B, {self.d}]")
+        # the library takes a bare pointer: rows of another type would be
+        # misread, of a smaller one past their end
+        if h.dtype != self.W.dtype:
+            raise ValueError(f"h must have the head's dtype, {self.W.dtype}")
+        if h.device != self.W.device:
+            raise ValueError(f"h must be on the head's device, {self.W.device}")
 
     def greedy(self, h, with_logits: bool = False, stream=None, out=None):
         """Returns (token int32 [B], gap [B], logits [B, V] or None) on h's device."""
@@ -474,8 +480,6 @@ class Head:
         import torch
         self._check_h(h)
         B = int(h.shape[0])
-        if h.dtype != self.W.dtype:
-            raise ValueError("h must have the head's dtype")
         _vector(targets, "targets", B, torch.int32, h.device)
         for name, t in (("lse", lse), ("dlogp", dlogp), ("dentropy", dentropy),
                         ("entropy", entropy if dentropy is not None else None)):
@@ -514,8 +518,6 @@ class Head:
         if self.dtype != "int8":
             raise DetlmError(DETLM_EUNSUPPORTED, "scaled_logits")
         self._check_h(q)
-        if q.dtype != torch.int8:
-            raise ValueError("q must be an int8 tensor")
         B = int(q.shape[0])
         _vector(x_scale, "x_scale", B, torch.float32, q.device)
         _vector(w_scale, "w_scale", self.V, torch.float32, q.device)
