@@ -71,7 +71,8 @@ typedef enum {
  *
  * "Greedy Decoding Has a Precision Clause", section "Token-ranking margins
  * ...": the weight of the lm_head projection. W is BORROWED: the caller keeps
- * it alive and unchanged until detlm_head_destroy. The handle owns its TMA
+ * it alive until detlm_head_destroy, and announces a change of it in place
+ * with detlm_head_weights_changed. The handle owns its TMA
  * descriptors, its workspace and a device error word, all made on the
  * current device.
  * Requirements: 1 <= V < 2^31; d >= 1; for BF16/FP16 d % 8 == 0 and for INT8
@@ -82,7 +83,10 @@ int detlm_head_create(detlm_head_t** out, const void* W_dev, int64_t V,
 
 /* Grow the workspace so that calls with up to max_B rows allocate nothing.
  * Optional: calls grow it on demand (a synchronous allocation). Call it
- * before capturing calls into a CUDA graph. For an INT8 head, max_B >= 256
+ * before capturing calls into a CUDA graph, and for the most rows that any
+ * call of the handle will have: a graph keeps the workspace's address, and a
+ * larger call would move it. The reserve calls take no stream; one that has to
+ * copy W waits for the device first. For an INT8 head, max_B >= 256
  * also makes what its calls of 256 rows or more run on: an fp16 copy of W
  * (2 * V * d bytes, converted once, exactly, and kept until destroy) and an
  * fp16 staging buffer for max_B hidden rows (2 * max_B * d bytes). */
@@ -338,7 +342,11 @@ int detlm_head_reserve_backward(detlm_head_t* head, int64_t max_B);
  * the stream's earlier kernels have finished, an INT8 head keeps an fp16 copy
  * for its wide calls, and a BF16/FP16 head with d % 16 == 8 keeps a copy of W
  * with padded rows for score and gradient calls (2 V d bytes or a little more;
- * made by the first such call or reserve). */
+ * made by the first such call or reserve). The copies are made again here, on
+ * `stream` and in place, so calls captured into a graph before the change use
+ * the new W when they are replayed after it. It can be captured itself, with
+ * the change that it announces; make the copies first then (by a reserve or a
+ * call outside the capture), or the replays do not keep them up to date. */
 int detlm_head_weights_changed(detlm_head_t* head, cudaStream_t stream);
 
 /* Scaled logits of an INT8 head ("Eliminating Nondeterminism in LLM Inference

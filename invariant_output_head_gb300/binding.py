@@ -506,7 +506,8 @@ class Head:
         detlm_head_reserve_backward(self.handle, int(max_B))
 
     def weights_changed(self, stream=None) -> None:
-        """Tell the head that W was changed in place on the stream
+        """Tell the head that W was changed in place on the stream; graphs
+        captured before the change use the new W from then on
         (detlm_head_weights_changed)."""
         detlm_head_weights_changed(self.handle, _stream_ptr(stream))
 

@@ -69,7 +69,7 @@ struct detlm_head {
   // integer head, wide batches: fp16 copy of W (made at the first such call)
   // and the call's hidden rows in fp16
   void* W16 = nullptr;
-  bool w16_stale = false;    // W changed since the copy was made
+  bool w16_ready = false;    // a copy of W has been enqueued (see copy_enqueued)
   CUtensorMap tmW16;
   void* h16 = nullptr;
   size_t h16_bytes = 0;
@@ -84,7 +84,7 @@ struct detlm_head {
   // score and gradient calls, rows of W that do not start on 32-byte sectors
   // (d % 16 == 8): a copy with rows on cache lines (see padded_weights)
   void* Wp = nullptr;
-  bool wp_stale = false;
+  bool wp_ready = false;     // as w16_ready
   // score and gradient calls: one buffer each, laid out per call
   void* sws = nullptr;
   size_t sws_bytes = 0;
@@ -685,27 +685,38 @@ cudaError_t i8_to_f16(const void* in, void* out, size_t n, cudaStream_t stream) 
   return cudaGetLastError();
 }
 
-// The wide integer path's buffers: the fp16 copy of W (2 V d bytes, made
-// once and kept until destroy) and the fp16 staging of B hidden rows. Made by
-// detlm_head_reserve when max_B >= kI8WideB, else by the first such call.
+// The handle's copies of W (W16, Wp) are filled on the stream of the first
+// call that reads one, and from then on by every detlm_head_weights_changed,
+// on its stream and at the same address: work captured into graphs finds the
+// current copy too. A fill that was only recorded into a graph has not
+// happened: the copy counts as filled once one ran, and until then every call
+// (and every replay of a call captured meanwhile) fills it for itself.
+bool copy_enqueued(cudaStream_t stream) {
+  cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(stream, &s);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess && s == cudaStreamCaptureStatusNone;
+}
+
+// The wide integer path's buffers: the fp16 copy of W (2 V d bytes, kept until
+// destroy) and the fp16 staging of B hidden rows. Made by detlm_head_reserve
+// when max_B >= kI8WideB, else by the first such call.
 int ensure_wide(detlm_head* h, int64_t B, cudaStream_t stream) {
   cudaError_t e;
   if (h->W16 == nullptr) {
-    const size_t n = static_cast<size_t>(h->V) * h->d;
     void* w16 = nullptr;
-    e = cudaMalloc(&w16, n * 2);
+    e = cudaMalloc(&w16, static_cast<size_t>(h->V) * h->d * 2);
     if (e != cudaSuccess) return status_from_cuda(e);
-    e = i8_to_f16(h->W, w16, n, stream);
-    if (e != cudaSuccess || !encode_2d(&h->tmW16, DETLM_FP16, w16, h->d, h->V, kBM)) {
+    if (!encode_2d(&h->tmW16, DETLM_FP16, w16, h->d, h->V, kBM)) {
       cudaFree(w16);
-      return e != cudaSuccess ? status_from_cuda(e) : DETLM_EINVAL;
+      return DETLM_EINVAL;
     }
     h->W16 = w16;
-    h->w16_stale = false;
-  } else if (h->w16_stale) {
+  }
+  if (!h->w16_ready) {
     e = i8_to_f16(h->W, h->W16, static_cast<size_t>(h->V) * h->d, stream);
     if (e != cudaSuccess) return status_from_cuda(e);
-    h->w16_stale = false;
+    h->w16_ready = copy_enqueued(stream);
   }
   const size_t hb = static_cast<size_t>(B) * h->d * 2;
   if (hb > h->h16_bytes) {
@@ -1240,7 +1251,9 @@ int detlm_head_reserve(detlm_head_t* h, int64_t max_B) {
   if (h == nullptr || bad_B(max_B)) return DETLM_EINVAL;
   int st = ensure_ws(h, max_B, nullptr);
   if (st == DETLM_OK && h->dtype == DETLM_INT8 && max_B >= kI8WideB) {
-    st = ensure_wide(h, max_B, nullptr);
+    // the copy is made on no stream of the caller's: whatever writes W first
+    if (!h->w16_ready) st = status_from_cuda(cudaDeviceSynchronize());
+    if (st == DETLM_OK) st = ensure_wide(h, max_B, nullptr);
     if (st == DETLM_OK) st = status_from_cuda(cudaStreamSynchronize(nullptr));
   }
   return st;

@@ -82,12 +82,16 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, unsigned block,
 // and a call whose kernels request W boxes before waiting for the stream: it
 // starts when everything before it is complete and visible.
 __global__ void weights_fence_kernel() {}
+int weights_fence(cudaStream_t stream) {
+  weights_fence_kernel<<<1, 32, 0, stream>>>();
+  return status_from_cuda(cudaGetLastError());
+}
 
 // Rows of 16-bit operands whose length is an odd multiple of 16 bytes start
 // in the middle of a 32-byte sector every other time, and a TMA box of them
 // moves half as fast (1024 x 50001 x 1000 scored: 105 us, x 1008: 76 us). Such
 // heads keep a copy of W with rows on cache lines, made by the first call (or
-// reserve) that wants it and again after detlm_head_weights_changed, and the
+// reserve) that wants it and again by detlm_head_weights_changed, and the
 // pair products copy their hidden rows likewise.
 bool needs_padding(const detlm_head* h) { return h->d % 16 != 0; }
 int64_t padded_d(const detlm_head* h) { return needs_padding(h) ? (h->d + 63) / 64 * 64 : h->d; }
@@ -103,7 +107,8 @@ int pad_rows(const detlm_head* h, const void* in, void* out, int64_t rows, cudaS
                                            rows, d8, ld8));
 }
 
-// W for the score and gradient calls: itself, or its copy with padded rows.
+// W for the score and gradient calls: itself, or its copy with padded rows
+// (see copy_enqueued).
 int padded_weights(detlm_head* h, cudaStream_t stream, const void** W) {
   *W = h->W;
   if (!needs_padding(h)) return DETLM_OK;
@@ -115,25 +120,25 @@ int padded_weights(detlm_head* h, cudaStream_t stream, const void** W) {
       return status_from_cuda(e);
     }
     h->Wp = p;
-    h->wp_stale = true;
   }
-  if (h->wp_stale) {
-    const int st = pad_rows(h, h->W, h->Wp, h->V, stream);
+  if (!h->wp_ready) {
+    int st = pad_rows(h, h->W, h->Wp, h->V, stream);
+    if (st == DETLM_OK) st = weights_fence(stream);
     if (st != DETLM_OK) return st;
-    weights_fence_kernel<<<1, 32, 0, stream>>>();
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return status_from_cuda(e);
-    h->wp_stale = false;
+    h->wp_ready = copy_enqueued(stream);
   }
   *W = h->Wp;
   return DETLM_OK;
 }
 
 int reserve_weights(detlm_head* h) {
+  if (!needs_padding(h) || h->wp_ready) return DETLM_OK;
+  // the copy is made on no stream of the caller's: whatever writes W first
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return status_from_cuda(e);
   const void* W = nullptr;
   const int st = padded_weights(h, nullptr, &W);
-  if (st != DETLM_OK || W == h->W) return st;
-  return status_from_cuda(cudaStreamSynchronize(nullptr));
+  return st == DETLM_OK ? status_from_cuda(cudaStreamSynchronize(nullptr)) : st;
 }
 
 // CTA pairs of the pair-product kernels that fit on the GPU at once (they all
@@ -722,10 +727,17 @@ extern "C" {
 
 int detlm_head_weights_changed(detlm_head_t* h, cudaStream_t stream) {
   if (h == nullptr) return DETLM_EINVAL;
-  h->w16_stale = true;
-  h->wp_stale = true;
-  weights_fence_kernel<<<1, 32, 0, stream>>>();
-  return status_from_cuda(cudaGetLastError());
+  // the copies that calls (and graphs) may already read, in place; a copy that
+  // is not filled yet is filled by the call that needs it
+  if (h->w16_ready) {
+    const cudaError_t e = i8_to_f16(h->W, h->W16, static_cast<size_t>(h->V) * h->d, stream);
+    if (e != cudaSuccess) return status_from_cuda(e);
+  }
+  if (h->wp_ready) {
+    const int st = pad_rows(h, h->W, h->Wp, h->V, stream);
+    if (st != DETLM_OK) return st;
+  }
+  return weights_fence(stream);
 }
 
 int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
