@@ -86,10 +86,11 @@ int detlm_head_create(detlm_head_t** out, const void* W_dev, int64_t V,
  * before capturing calls into a CUDA graph, and for the most rows that any
  * call of the handle will have: a graph keeps the workspace's address, and a
  * larger call would move it. The reserve calls take no stream; one that has to
- * copy W waits for the device first. For an INT8 head, max_B >= 256
- * also makes what its calls of 256 rows or more run on: an fp16 copy of W
- * (2 * V * d bytes, converted once, exactly, and kept until destroy) and an
- * fp16 staging buffer for max_B hidden rows (2 * max_B * d bytes). */
+ * copy W waits for the device first. For an INT8 head, max_B >= 65
+ * (a vocabulary shard: 256) also makes what its scaled logits of 65 rows or
+ * more and its other calls of 256 or more run on: an fp16 copy of W (2 * V * d
+ * bytes beside W's V * d, exact, kept until destroy) and an fp16 staging buffer
+ * for max_B hidden rows (2 * max_B * d bytes). */
 int detlm_head_reserve(detlm_head_t* head, int64_t max_B);
 
 /* Greedy decision for B hidden rows h_dev [B, d].

@@ -674,6 +674,10 @@ cudaError_t launch_int8_n(int N, const CUtensorMap& tmW, const CUtensorMap& tmH,
 // there; the int8-streaming kernel serves smaller batches. Both are exact,
 // so every B gives the same bits.
 constexpr int64_t kI8WideB = 256;
+// Scaled logits of as many rows as this run on the fp16 copies: above 64 rows
+// the int8-streaming kernel converts W again for every 64 (50001 x 1040, 64 rows:
+// streaming 23.7 us; 67 rows: streaming 38, on the copies 26).
+constexpr int64_t kI8ScaledWideB = 65;
 
 cudaError_t i8_to_f16(const void* in, void* out, size_t n, cudaStream_t stream) {
   const size_t n16 = n / 16;
@@ -700,7 +704,7 @@ bool copy_enqueued(cudaStream_t stream) {
 
 // The wide integer path's buffers: the fp16 copy of W (2 V d bytes, kept until
 // destroy) and the fp16 staging of B hidden rows. Made by detlm_head_reserve
-// when max_B >= kI8WideB, else by the first such call.
+// when max_B reaches the calls that use them, else by the first such call.
 int ensure_wide(detlm_head* h, int64_t B, cudaStream_t stream) {
   cudaError_t e;
   if (h->W16 == nullptr) {
@@ -1250,7 +1254,8 @@ int detlm_merge_logprob_shards(const detlm_shard_rec_t* recs_dev, int P, int64_t
 int detlm_head_reserve(detlm_head_t* h, int64_t max_B) {
   if (h == nullptr || bad_B(max_B)) return DETLM_EINVAL;
   int st = ensure_ws(h, max_B, nullptr);
-  if (st == DETLM_OK && h->dtype == DETLM_INT8 && max_B >= kI8WideB) {
+  // (a vocabulary shard has no scaled logits)
+  if (st == DETLM_OK && h->dtype == DETLM_INT8 && max_B >= (h->P > 1 ? kI8WideB : kI8ScaledWideB)) {
     // the copy is made on no stream of the caller's: whatever writes W first
     if (!h->w16_ready) st = status_from_cuda(cudaDeviceSynchronize());
     if (st == DETLM_OK) st = ensure_wide(h, max_B, nullptr);

@@ -6,10 +6,6 @@
 
 namespace {
 
-// Scaled logits of as many rows as this run on the fp16 copies: above 64 rows
-// the int8-streaming kernel converts W again for every 64 (50001 x 1040, 64 rows:
-// streaming 23.7 us; 67 rows: streaming 38, on the copies 26).
-constexpr int64_t kI8ScaledWideB = 65;
 constexpr int kNarrowRows = 128;             // rows of the one-CTA projection at most
 // The wide projection writes its logits (OP_SCOREZ) where candidates do not
 // pay. Candidates cost some 14 us whatever the size (until a threshold can thin

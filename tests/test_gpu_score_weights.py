@@ -133,7 +133,7 @@ def test_a_change_captured_with_the_calls(kind, B):
     _check(c, c.run())
 
 
-@pytest.mark.parametrize("kind,B", [(_Scored, 5), (_Scored, 200), (_Scaled, 300)])
+@pytest.mark.parametrize("kind,B", _CASES)
 def test_first_call_captured(kind, B):
     """Reserved, then captured before any eager call."""
     import torch
@@ -169,3 +169,29 @@ def test_reserve_after_a_change_on_another_stream(kind, B, seen):
     c.reserve()
     side.synchronize()
     _check(c, c.run())
+
+
+@pytest.mark.parametrize("kind,B", [(_Scaled, 65), (_Scaled, 100), (_Scaled, 255), (_Scaled, 300),
+                                    (_Scored, 5), (_Scored, 200)])
+def test_reserved_calls_allocate_nothing(kind, B):
+    """After a reserve the first calls leave the free memory as it is and can
+    be captured, for every number of rows up to the reserved one."""
+    import torch
+    c = kind(B)
+    c.reserve()
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    got = c.run()
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free
+    d = kind(B)
+    d.reserve()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d.run()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, [*d.out, *d.grads] if kind is _Scored else [d.out, *d.best[:2]]):
+        assert torch.equal(a, b)
+    assert c.head.check() == 0 and d.head.check() == 0
