@@ -20,6 +20,7 @@ constexpr int kNarrowRows = 128;             // rows of the one-CTA projection a
 // (The largest exception found: 384 x 151936 x 1536, 181 / 176.)
 constexpr int64_t kLogitWork = 68000000;
 constexpr int64_t kGradPassBytes = int64_t{8} << 30;   // dz held at once, about
+constexpr int64_t kGradSeg = static_cast<int64_t>(kSegChunks) * kGradChunkBoxes * 64;   // entries of a segment
 
 // 2-D tensor map of 16-bit or 32-bit elements: `inner` contiguous, rows of
 // `stride` bytes.
@@ -461,11 +462,10 @@ struct GradLayout {
 };
 GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   GradLayout L;
-  const int64_t seg = static_cast<int64_t>(kSegChunks) * kGradChunkBoxes * 64;
-  const int64_t segs = (h->V + seg - 1) / seg;
-  int64_t per = kGradPassBytes / (2 * seg * B);
+  const int64_t segs = (h->V + kGradSeg - 1) / kGradSeg;
+  int64_t per = kGradPassBytes / (2 * kGradSeg * B);
   per = per < 1 ? 1 : per > segs ? segs : per;
-  L.pass = per * seg;
+  L.pass = per * kGradSeg;
   const int64_t entries = L.pass < h->V ? L.pass : h->V;
   L.ld = (entries + 63) / 64 * 64;
   L.n_rt = (B + 255) / 256;
@@ -491,6 +491,25 @@ GradLayout grad_layout(const detlm_head* h, int64_t B, int pairs) {
   L.acc = part(L.pass < h->V ? static_cast<size_t>(B) * h->d * 4 : 0);
   L.total = at;
   return L;
+}
+
+// The most that any call of up to max_B rows needs. The layout grows with B but
+// for two steps down: behind every multiple of 256 rows (a new tile of rows
+// may end the split of segments, and with it seven eighths of the partial
+// sums), and where the pass loses a segment.
+size_t grad_reserve(const detlm_head* h, int64_t max_B, int pairs) {
+  size_t need = 0;
+  auto at = [&](int64_t b) {
+    const size_t n = grad_layout(h, b, pairs).total;
+    if (n > need) need = n;
+  };
+  for (int64_t b = max_B; b > 0; b = (b - 1) / 256 * 256) at(b);
+  const int64_t segs = (h->V + kGradSeg - 1) / kGradSeg;
+  for (int64_t per = 1; per <= segs; ++per) {
+    const int64_t last = kGradPassBytes / (2 * kGradSeg * per);   // rows of passes of `per` segments
+    if (last > 0 && last < max_B) at(last);
+  }
+  return need;
 }
 
 struct GradIn {
@@ -783,13 +802,7 @@ int detlm_head_reserve_backward(detlm_head_t* h, int64_t max_B) {
   int pairs = 0;
   const cudaError_t e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return status_from_cuda(e);
-  // a smaller call may split its segments (more partial sums): the largest
-  // of every 256-row step
-  size_t need = 0;
-  for (int64_t b = max_B; b > 0; b = (b - 1) / 256 * 256) {
-    const size_t n = grad_layout(h, b, pairs).total;
-    if (n > need) need = n;
-  }
+  const size_t need = grad_reserve(h, max_B, pairs);
   const int st = ensure_buffer(&h->gws, &h->gws_bytes, need, nullptr);
   return st == DETLM_OK ? reserve_weights(h) : st;
 }
