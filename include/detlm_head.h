@@ -289,8 +289,9 @@ int detlm_head_logprob_host_async(detlm_head_t* head, const void* h_host,
  *                        equal logits. top_k = 0: not written. A row with
  *                        fewer logits that are numbers: -1 and NaN behind them.
  *
- * temperature T: finite and > 0. 0 <= top_k <= min(DETLM_MAX_TOP, V).
- * A row of NaN or infinite logits gives NaN.
+ * temperature T: finite and at least 4.3e-39 (log2(e) / T has to be finite).
+ * 0 <= top_k <= min(DETLM_MAX_TOP, V). A logit of -inf has probability 0; a
+ * row with a NaN or +inf among its logits, or with nothing but -inf, gives NaN.
  * The logits are accumulated in K chunks of 512 elements (the other calls: of
  * 128), so they can differ from those in the last bits, and alternatives that
  * close can rank differently from the greedy call's token. Every sum runs in

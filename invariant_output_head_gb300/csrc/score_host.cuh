@@ -734,7 +734,10 @@ cudaError_t launch_int8_regs(const detlm_head* h, const Int8RegsParams& p, cudaS
   return cudaLaunchKernelEx(&cfg, int8_regs_kernel, p);
 }
 
-bool bad_temperature(float t) { return !(t > 0.0f) || !std::isfinite(t) || !std::isfinite(1.0f / t); }
+// (log2(e) / T, the larger, scales the differences of logits)
+bool bad_temperature(float t) {
+  return !(t > 0.0f) || !std::isfinite(t) || !std::isfinite(kLog2eScore * (1.0f / t));
+}
 
 }  // namespace
 

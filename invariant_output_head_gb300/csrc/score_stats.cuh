@@ -40,14 +40,14 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
 }
 
 // One entry into the sums relative to `mm` (the group's maximum, or kVeryLow
-// when the group has none). c = log2(e) / T. A logit of -inf counts as zero
-// (its difference is clamped, so the product with e = 0 stays finite); a NaN
-// stays one.
+// when the group has none). c = log2(e) / T. A logit of -inf counts as zero at
+// any temperature (its difference is clamped where it meets e = 0, so that the
+// product stays finite); a NaN stays one.
 __device__ __forceinline__ void stat_add(float z, float mm, float c, float& S, float& U) {
-  const float t = fmax_nan(__fsub_rn(z, mm), kVeryLow);
+  const float t = __fsub_rn(z, mm);
   const float e = exp2_approx(__fmul_rn(t, c));
   S = __fadd_rn(S, e);
-  U = __fmaf_rn(t, e, U);
+  U = __fmaf_rn(fmax_nan(t, kVeryLow), e, U);
 }
 
 // Union of two disjoint sets; commutative bit for bit. An empty side (S = 0)
@@ -56,9 +56,11 @@ __device__ __forceinline__ Stat stat_merge(const Stat& a, const Stat& b, float c
   const bool sw = a.m < b.m;
   const Stat hi = sw ? b : a, lo = sw ? a : b;
   if (lo.S == 0.0f) return hi;
-  const float d = lo.m == hi.m ? 0.0f : __fsub_rn(lo.m, hi.m);
-  const float e = exp2_approx(__fmul_rn(d, c));
-  // the scaled sum first: for a far lower side it is zero before d meets it
+  const float far = lo.m == hi.m ? 0.0f : __fsub_rn(lo.m, hi.m);
+  const float e = exp2_approx(__fmul_rn(far, c));
+  // the scaled sum first: for a far lower side it is zero before d, which is
+  // kept finite, meets it
+  const float d = fmax_nan(far, kVeryLow);
   const float s = __fmul_rn(lo.S, e);
   return Stat{hi.m, __fadd_rn(hi.S, s), __fadd_rn(hi.U, __fmaf_rn(s, d, __fmul_rn(lo.U, e)))};
 }

@@ -1,5 +1,5 @@
 """The score call, its gradient and the scaled logits at the ends of their
-ranges: workspaces of many rows."""
+ranges: workspaces of many rows, logits far apart or infinite."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +33,71 @@ def test_reserved_gradients_of_many_rows_allocate_nothing(max_B, B):
     assert torch.cuda.mem_get_info()[0] == free
     assert head.check() == 0
     head.close()
+
+
+def _far_apart(B, top, rest, x):
+    """A head of 300 entries whose logits are top * x for the last and rest * x
+    for the others, on B equal rows."""
+    import torch
+    from invariant_output_head_gb300 import Head
+    W = torch.zeros(300, 16, dtype=torch.bfloat16, device="cuda")
+    W[:, 0] = rest
+    W[299, 0] = top
+    h = torch.zeros(B, 16, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = x
+    return Head(W), h
+
+
+@pytest.mark.parametrize("B", [4, 300])
+@pytest.mark.parametrize("top,rest,x", [
+    (2.0 ** 20, -(2.0 ** 20), 2.0 ** 100),       # far apart, and far from zero
+    (0.0, -(2.0 ** 100), 2.0 ** 100),            # the others' logits are -inf
+    (2.0 ** 27, -(2.0 ** 27), 2.0 ** 100),       # their distance is not finite
+])
+def test_score_of_a_distribution_on_one_token(top, rest, x, B):
+    import torch
+    head, h = _far_apart(B, top, rest, x)
+    t = torch.full((B,), 299, dtype=torch.int32, device="cuda")
+    t[0] = 7
+    for K in (2, 0):
+        s = head.score(h, t, top_k=K)
+        assert (s.lse == top * x).all() and (s.entropy == 0).all()
+        assert (s.logp[1:] == 0).all()
+        assert s.logp[0].item() == torch.tensor((rest - top) * x).item()     # -inf past fp32
+    s = head.score(h, t, top_k=2)
+    assert s.top_token.tolist() == [[299, 0]] * B and (s.top_logp[:, 0] == 0).all()
+    assert head.check() == 0
+
+
+@pytest.mark.parametrize("B", [4, 300])
+def test_infinite_logits_at_a_huge_temperature(B):
+    """A logit of -inf has no probability at any temperature."""
+    import torch
+    head, h = _far_apart(B, 0.0, -(2.0 ** 100), 2.0 ** 100)
+    head.W[298] = 0.0
+    t = torch.full((B,), 298, dtype=torch.int32, device="cuda")
+    for T in (1.0, 1e36, 1e38, 3e38):
+        s = head.score(h, t, temperature=T)
+        log2 = 0.6931471805599453
+        # one rounding each of log S and of the differences, 2^-23 of them
+        for got, want in ((s.lse, log2), (s.entropy, log2), (s.logp, -log2)):
+            assert ((got.double() - want).abs() <= 2e-7).all()
+    assert head.check() == 0
+
+
+def test_temperatures_whose_inverse_overflows_are_refused():
+    """1 / T and log2(e) / T, by which logits are scaled, have to be finite."""
+    import torch
+    from invariant_output_head_gb300 import DETLM_EINVAL, DetlmError
+    head, h = _far_apart(3, 1.0, 0.0, 1.0)
+    t = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ok = head.score(h, t, temperature=5e-39)
+    assert (ok.entropy == 0).all() and not torch.isnan(ok.lse).any()
+    for T in (1e-39, 2.9e-39, 3e-39, 4e-39):
+        for call in (lambda: head.score(h, t, temperature=T),
+                     lambda: head.score_backward(h, t, ok.lse, ok.entropy, ok.entropy,
+                                                 temperature=T)):
+            with pytest.raises(DetlmError) as e:
+                call()
+            assert e.value.status == DETLM_EINVAL
+    assert head.check() == 0
