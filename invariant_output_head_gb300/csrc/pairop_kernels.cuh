@@ -89,6 +89,7 @@ constexpr int kGradChunkBoxes = 32;      // 64-element K boxes per gradient chun
 constexpr int kScaledChunkBoxes = 16;    // OP_SCALED: 1024
 constexpr int kSegChunks = 8;            // gradient chunks per vocabulary segment (16384)
 constexpr int kCandFloats = 20;          // a candidate block: 16 logits, its index, padding
+constexpr float kLowLogP = -1.0e4f;       // e^ of it is zero in fp32
 constexpr int kFewRows = 128;            // OP_DW: rows whose targets a warp holds in registers
 constexpr int kRowWords = 4;             // words of a row before its slots
 enum : int { RW_COUNT = 0, RW_SEL_M = 1, RW_SEL_T = 2, RW_OVER = 3 };
@@ -167,7 +168,7 @@ struct PairOpParams {
                             // OP_DH, OP_DW: K is the number of columns of D (d);
                             // OP_DZ: K is the whole head's V
   int32_t t_off;            // gradient: vocabulary index of this pass's first entry
-  float c, inv_t;           // log2(e) / T, 1 / T
+  float c, inv_t;           // score: log2(e) / T; 1 / T
   union {
     int64_t rec_part;       // score: elements between the record arrays
     float* coef;            // OP_DZ: [B] out, OP_DW: in: the target's entry of dz (as scaled)
@@ -984,14 +985,17 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           scaled_tail(p, &tmO, acc, red + (warp - 4) * 128, sg, lane, n, nw0, vb, min(128, p.V - vb));
         }
       } else if constexpr (OP == OP_DZ) {
-        // dz - (1/T) g_l 1[v = t] = -(1/T) p (g_l + g_H (log p + H)),
-        // p = e^(z/T - lse), written as p (a1 z + a0) with the row's own a1, a0
-        float a0 = 0.0f, a1 = 0.0f, l2 = 0.0f, gl = 0.0f;
+        // dz - (1/T) g_l 1[v = t] = -(1/T) p (g_l + g_H (log p + H)), written
+        // as p (a1 log p + a0) with the row's own a1, a0. log p = z/T - lse is
+        // one rounding of the difference itself: a rounded lse log2(e), or H -
+        // lse, would leave the size of the logits in it. Below kLowLogP, where p
+        // is zero, it stays there, so that their product is zero for -inf too.
+        float a0 = 0.0f, a1 = 0.0f, lse = 0.0f, gl = 0.0f;
         int tl = -1;                        // the target's place in this half
         if (n < p.B) {
           const int tg = p.g.targets[n];
           const float s = -p.inv_t * (p.g.scale != nullptr ? p.g.scale[0] : 1.0f);
-          const float lse = p.g.lse[n];
+          lse = p.g.lse[n];
           // (no such token: no term)
           if (tg >= 0 && tg < p.K) {
             gl = p.g.dlogp[n] * s;
@@ -999,11 +1003,9 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           }
           a0 = gl;
           if (p.g.dentropy != nullptr) {
-            const float gh = p.g.dentropy[n] * s;
-            a1 = gh * p.inv_t;
-            a0 = fmaf(gh, p.g.entropy[n] - lse, a0);
+            a1 = p.g.dentropy[n] * s;
+            a0 = fmaf(a1, p.g.entropy[n], a0);
           }
-          l2 = -lse * kLog2eScore;
         }
         if (vb < p.V && nw0 < p.B) {
           const bool f16 = (p.idesc & (7u << 7)) == 0;   // the head's format
@@ -1017,8 +1019,8 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
               float x[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float z = acc[(c0 + i) >> 4][i & 15];
-                x[i] = exp2_approx(fmaf(z, p.c, l2)) * fmaf(z, a1, a0);
+                const float lp = fmax_nan(fmaf(acc[(c0 + i) >> 4][i & 15], p.inv_t, -lse), kLowLogP);
+                x[i] = exp2_approx(lp * kLog2eScore) * fmaf(lp, a1, a0);
               }
               const bool hit = tl >= c0 && tl < c0 + 32;
               if (__any_sync(0xffffffffu, hit)) {

@@ -571,7 +571,6 @@ int score_backward(detlm_head* h, const GradIn& in, int64_t B, float inv_t, void
     p.idesc = idesc;
     p.K = static_cast<int32_t>(h->V);
     p.t_off = static_cast<int32_t>(v0);
-    p.c = kLog2eScore * inv_t;
     p.inv_t = inv_t;
     p.coef = reinterpret_cast<float*>(ws + L.coef);
     p.g.lse = in.lse;

@@ -101,3 +101,32 @@ def test_temperatures_whose_inverse_overflows_are_refused():
                 call()
             assert e.value.status == DETLM_EINVAL
     assert head.check() == 0
+
+
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("B", [4, 300])
+@pytest.mark.parametrize("top,rest,x", [
+    (2.0 ** 20, -(2.0 ** 20), 2.0 ** 100),       # far apart, and far from zero
+    (0.0, -(2.0 ** 100), 2.0 ** 100),            # the others' logits are -inf
+    (2.0 ** 27, -(2.0 ** 27), 2.0 ** 100),       # their distance is not finite
+])
+def test_gradient_of_a_distribution_on_one_token(top, rest, x, B, entropy):
+    """p is 1 on the last entry and 0 elsewhere, so dz is g at the target and
+    -g at the last entry; the entropy term is 0 (p (log p + H) -> 0). All of it
+    is exact: one row a target, powers of two."""
+    import torch
+    head, h = _far_apart(B, top, rest, x)
+    t = torch.full((B,), 299, dtype=torch.int32, device="cuda")
+    t[0] = 7
+    s = head.score(h, t)
+    assert (s.lse == top * x).all() and (s.entropy == 0).all()
+    dl = torch.full((B,), 2.0 ** -90, device="cuda")
+    de = torch.full((B,), 0.5, device="cuda") if entropy else None
+    dh, dW = head.score_backward(h, t, s.lse, s.entropy, dl, de)
+    want_h = torch.zeros_like(h)
+    want_h[0, 0] = 2.0 ** -90 * (rest - top)
+    want_W = torch.zeros_like(head.W)
+    want_W[7, 0] = 2.0 ** -90 * x
+    want_W[299, 0] = -(2.0 ** -90) * x
+    assert torch.equal(dh, want_h) and torch.equal(dW, want_W)
+    assert head.check() == 0
