@@ -322,11 +322,13 @@ int detlm_head_reserve_score(detlm_head_t* head, int64_t max_B, int top_k);
  * (entropy_dev is then not read). A row whose target is DETLM_NO_TARGET, or
  * outside [0, V), has no dlogp term. dh_dev or dW_dev may be NULL; both
  * 16-byte aligned device memory. B == 0 sets dW_dev to zero.
- * dz is held in the head's type between the products (for FP16 heads times a
- * power of two set by the largest |dlogp| and |dentropy| of the call), sums
- * run in fp32 in a fixed order without atomics; dh of a row is the same bits
- * for any B and any co-rows (FP16 heads: up to that power of two's effect on
- * terms 2^24 times smaller than the call's largest). */
+ * dz is held in the head's type between the products, but for the target's
+ * entry; sums run in fp32 in a fixed order without atomics. For FP16 heads it
+ * is held times a power of two set by the largest finite C = (|dlogp| +
+ * |dentropy| (1 + log V)) / T of the call's rows: a dz of 2^-27 C or more keeps
+ * its 11 bits, a smaller one is off by at most 2^-38 C. dh of a row is the same
+ * bits for any B and any co-rows (FP16 heads: but for what co-rows of much
+ * larger gradients cost its small dz in this way). */
 int detlm_head_score_backward(detlm_head_t* head, const void* h_dev,
                               const int32_t* targets_dev, int64_t B,
                               float temperature, const float* lse_dev,

@@ -130,3 +130,68 @@ def test_gradient_of_a_distribution_on_one_token(top, rest, x, B, entropy):
     want_W[299, 0] = -(2.0 ** -90) * x
     assert torch.equal(dh, want_h) and torch.equal(dW, want_W)
     assert head.check() == 0
+
+
+def _fp16_gradient(V, d, B, seed):
+    from tests import score_ref as ref
+    import numpy as np
+    import torch
+    from invariant_output_head_gb300 import Head
+    W, h, t = ref.grid_inputs(seed, V, d, B)
+    rng = np.random.Generator(np.random.PCG64(seed))
+    dl, de = rng.standard_normal(B), 0.1 * rng.standard_normal(B)
+    head = Head(ref.to_dev(W, "fp16"))
+    hd, td = ref.to_dev(h, "fp16"), torch.from_numpy(t).cuda()
+    return W, h, t, head, hd, td, head.score(hd, td), dl.astype(np.float32), de.astype(np.float32)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_fp16_rows_beside_one_whose_gradient_is_not_finite(value):
+    """A row whose loss overflowed leaves the other rows' dh as it is without
+    that row, bit for bit. (Its own dh, and dW, are not finite.)"""
+    import torch
+    *_, head, hd, td, s, dl, de = _fp16_gradient(3000, 72, 90, 17)
+    dl, de = torch.from_numpy(dl * 1e-3).cuda(), torch.from_numpy(de * 1e-3).cuda()
+    keep = torch.arange(90, device="cuda") != 40
+    want, _ = head.score_backward(*(x[keep].contiguous() for x in (hd, td, s.lse, s.entropy, dl, de)),
+                                  need_dW=False)
+    assert (want != 0).float().mean() > 0.9
+    dl[40] = value
+    got, dW = head.score_backward(hd, td, s.lse, s.entropy, dl, de, temperature=1.0)
+    assert torch.equal(got[keep], want)
+    assert not torch.isfinite(got[40]).any() and not torch.isfinite(dW).all()
+    assert head.check() == 0
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** -8, 2.0 ** -18])
+def test_fp16_rows_beside_rows_of_larger_gradients(ratio):
+    """dz is held in fp16 times a power of two S of the whole call. C, the
+    largest (|dlogp| + |dentropy| (1 + log V)) / T, times S lies in [2^13, 2^14):
+    a stored value is off by at most half a step of the subnormals, 2^-25 / S <=
+    2^-38 C, beyond its 11 bits, in the call and in the smaller one alike. dh
+    adds 5e-5 of the terms' magnitudes for the exponentials and the sums and,
+    rounded twice, 2^-10 of itself and a step of fp16's subnormals."""
+    import numpy as np
+    import torch
+    from tests import score_ref as ref
+    V, B, small = 3000, 200, 50
+    W, h, t, head, hd, td, s, dl, de = _fp16_gradient(V, 72, B, 23)
+    dl[:small] *= ratio
+    de[:small] *= ratio
+    args = [hd, td, s.lse, s.entropy, torch.from_numpy(dl).cuda(), torch.from_numpy(de).cuda()]
+    full = head.score_backward(*args, need_dW=False)[0][:small].double().cpu().numpy()
+    part = head.score_backward(*(x[:small].contiguous() for x in args), need_dW=False)[0]
+    part = part.double().cpu().numpy()
+    C = (np.abs(dl) + np.abs(de) * (1 + np.log(V))).max()
+    logp, _ = ref.logsoftmax(h[:small] @ W.T)
+    p = np.exp(logp)
+    H = -(p * logp).sum(axis=1, keepdims=True)
+    terms = p * (np.abs(dl[:small, None]) + np.abs(de[:small, None]) * (np.abs(logp) + H))
+    terms[np.arange(small), t[:small]] += np.abs(dl[:small])
+    rounded = 2.0 ** -10 * np.abs(part) + 2.0 ** -24 + 5e-5 * (terms @ np.abs(W))
+    assert (np.abs(full - part) <= 2.0 ** -37 * C * np.abs(W).sum(axis=0) + rounded).all()
+    # and against the formula, with the call's own C
+    g = ref.gradient(W, h, t, dl, de, 1.0)["dh"][:small]
+    each = 2.0 ** -11 * (terms @ np.abs(W))
+    assert (np.abs(full - g) <= 2.0 ** -38 * C * np.abs(W).sum(axis=0) + each + rounded).all()
+    assert head.check() == 0
