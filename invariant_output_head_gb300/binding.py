@@ -8,6 +8,7 @@ if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -73,6 +74,26 @@ def _float_dtype_code(x) -> int:
     return codes[x.dtype]
 
 
+def _on_its_stream(call):
+    """Run a call that was given a stream with that stream current: tensors
+    that it makes are then the stream's (memory of the current stream's may
+    still be in use by that stream's earlier work)."""
+    at = call.__code__.co_varnames.index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return call(*args, **kwargs)
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return run
+
+
+@_on_its_stream
 def quantize_rows(x, stream=None):
     """Integer front end on a float CUDA tensor x [B, d]: returns (q int8
     [B, d], mult int32 [B], shift int32 [B])."""
@@ -397,6 +418,7 @@ class Head:
         if h.device != self.W.device:
             raise ValueError(f"h must be on the head's device, {self.W.device}")
 
+    @_on_its_stream
     def greedy(self, h, with_logits: bool = False, stream=None, out=None):
         """Returns (token int32 [B], gap [B], logits [B, V] or None) on h's device."""
         import torch
@@ -414,6 +436,7 @@ class Head:
                           _stream_ptr(stream))
         return token, gap, logits
 
+    @_on_its_stream
     def logprob(self, h, targets, stream=None, out=None):
         import torch
         self._check_h(h)
@@ -433,6 +456,7 @@ class Head:
         return Score(torch.empty(B, **f32) if targets else None, torch.empty(B, **f32),
                      torch.empty(B, **f32), top, torch.empty((B, top_k), **f32) if top_k else None)
 
+    @_on_its_stream
     def score(self, h, targets=None, top_k: int = 0, temperature: float = 1.0, stream=None,
               out: Score | None = None) -> Score:
         """Log-probability of targets int32 [B] (DETLM_NO_TARGET: nothing to
@@ -470,6 +494,7 @@ class Head:
         """Workspace for score calls of up to max_B rows and top_k alternatives."""
         detlm_head_reserve_score(self.handle, int(max_B), int(top_k))
 
+    @_on_its_stream
     def score_backward(self, h, targets, lse, entropy, dlogp, dentropy=None,
                        temperature: float = 1.0, need_dh: bool = True, need_dW: bool = True,
                        stream=None, out=None):
@@ -511,6 +536,7 @@ class Head:
         (detlm_head_weights_changed)."""
         detlm_head_weights_changed(self.handle, _stream_ptr(stream))
 
+    @_on_its_stream
     def scaled_logits(self, q, x_scale, w_scale, out_dtype=None, stream=None, out=None):
         """int8 head: (q . W^T) * x_scale[:, None] * w_scale[None, :] as
         float32 (default), bfloat16 or float16 [B, V]; q int8 [B, d], x_scale
@@ -532,6 +558,7 @@ class Head:
                                  _stream_ptr(stream))
         return out
 
+    @_on_its_stream
     def greedy_gated(self, h, tau: float = 0.001, with_logits: bool = False, stream=None):
         """Margin-gated greedy call. Returns (token, gap, logits or None,
         base_token, margin)."""
@@ -549,6 +576,7 @@ class Head:
                                 base.data_ptr(), margin.data_ptr(), _stream_ptr(stream))
         return token, gap, logits, base, margin
 
+    @_on_its_stream
     def sample(self, h, temperature, seeds, positions, with_logits: bool = False, stream=None):
         """Seeded sampling. seeds, positions: int64/uint64 CUDA tensors [B]
         (read as unsigned 64-bit). Returns (token, score_gap, logits or None)."""
@@ -569,6 +597,7 @@ class Head:
                           logits.data_ptr() if logits is not None else None, _stream_ptr(stream))
         return token, gap, logits
 
+    @_on_its_stream
     def greedy_from_float(self, x, with_logits: bool = False, stream=None):
         """int8 head fed by float rows x [B, d] (bf16, fp16 or fp32 CUDA
         tensor). Returns (token, gap, logits or None, mult, shift)."""
@@ -591,6 +620,7 @@ class Head:
                                      mult.data_ptr(), shift.data_ptr(), _stream_ptr(stream))
         return token, gap, logits, mult, shift
 
+    @_on_its_stream
     def verify(self, h, drafts, with_logits: bool = False, stream=None):
         """Greedy speculative verify. h [R*P, d] request-major, drafts int32
         [R, P]. Returns (token [R*P], gap, logits or None, accepted [R])."""
@@ -644,6 +674,7 @@ class ShardHead(Head):
         self.V_total, self.P, self.rank, self.v_begin, self.v_end = V, P, rank, v0, v1
         self.handle = detlm_head_create_shard(W_shard.data_ptr(), V, self.d, DTYPES[dtype], P, rank)
 
+    @_on_its_stream
     def greedy_records(self, h, with_logits: bool = False, stream=None):
         """Records int32 [B, 4] (detlm_shard_rec_t) and the shard's logits or None."""
         import torch
@@ -657,6 +688,7 @@ class ShardHead(Head):
                                 _stream_ptr(stream))
         return rec, logits
 
+    @_on_its_stream
     def logprob_records(self, h, targets, stream=None):
         import torch
         self._check_h(h)
@@ -669,6 +701,7 @@ class ShardHead(Head):
         return rec
 
 
+@_on_its_stream
 def merge_greedy(recs, dtype: str, stream=None):
     """recs int32 [P, B, 4] (shard-major) -> (token int32 [B], gap [B])."""
     import torch
@@ -684,6 +717,7 @@ def merge_greedy(recs, dtype: str, stream=None):
     return token, gap
 
 
+@_on_its_stream
 def merge_logprob(recs, V: int, targets, err=None, stream=None):
     """recs int32 [P, B, 4] -> logp float32 [B]."""
     import torch
