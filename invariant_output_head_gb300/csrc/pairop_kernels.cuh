@@ -1018,9 +1018,16 @@ pairop_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
               const int c0 = 64 * b + 32 * hb;             // first of 32 columns
               float x[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float lp = fmax_nan(fmaf(acc[(c0 + i) >> 4][i & 15], p.inv_t, -lse), kLowLogP);
-                x[i] = exp2_approx(lp * kLog2eScore) * fmaf(lp, a1, a0);
+              for (int i = 0; i < 32; i += 2) {
+                const float* z = &acc[(c0 + i) >> 4][i & 15];
+                float2 lp = fma2_rn(make_float2(z[0], z[1]), make_float2(p.inv_t, p.inv_t),
+                                    make_float2(-lse, -lse));
+                lp = make_float2(fmax_nan(lp.x, kLowLogP), fmax_nan(lp.y, kLowLogP));
+                const float2 e = mul2_rn(lp, make_float2(kLog2eScore, kLog2eScore));
+                const float2 y = mul2_rn(make_float2(exp2_approx(e.x), exp2_approx(e.y)),
+                                         fma2_rn(lp, make_float2(a1, a1), make_float2(a0, a0)));
+                x[i] = y.x;
+                x[i + 1] = y.y;
               }
               const bool hit = tl >= c0 && tl < c0 + 32;
               if (__any_sync(0xffffffffu, hit)) {
