@@ -321,7 +321,8 @@ int detlm_head_reserve_score(detlm_head_t* head, int64_t max_B, int top_k);
  * in the head's type, overwritten. dentropy_dev NULL: no entropy term
  * (entropy_dev is then not read). A row whose target is DETLM_NO_TARGET, or
  * outside [0, V), has no dlogp term. dh_dev or dW_dev may be NULL; both
- * 16-byte aligned device memory. B == 0 sets dW_dev to zero.
+ * 16-byte aligned device memory that overlaps no input and not each other.
+ * B == 0 sets dW_dev to zero.
  * dz is held in the head's type between the products, but for the target's
  * entry; sums run in fp32 in a fixed order without atomics. For FP16 heads it
  * is held times a power of two set by the largest finite C = (|dlogp| +

@@ -59,15 +59,17 @@
 // MMA fills the slots with the next unit's first chunks, which hide them if they
 // are long enough.
 //
-// What bounds them: for thousands of rows the tensor pipe, and on calls of
-// milliseconds the power limit under it (products run at the 1.72 to 1.74
-// PFLOP/s that a library product sustains there). Of one launch, with cold
-// caches, the pipe is active (2048 x 50176 x 1536 unless said otherwise):
-//   OP_SCORE   K = 8, 206 us    64 %    OP_DZ      187 us    70 %
-//   OP_DH      183 us           73 %    OP_DW      180 us    74 %
-//   OP_SCALED  2048 x 32000 x 4096, 303 us         74 %
-// the rest being the drains at a unit's end, the partial last round of units
-// and the clock, which drops under this load. With a few hundred rows the
+// What bounds them: for thousands of rows the tensor pipe and, on calls of
+// milliseconds, the power limit under it: called again and again at 8192 x
+// 151936 x 1536 the gradient's products run at 1.71 GHz of 2.07 (1.7 PFLOP/s,
+// what a library product sustains), the int8 product of 2048 rows at 1.88, the
+// score, whose drains leave the pipe idle longer, at 2.02. Of one launch, with
+// cold caches, the pipe is active (2048 x 50176 x 1536 unless said otherwise):
+//   OP_SCORE   K = 8, 212 us    63 %    OP_DZ      192 us    70 %
+//   OP_DH      186 us           73 %    OP_DW      184 us    76 %
+//   OP_SCALED  2048 x 32000 x 4096, 305 us         74 %
+// the rest being the drains at a unit's end and the partial last round of
+// units. With a few hundred rows the
 // operands bound them (units share W tiles and hidden rows through L2, which
 // delivers about 15.5 TB/s to the SMs): 301 x 50001 x 1000 scores in 58 us
 // where the MMAs of its 512 padded rows need 27. Under 128 rows the gradient's

@@ -305,7 +305,10 @@ __device__ __forceinline__ void visit_blocks(const ScoreMergeParams& p, int n, i
 
 // More than 128 rows: 256-entry records, slots and candidate blocks. A row
 // whose list overflowed gets the exact rule for its K best tiles -- (maximum,
-// lowest index) of the K-th -- and its 256-row tile is marked for OP_SELECT.
+// lowest index) of the K-th -- and its 256-row tile is marked for OP_SELECT,
+// which computes the whole tile's product again (rows of all equal logits, say
+// of zeros: 8192 x 151936 x 1536, K = 8, none 2327 us, one such row 2744, one in
+// every tile 4891).
 __global__ void __launch_bounds__(kScoreThreads) score_wide_kernel(const ScoreMergeParams p) {
   __shared__ ScoreShared sh;
   const int n = blockIdx.x;
@@ -585,8 +588,12 @@ __global__ void __launch_bounds__(256) target_list_kernel(const TargetListParams
 
 // The sums of the list's runs: sums[first][k] = sum coef_n h[n][k], fp32, rows
 // in ascending order. Block (i, j): the run that starts at list position i, if
-// one does, columns 1024 j on, eight a thread. Bound by latency (a run's rows
-// are fetched one after another): 777 x 1000 in 5.3 us, 2048 x 1536 in 9.3.
+// one does, columns 1024 j on, eight a thread. Bound by latency: 777 x 1000 in
+// 5.6 us, 2048 x 1536 in 9.6, with a few rows a run. A run's rows are fetched
+// eight at a time, one group after another, so a token that many rows share
+// costs about a microsecond for every eight of them: 5928 x 1077 x 296, the
+// whole gradient (alone, cold caches) 117 us with uniform targets, 459 with half
+// of them equal; rows without a token to score are best given as -1 (107).
 struct TargetSumParams {
   const int32_t* targets;
   const int32_t* starts;
