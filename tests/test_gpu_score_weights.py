@@ -177,6 +177,7 @@ def test_reserved_calls_allocate_nothing(kind, B):
     """After a reserve the first calls leave the free memory as it is and can
     be captured, for every number of rows up to the reserved one."""
     import torch
+    kind(B).run()                          # (kernels are loaded by their first launch)
     c = kind(B)
     c.reserve()
     torch.cuda.synchronize()
