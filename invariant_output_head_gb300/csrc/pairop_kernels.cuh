@@ -32,8 +32,9 @@
 //              two exact integers is the rounding of their exact sum).
 //
 // The target's entry (g_l (1 - p) - ...) / T of the gradient never passes
-// through 16 bits: it is by far the largest of its row, and its rounding would
-// be as large as that of the result. dz holds a zero in its place; its fp32
+// through 16 bits: it is mostly by far the largest of its row, and its rounding
+// would be as large as that of the result (as it is where another token holds
+// most of the row: the result's error is then up to sqrt(2) of its own rounding). dz holds a zero in its place; its fp32
 // value contributes a row of W to dh and a row of h to dW, added in fp32
 // (grad_fold_kernel, and this kernel's OP_DW epilogue).
 //
