@@ -54,7 +54,9 @@ typedef enum {
   DETLM_BF16 = 0,   /* bf16 W and h, fp32 accumulation, fp32 logits        */
   DETLM_FP16 = 1,   /* IEEE fp16 W and h, fp32 accumulation, fp32 logits   */
   DETLM_INT8 = 2,   /* int8 W and h, exact int32 accumulation and logits   */
-  DETLM_FP32 = 3    /* fp32 rows into the integer front end, scaled logits */
+  DETLM_FP32 = 3,   /* fp32 rows into the front ends, logits                */
+  DETLM_E4M3 = 4    /* 8-bit floats (e4m3) W and h with block scales; such a */
+                    /* head has block-scaled logits and beam selection only  */
 } detlm_dtype_t;
 
 typedef enum {
@@ -76,7 +78,8 @@ typedef enum {
  * descriptors, its workspace and a device error word, all made on the
  * current device.
  * Requirements: 1 <= V < 2^31; d >= 1; for BF16/FP16 d % 8 == 0 and for INT8
- * d % 16 == 0 (rows start on 16-byte boundaries); W_dev 16-byte aligned.
+ * and E4M3 d % 16 == 0 (rows start on 16-byte boundaries) and d <= 16384; W_dev
+ * 16-byte aligned.
  * Returns DETLM_EINVAL on a bad argument, DETLM_ECUDA when no usable GPU. */
 int detlm_head_create(detlm_head_t** out, const void* W_dev, int64_t V,
                       int64_t d, int dtype);
@@ -127,7 +130,7 @@ int detlm_head_greedy(detlm_head_t* head, const void* h_dev, int64_t B,
  * 128 leaves of contiguous tiles, each folded in ascending order, combined
  * in a balanced binary tree), so logp_dev[n] is the same bits for any B and
  * any co-rows.
- * INT8 heads return DETLM_EUNSUPPORTED. */
+ * Other heads return DETLM_EUNSUPPORTED. */
 int detlm_head_logprob(detlm_head_t* head, const void* h_dev,
                        const int32_t* targets_dev, int64_t B, float* logp_dev,
                        cudaStream_t stream);
@@ -372,6 +375,122 @@ int detlm_head_scaled_logits(detlm_head_t* head, const int8_t* q_dev,
                              int64_t B, int out_dtype, void* out_dev,
                              cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating-point heads with a scale for each block of 128, and beam
+ * search on the logits of any head.
+ * ------------------------------------------------------------------------ */
+
+#define DETLM_MAX_BEAMS 32      /* beams of a sequence                        */
+#define DETLM_MAX_BEAM_OUT 64   /* continuations a sequence can ask for       */
+
+/* Float rows x_dev [B, d] (dtype BF16, FP16 or FP32) in e4m3, q_dev [B, d],
+ * with a scale for each block of block_rows x 128 elements, block_rows 1
+ * (hidden rows) or 128 (a weight): scale_dev float [ceil(B / block_rows),
+ * ceil(d / 128)], blocks at the right and lower edge of what there is.
+ *
+ *   scale = 2^e, e >= -126 the smallest with max |x| <= 448 * 2^e
+ *   q     = x / scale rounded to the nearest e4m3, ties to even
+ *
+ * ("Eliminating Nondeterminism in LLM Inference with Integer-Only Arithmetic",
+ * section DetLLM: dyadic scales, one fixed rounding rule, each token quantized
+ * from its own values.) The division is exact, so q has one right value. An
+ * all-zero block has scale 1; a block with a NaN or an infinity has scale NaN
+ * and q NaN. Requirements: d % 16 == 0; x_dev and q_dev 16-byte aligned,
+ * scale_dev 4-byte aligned; fewer than 2^31 blocks. B == 0 is a no-op. */
+int detlm_quantize_blocks(const void* x_dev, int dtype, int64_t B, int64_t d,
+                          int block_rows, void* q_dev, float* scale_dev,
+                          cudaStream_t stream);
+
+/* Logits of an E4M3 head whose values carry block scales:
+ *
+ *   out[n, v] = sum_c xs[n, c] ws[v / 128, c] sum_{k in block c} q[n, k] W[v, k]
+ *
+ * with c over the ceil(d / 128) blocks of K. q_dev e4m3 [B, d]; x_scale_dev
+ * float [B, ceil(d / 128)]; w_scale_dev float [ceil(V / 128), ceil(d / 128)];
+ * out_dev [B, V] of out_dtype (DETLM_FP32, DETLM_BF16 or DETLM_FP16). The
+ * scales are any floats whose products are normal numbers or zero (those that
+ * detlm_quantize_blocks gives, or a checkpoint's amax / 448). A block's sum is
+ * accumulated by the tensor core in fp32 from zero; the product of the scales
+ * is rounded once to fp32; sum and product are added by one fused multiply-add
+ * a block, in ascending order; the result is rounded once to out_dtype. Rows
+ * are the same bits for any B and any co-rows. Other heads:
+ * DETLM_EUNSUPPORTED. B == 0 is a no-op; q_dev 16-byte aligned, the scales
+ * 4-byte aligned, out_dev aligned to its element (rows that start on 16-byte
+ * boundaries are written fastest). The call allocates nothing. */
+int detlm_head_block_scaled_logits(detlm_head_t* head, const void* q_dev,
+                                   const float* x_scale_dev,
+                                   const float* w_scale_dev, int64_t B,
+                                   int out_dtype, void* out_dev,
+                                   cudaStream_t stream);
+
+/* One step of beam search ("Inference and Decoding", section 3: the
+ * distribution a step draws from): the n_out best continuations of each
+ * sequence's beams. logits_dev [n_seq * beams, V] (logits_dtype DETLM_FP32,
+ * DETLM_BF16 or DETLM_FP16; V the head's) are what any head's call returned,
+ * masked or penalised as the caller likes; score_dev float [n_seq, beams] the
+ * beams' log-probabilities so far. Candidate (beam b, token v) scores
+ *
+ *   score[b] + log softmax(z_b / T)_v
+ *
+ * and the n_out best, the best first, are written to parent_dev int32 (the
+ * beam, 0 .. beams - 1), token_dev int32 and out_score_dev float, each [n_seq,
+ * n_out]. Candidates of one beam rank by their logits, the lowest token first
+ * among equal ones; equal scores of different beams (as rounded to fp32) rank
+ * by beam. A candidate whose score is -inf is none, and places without one hold
+ * parent -1, token -1, score -inf. A beam with a score that is not finite (an
+ * unused place of the last step), or with a NaN or +inf among its logits or
+ * nothing but -inf, has no candidates.
+ *
+ * finished_dev, optional uint8 [n_seq, beams]: a beam whose entry is not 0 has
+ * one candidate, end_token (0 .. V - 1) at the beam's own score; its logits are
+ * not read.
+ *
+ * Any whole head, of any dtype; its weight is not read. 1 <= beams <=
+ * DETLM_MAX_BEAMS, 1 <= n_out <= DETLM_MAX_BEAM_OUT, n_seq * beams < 2^31;
+ * temperature as in detlm_head_score. n_seq == 0 is a no-op. Arrays aligned to
+ * their elements. out_score_dev may be score_dev where n_out == beams; outputs
+ * otherwise overlap nothing. A sequence's outputs are the same bits whatever
+ * other sequences share the call. */
+int detlm_head_beam_select(detlm_head_t* head, const void* logits_dev,
+                           int logits_dtype, const float* score_dev,
+                           const uint8_t* finished_dev, int32_t end_token,
+                           int64_t n_seq, int beams, int n_out,
+                           float temperature, int32_t* parent_dev,
+                           int32_t* token_dev, float* out_score_dev,
+                           cudaStream_t stream);
+
+/* Workspace for selections of up to max_rows = n_seq * beams rows and n_out
+ * continuations (these then allocate nothing). Optional, like
+ * detlm_head_reserve. */
+int detlm_head_reserve_beams(detlm_head_t* head, int64_t max_rows, int n_out);
+
+/* A tensor whose rows belong to beams: row n is n_seg pieces of seg_bytes
+ * contiguous bytes, *_seg bytes apart, and rows are *_row bytes apart (device
+ * memory; strides in bytes, any alignment, 16 bytes fastest). A cache [rows,
+ * heads, room, size] of which `used` positions are filled has n_seg = heads and
+ * seg_bytes = used * size * element. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_row, dst_row;
+  int64_t src_seg, dst_seg;
+  int64_t n_seg, seg_bytes;
+} detlm_beam_state_t;
+
+/* Move the beams' states to where a selection put them: row s * beams_out + j
+ * of every state's dst becomes row s * beams_in + parent_dev[s, j] of its src.
+ * parent_dev int32 [n_seq, beams_out] on the device; an entry outside [0,
+ * beams_in) leaves its row as it was. src == dst (with the same strides and
+ * beams_in == beams_out) moves the rows in place; otherwise a state's dst
+ * overlaps no src. Different states overlap nowhere. 1 <= beams_in, beams_out
+ * <= DETLM_MAX_BEAMS. A row has fewer than 2^31 columns of the widest of 16, 8,
+ * 4, 2 and 1 bytes that divides the state's addresses, strides and seg_bytes. One
+ * launch for up to 48 states. `states` is a host array, read before the call
+ * returns. No handle: the call allocates nothing. */
+int detlm_beam_reorder(const detlm_beam_state_t* states, int n_states,
+                       const int32_t* parent_dev, int64_t n_seq, int beams_in,
+                       int beams_out, cudaStream_t stream);
+
 /* Wait for the stream and for the copies of the handle's pending
  * asynchronous host-buffer calls, read and clear the handle's device error
  * word. DETLM_ETIMEOUT if a kernel's bounded wait ran out (its outputs are
@@ -444,7 +563,7 @@ int detlm_shard_range(int64_t V, int P, int rank, int64_t* v_begin,
  * [v_begin, v_end) of the full W (borrowed, as in detlm_head_create; same
  * dtype and alignment rules). V is the full vocabulary. The shard head
  * serves the *_shard calls only (the whole-head calls return
- * DETLM_EUNSUPPORTED); detlm_head_reserve, detlm_head_check,
+ * DETLM_EUNSUPPORTED; so does this one for E4M3); detlm_head_reserve, detlm_head_check,
  * detlm_head_time_next, detlm_head_debug and detlm_head_destroy apply. */
 int detlm_head_create_shard(detlm_head_t** out, const void* W_shard_dev,
                             int64_t V, int64_t d, int dtype, int P, int rank);

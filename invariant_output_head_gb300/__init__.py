@@ -8,7 +8,9 @@ verification, bit-identical for a row whatever the batch size; an integer
 front end quantizes float rows for the exact int8 head. The score call gives
 log-probability, entropy and the most likely alternatives of given tokens, its
 backward call the gradients of the hidden rows and the weight, and the int8
-head's scaled logits apply a scale per token and per channel. This package is
+head's scaled logits apply a scale per token and per channel. An e4m3 head
+gives logits of rows and weights with a scale for each block of 128; beam
+search selects over beams and vocabulary and reorders the beams' states. This package is
 the thin Python binding; see ``binding.Head``, and ``training`` for the score
 call as a differentiable function.
 """
@@ -28,5 +30,8 @@ from .binding import (  # noqa: F401
     ShardHead, VocabParallelHead, merge_greedy, merge_logprob, gather_records,
     DETLM_BF16, DETLM_FP16, DETLM_INT8, DETLM_FP32, DETLM_OK, DETLM_EINVAL, DETLM_EUNSUPPORTED,
     DETLM_ECUDA, DETLM_ETIMEOUT, DETLM_ENOMEM, DETLM_ETARGET, DETLM_DEBUG_STALL,
-    DETLM_NO_TARGET, DETLM_MAX_TOP,
+    DETLM_NO_TARGET, DETLM_MAX_TOP, DETLM_E4M3, DETLM_MAX_BEAMS, DETLM_MAX_BEAM_OUT,
+    detlm_quantize_blocks, detlm_head_block_scaled_logits, detlm_head_beam_select,
+    detlm_head_reserve_beams, detlm_beam_reorder,
+    quantize_blocks, block_buffers, Beams, beam_buffers, BeamStates,
 )

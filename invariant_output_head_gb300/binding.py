@@ -15,13 +15,14 @@ from typing import NamedTuple
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib",
                          "libdetlm_head.so")
 
-DETLM_BF16, DETLM_FP16, DETLM_INT8, DETLM_FP32 = 0, 1, 2, 3
-DTYPES = {"bf16": DETLM_BF16, "fp16": DETLM_FP16, "int8": DETLM_INT8}
+DETLM_BF16, DETLM_FP16, DETLM_INT8, DETLM_FP32, DETLM_E4M3 = 0, 1, 2, 3, 4
+DTYPES = {"bf16": DETLM_BF16, "fp16": DETLM_FP16, "int8": DETLM_INT8, "e4m3": DETLM_E4M3}
 DETLM_OK, DETLM_EINVAL, DETLM_EUNSUPPORTED, DETLM_ECUDA = 0, -1, -2, -3
 DETLM_ETIMEOUT, DETLM_ENOMEM, DETLM_ETARGET = -4, -5, -6
 DETLM_DEBUG_STALL = 1
 DETLM_NO_TARGET = -1
 DETLM_MAX_TOP = 32
+DETLM_MAX_BEAMS, DETLM_MAX_BEAM_OUT = 32, 64
 
 _vp, _i64, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
 _SIGS = {
@@ -41,6 +42,12 @@ _SIGS = {
     "detlm_head_reserve_backward": (_i32, [_vp, _i64]),
     "detlm_head_weights_changed": (_i32, [_vp, _vp]),
     "detlm_head_scaled_logits": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "detlm_quantize_blocks": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "detlm_head_block_scaled_logits": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "detlm_head_beam_select": (_i32, [_vp, _vp, _i32, _vp, _vp, ctypes.c_int32, _i64, _i32, _i32,
+                                      ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "detlm_head_reserve_beams": (_i32, [_vp, _i64, _i32]),
+    "detlm_beam_reorder": (_i32, [_vp, _i32, _vp, _i64, _i32, _i32, _vp]),
     "detlm_quantize_rows": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_from_float": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_host": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
@@ -93,6 +100,15 @@ def _on_its_stream(call):
     return run
 
 
+def _on_device(t, call, *args, **kwargs):
+    """call(...) with t's device current: a launch goes to the current one."""
+    import torch
+    if t.device.index == torch.cuda.current_device():
+        return call(*args, **kwargs)
+    with torch.cuda.device(t.device):
+        return call(*args, **kwargs)
+
+
 @_on_its_stream
 def quantize_rows(x, stream=None):
     """Integer front end on a float CUDA tensor x [B, d]: returns (q int8
@@ -108,6 +124,41 @@ def quantize_rows(x, stream=None):
     detlm_quantize_rows(x.data_ptr(), xd, B, d, q.data_ptr(), mult.data_ptr(),
                         shift.data_ptr(), _stream_ptr(stream))
     return q, mult, shift
+
+
+def block_buffers(B: int, d: int, block_rows: int = 1, device=None):
+    """Output buffers (q, scale) for quantize_blocks of [B, d] rows."""
+    import torch
+    return (torch.empty((B, d), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((-(-B // block_rows), -(-d // 128)), dtype=torch.float32, device=device))
+
+
+@_on_its_stream
+def quantize_blocks(x, block_rows: int = 1, stream=None, out=None):
+    """Float rows x [B, d] (bf16, fp16 or fp32 CUDA tensor, d a multiple of 16)
+    in e4m3 with a power-of-two scale for each block of block_rows x 128
+    elements (block_rows 1 for hidden rows, 128 for a weight). Returns (q
+    float8_e4m3fn [B, d], scale float32 [ceil(B / block_rows), ceil(d / 128)])
+    (detlm_quantize_blocks)."""
+    import torch
+    xd = _float_dtype_code(x)
+    if not x.is_cuda or not x.is_contiguous() or x.dim() != 2:
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    B, d = x.shape
+    if out is None:
+        out = block_buffers(B, d, block_rows, x.device)
+    q, scale = out
+    if q.dtype != torch.float8_e4m3fn or q.shape != x.shape or not q.is_contiguous() \
+            or q.device != x.device:
+        raise ValueError("q must be a contiguous float8_e4m3fn tensor like x")
+    if scale.dtype != torch.float32 or scale.shape != (-(-B // block_rows), -(-d // 128)) \
+            or not scale.is_contiguous() or scale.device != x.device:
+        raise ValueError("scale must be a contiguous float32 tensor, a value a block, on x's device")
+    _on_device(x, lambda: detlm_quantize_blocks(x.data_ptr(), xd, B, d, block_rows, q.data_ptr(),
+                                                scale.data_ptr(), _stream_ptr(stream)))
+    return out
 
 
 class DetlmError(RuntimeError):
@@ -222,6 +273,41 @@ def detlm_head_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr, B, out_dty
     _check(load_library().detlm_head_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr, B,
                                                    out_dtype, out_ptr, stream),
            "detlm_head_scaled_logits")
+
+
+def detlm_quantize_blocks(x_ptr, dtype, B, d, block_rows, q_ptr, scale_ptr, stream) -> None:
+    _check(load_library().detlm_quantize_blocks(x_ptr, dtype, B, d, block_rows, q_ptr, scale_ptr,
+                                                stream),
+           "detlm_quantize_blocks")
+
+
+def detlm_head_block_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr, B, out_dtype, out_ptr,
+                                   stream) -> None:
+    _check(load_library().detlm_head_block_scaled_logits(handle, q_ptr, x_scale_ptr, w_scale_ptr,
+                                                         B, out_dtype, out_ptr, stream),
+           "detlm_head_block_scaled_logits")
+
+
+def detlm_head_beam_select(handle, logits_ptr, logits_dtype, score_ptr, finished_ptr, end_token,
+                           n_seq, beams, n_out, temperature, parent_ptr, token_ptr, out_score_ptr,
+                           stream) -> None:
+    _check(load_library().detlm_head_beam_select(handle, logits_ptr, logits_dtype, score_ptr,
+                                                 finished_ptr, end_token, n_seq, beams, n_out,
+                                                 temperature, parent_ptr, token_ptr,
+                                                 out_score_ptr, stream),
+           "detlm_head_beam_select")
+
+
+def detlm_head_reserve_beams(handle, max_rows, n_out) -> None:
+    _check(load_library().detlm_head_reserve_beams(handle, max_rows, n_out),
+           "detlm_head_reserve_beams")
+
+
+def detlm_beam_reorder(states_ptr, n_states, parent_ptr, n_seq, beams_in, beams_out,
+                       stream) -> None:
+    _check(load_library().detlm_beam_reorder(states_ptr, n_states, parent_ptr, n_seq, beams_in,
+                                             beams_out, stream),
+           "detlm_beam_reorder")
 
 
 def detlm_quantize_rows(x_ptr, dtype, B, d, q_ptr, mult_ptr, shift_ptr, stream) -> None:
@@ -367,6 +453,27 @@ class Score(NamedTuple):
     top_logp: object    # float32 [B, top_k]
 
 
+class Beams(NamedTuple):
+    """What Head.beam_select returns (and the buffers it can be given as `out`)."""
+    parent: object      # int32 [n_seq, n_out]: the beam continued, -1 for none
+    token: object       # int32 [n_seq, n_out]
+    score: object       # float32 [n_seq, n_out]
+
+
+def beam_buffers(n_seq: int, n_out: int, device=None) -> Beams:
+    """Output buffers for Head.beam_select (pass them as `out`)."""
+    import torch
+    i32 = dict(dtype=torch.int32, device=device)
+    return Beams(torch.empty((n_seq, n_out), **i32), torch.empty((n_seq, n_out), **i32),
+                 torch.empty((n_seq, n_out), dtype=torch.float32, device=device))
+
+
+def _matrix(t, name, shape, dtype, device):
+    """A contiguous CUDA tensor of the shape and type, or a ValueError."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
 def _vector(t, name, B, dtype, device):
     """A contiguous 1-D CUDA tensor of B values, or a ValueError."""
     if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != B \
@@ -375,7 +482,8 @@ def _vector(t, name, B, dtype, device):
 
 
 class Head:
-    """One output head over a device weight W [V, d] (bf16, fp16 or int8 tensor).
+    """One output head over a device weight W [V, d] (bf16, fp16, int8 or
+    float8_e4m3fn tensor; the last has block_scaled_logits and beam_select only).
 
     The handle borrows W: keep the tensor alive while the Head is in use.
     """
@@ -383,7 +491,8 @@ class Head:
     def __init__(self, W, dtype: str | None = None):
         import torch
         if dtype is None:
-            dtype = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.int8: "int8"}[W.dtype]
+            dtype = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.int8: "int8",
+                     torch.float8_e4m3fn: "e4m3"}[W.dtype]
         if not W.is_cuda or not W.is_contiguous() or W.dim() != 2:
             raise ValueError("W must be a contiguous 2-D CUDA tensor [V, d]")
         self.W = W
@@ -559,6 +668,67 @@ class Head:
         return out
 
     @_on_its_stream
+    def block_scaled_logits(self, q, x_scale, w_scale, out_dtype=None, stream=None, out=None):
+        """e4m3 head: the logits [B, V] of rows q float8_e4m3fn [B, d] as
+        float32 (default), bfloat16 or float16, with x_scale float32 [B, ceil(d
+        / 128)] for each row's blocks and w_scale float32 [ceil(V / 128), ceil(d
+        / 128)] for W's (detlm_head_block_scaled_logits)."""
+        import torch
+        if self.dtype != "e4m3":
+            raise DetlmError(DETLM_EUNSUPPORTED, "block_scaled_logits")
+        self._check_h(q)
+        B, blocks = q.shape[0], -(-self.d // 128)
+        _matrix(x_scale, "x_scale", (B, blocks), torch.float32, q.device)
+        _matrix(w_scale, "w_scale", (-(-self.V // 128), blocks), torch.float32, q.device)
+        if out is None:
+            out = torch.empty((B, self.V), dtype=out_dtype or torch.float32, device=q.device)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out has another dtype")
+        _matrix(out, "out", (B, self.V), out.dtype, q.device)
+        code = _float_dtype_code(out)
+        _on_device(q, lambda: detlm_head_block_scaled_logits(
+            self.handle, q.data_ptr(), x_scale.data_ptr(), w_scale.data_ptr(), B, code,
+            out.data_ptr(), _stream_ptr(stream)))
+        return out
+
+    @_on_its_stream
+    def beam_select(self, logits, scores, n_out: int, temperature: float = 1.0, finished=None,
+                    end_token: int = 0, stream=None, out: Beams | None = None) -> Beams:
+        """The n_out best continuations of each sequence's beams: logits
+        [n_seq * beams, V] (float32, bfloat16 or float16) of this head, scores
+        float32 [n_seq, beams] the beams' log-probabilities so far. Beams marked
+        in finished (bool or uint8 [n_seq, beams]) stay as they are, with
+        end_token (detlm_head_beam_select). out.score may be scores."""
+        import torch
+        if scores.dim() != 2:
+            raise ValueError("scores must be [n_seq, beams]")
+        n_seq, beams = scores.shape
+        device = self.W.device
+        _matrix(scores, "scores", (n_seq, beams), torch.float32, device)
+        _matrix(logits, "logits", (n_seq * beams, self.V), logits.dtype, device)
+        code = _float_dtype_code(logits)
+        if finished is not None:
+            if finished.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("finished must be a bool or uint8 tensor")
+            _matrix(finished, "finished", (n_seq, beams), finished.dtype, device)
+        if out is None:
+            out = beam_buffers(n_seq, n_out, device)
+        else:
+            _matrix(out.parent, "out.parent", (n_seq, n_out), torch.int32, device)
+            _matrix(out.token, "out.token", (n_seq, n_out), torch.int32, device)
+            _matrix(out.score, "out.score", (n_seq, n_out), torch.float32, device)
+        _on_device(scores, lambda: detlm_head_beam_select(
+            self.handle, logits.data_ptr(), code, scores.data_ptr(), _ptr(finished), end_token,
+            n_seq, beams, n_out, temperature, out.parent.data_ptr(), out.token.data_ptr(),
+            out.score.data_ptr(), _stream_ptr(stream)))
+        return out
+
+    def reserve_beams(self, max_rows: int, n_out: int) -> None:
+        """Workspace for selections of up to max_rows = n_seq * beams rows and
+        n_out continuations."""
+        detlm_head_reserve_beams(self.handle, int(max_rows), int(n_out))
+
+    @_on_its_stream
     def greedy_gated(self, h, tau: float = 0.001, with_logits: bool = False, stream=None):
         """Margin-gated greedy call. Returns (token, gap, logits or None,
         base_token, margin)."""
@@ -647,6 +817,146 @@ class Head:
 
     def tiles(self, B: int):
         return detlm_head_tiles(self.handle, B)
+
+
+# ---- the beams' states ----------------------------------------------------
+
+class _State(ctypes.Structure):       # detlm_beam_state_t
+    _fields_ = [("src", _vp), ("dst", _vp), ("src_row", _i64), ("dst_row", _i64),
+                ("src_seg", _i64), ("dst_seg", _i64), ("n_seg", _i64), ("seg_bytes", _i64)]
+
+
+def _pieces(t, axis):
+    """Layout of a row of t, [rows, ...], in bytes: (row stride, piece stride,
+    pieces, bytes a position, positions). A row is equal contiguous pieces, each
+    of the positions along `axis` (a piece is one position without it)."""
+    size = t.element_size()
+    dims = [(n, s * size) for n, s in zip(t.shape, t.stride())]
+    axis = len(dims) if axis is None else axis
+
+    def fold(part):
+        """The axes as one of equal steps: (count, step), the step None for one."""
+        count, step = 1, None
+        for n, s in reversed(part):
+            if n == 1:
+                continue
+            if step is None:
+                step = s
+            elif s != step * count:
+                raise ValueError("the rows of a state must be equal contiguous pieces")
+            count *= n
+        return count, step
+
+    if axis == len(dims):
+        # contiguous axes at the end make the piece
+        k, each = len(dims), size
+        while k > 1 and (dims[k - 1][0] == 1 or dims[k - 1][1] == each):
+            each *= dims[k - 1][0]
+            k -= 1
+        positions = 1
+    else:
+        k = axis
+        n, step = fold(dims[axis + 1:])
+        each = n * size
+        if step is not None and step != size:
+            raise ValueError("the rows of a state must be equal contiguous pieces")
+        positions, s = dims[axis]
+        if positions > 1 and s != each:
+            raise ValueError("the positions of a state must be contiguous")
+    n_seg, step = fold(dims[1:k])
+    return dims[0][1], step or 0, n_seg, each, positions
+
+
+def _range(t):
+    """First and last byte of a tensor's elements, plus one."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+class BeamStates:
+    """The tensors that hold the states of beams (caches, token histories),
+    rows [n_seq * beams, ...] first, and their reordering (detlm_beam_reorder).
+
+    Rows move in place, or, with `out`, into other tensors of the same types
+    and shapes (but for the number of rows, where a step changes the number of
+    beams). token_dim names the axis of positions of each state (one number, or
+    one a state, None for a state without), of which reorder(used=n) moves the
+    first n. A row has to be equal contiguous pieces (any one axis, or several
+    that make one, strided). The tensors are kept; their addresses and strides
+    are read once, here.
+    """
+
+    def __init__(self, states, out=None, token_dim=None):
+        states = list(states)
+        outs = states if out is None else list(out)
+        dims = list(token_dim) if isinstance(token_dim, (list, tuple)) else [token_dim] * len(states)
+        if not states or len(outs) != len(states) or len(dims) != len(states):
+            raise ValueError("states, out and token_dim must be as many, and at least one")
+        self.states, self.out = states, outs
+        self.device = states[0].device
+        self.rows_in, self.rows_out = int(states[0].shape[0]), int(outs[0].shape[0])
+        self._table = (_State * len(states))()
+        self._each, self._full, self.positions = [], [], None
+        for e, s, o, dim in zip(self._table, states, outs, dims):
+            for t, rows in ((s, self.rows_in), (o, self.rows_out)):
+                if not t.is_cuda or t.device != self.device or t.dim() < 1 or t.shape[0] != rows:
+                    raise ValueError("states must be CUDA tensors of one device and as many rows")
+            if s.dtype != o.dtype or s.shape[1:] != o.shape[1:]:
+                raise ValueError("out must be like the states")
+            if dim is not None:
+                dim = dim + s.dim() if dim < 0 else dim
+                if not 1 <= dim < s.dim():
+                    raise ValueError("token_dim must be an axis behind the rows")
+            a, b = _pieces(s, dim), _pieces(o, dim)
+            if a[2:] != b[2:]:
+                raise ValueError("a state and its out must have rows of the same pieces")
+            e.src, e.dst = s.data_ptr(), o.data_ptr()
+            e.src_row, e.src_seg = a[:2]
+            e.dst_row, e.dst_seg = b[:2]
+            e.n_seg, each, positions = a[2:]
+            e.seg_bytes = each * positions
+            if s.numel() == 0:
+                e.n_seg = 0
+            self._full.append(each * positions)
+            self._each.append(each if dim is not None else None)
+            if dim is not None:
+                self.positions = positions if self.positions is None else min(positions, self.positions)
+        self._check_overlap(out is None)
+
+    def _check_overlap(self, in_place):
+        outs = [o for o in self.out if o.numel()]
+        if len({o.data_ptr() for o in outs}) < len(outs):
+            raise ValueError("the same tensor twice")
+        if any(n > 1 and s == 0 for o in outs for n, s in zip(o.shape, o.stride())):
+            raise ValueError("an output has more than one element at one place")
+        if in_place:
+            return
+        for a, b in map(_range, outs):
+            for c, d in (_range(s) for s in self.states if s.numel()):
+                if a < d and c < b:
+                    raise ValueError("out overlaps a state")
+
+    def reorder(self, parent, used: int | None = None, stream=None) -> None:
+        """Row s * beams + j becomes row s * beams + parent[s, j] (int32 [n_seq,
+        beams], as beam_select returns them; one outside the sequence's beams
+        leaves its row as it was). used: positions that hold something (all by
+        default)."""
+        import torch
+        if parent.dtype != torch.int32 or parent.dim() != 2 or not parent.is_contiguous() \
+                or parent.device != self.device:
+            raise ValueError(f"parent must be a contiguous int32 tensor [n_seq, beams] on {self.device}")
+        n_seq, beams = parent.shape
+        if n_seq * beams != self.rows_out or (n_seq and self.rows_in % n_seq):
+            raise ValueError(f"parent must have {self.rows_out} entries, for {self.rows_in} rows")
+        if n_seq == 0:
+            return
+        if used is not None and (self.positions is None or not 0 <= used <= self.positions):
+            raise ValueError("used must be a number of the states' positions")
+        for e, each, full in zip(self._table, self._each, self._full):
+            e.seg_bytes = full if used is None or each is None else used * each
+        _on_device(parent, lambda: detlm_beam_reorder(
+            ctypes.addressof(self._table), len(self._table), parent.data_ptr(), n_seq,
+            self.rows_in // n_seq, beams, _stream_ptr(stream)))
 
 
 # ---- vocabulary-parallel heads -------------------------------------------

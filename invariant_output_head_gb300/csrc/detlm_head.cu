@@ -27,6 +27,9 @@
 #include "int8_regs_kernel.cuh"
 #include "pairop_kernels.cuh"
 #include "score_kernels.cuh"
+#include "block_kernels.cuh"
+#include "blockquant_kernels.cuh"
+#include "beam_kernels.cuh"
 
 using namespace detlm;
 
@@ -91,6 +94,9 @@ struct detlm_head {
   void* gws = nullptr;
   size_t gws_bytes = 0;
   int op_pairs = 0;          // CTA pairs of the pair-product kernels that fit at once
+  // beam selection: the tiles' sums and the parts' lists
+  void* bws = nullptr;
+  size_t bws_bytes = 0;
   // test hook and timing hook
   int stall = 0;
   uint64_t timeout_ns = 2000000000ull;
@@ -116,7 +122,10 @@ bool load_encode() {
   return g_encode != nullptr;
 }
 
-size_t elem_bytes(int dtype) { return dtype == DETLM_INT8 ? 1 : 2; }
+size_t elem_bytes(int dtype) { return dtype == DETLM_INT8 || dtype == DETLM_E4M3 ? 1 : 2; }
+
+// heads of 16-bit floats (the others: integers, or values with block scales)
+bool is_float(const detlm_head* h) { return h->dtype == DETLM_BF16 || h->dtype == DETLM_FP16; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -1080,10 +1089,12 @@ int detlm_head_create(detlm_head_t** out, const void* W_dev, int64_t V, int64_t 
   if (out == nullptr) return DETLM_EINVAL;
   *out = nullptr;
   if (W_dev == nullptr || !aligned(W_dev, 16)) return DETLM_EINVAL;
-  if (dtype != DETLM_BF16 && dtype != DETLM_FP16 && dtype != DETLM_INT8) return DETLM_EINVAL;
+  if (dtype != DETLM_BF16 && dtype != DETLM_FP16 && dtype != DETLM_INT8 && dtype != DETLM_E4M3)
+    return DETLM_EINVAL;
   if (V < 1 || V >= (int64_t{1} << 31) || d < 1 || d >= (int64_t{1} << 31)) return DETLM_EINVAL;
   if ((d * static_cast<int64_t>(elem_bytes(dtype))) % 16 != 0) return DETLM_EINVAL;
   if (dtype == DETLM_INT8 && d > kI8MaxD) return DETLM_EINVAL;
+  if (dtype == DETLM_E4M3 && d > kBlockMaxD) return DETLM_EINVAL;
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1148,6 +1159,7 @@ int detlm_head_create_shard(detlm_head_t** out, const void* W_shard_dev, int64_t
                             int dtype, int P, int rank) {
   if (out == nullptr) return DETLM_EINVAL;
   *out = nullptr;
+  if (dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;   // no records of it to merge
   int64_t v0 = 0, v1 = 0;
   const int st = detlm_shard_range(V, P, rank, &v0, &v1);
   if (st != DETLM_OK) return st;
@@ -1181,7 +1193,7 @@ int detlm_head_greedy_shard(detlm_head_t* h, const void* h_dev, int64_t B,
 int detlm_head_logprob_shard(detlm_head_t* h, const void* h_dev, const int32_t* targets_dev,
                              int64_t B, detlm_shard_rec_t* rec_dev, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
   if (targets_dev == nullptr || !aligned(targets_dev, 4)) return DETLM_EINVAL;
@@ -1268,6 +1280,7 @@ int detlm_head_greedy(detlm_head_t* h, const void* h_dev, int64_t B, int32_t* to
                       void* gap_dev, void* logits_dev, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
   if (token_dev == nullptr || !aligned(token_dev, 4)) return DETLM_EINVAL;
@@ -1284,7 +1297,7 @@ int detlm_head_logprob(detlm_head_t* h, const void* h_dev, const int32_t* target
                        float* logp_dev, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
   if (targets_dev == nullptr || !aligned(targets_dev, 4)) return DETLM_EINVAL;
@@ -1298,7 +1311,7 @@ int detlm_head_greedy_gated(detlm_head_t* h, const void* h_dev, int64_t B, float
                             int32_t* base_token_dev, float* margin_dev, cudaStream_t stream) {
   if (h == nullptr || bad_B(B) || std::isnan(tau)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
   if (token_dev == nullptr || !aligned(token_dev, 4)) return DETLM_EINVAL;
@@ -1320,7 +1333,7 @@ int detlm_head_sample(detlm_head_t* h, const void* h_dev, int64_t B, float tempe
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
   if (!(temperature > 0.0f) || !std::isfinite(temperature)) return DETLM_EINVAL;
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
   if (seeds_dev == nullptr || !aligned(seeds_dev, 8)) return DETLM_EINVAL;
@@ -1396,6 +1409,7 @@ int detlm_head_verify(detlm_head_t* h, const void* h_dev, int64_t n_req, int64_t
                       void* logits_dev, int32_t* accepted_dev, cudaStream_t stream) {
   if (h == nullptr || n_req < 0 || P < 1) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;
   if (n_req > 0 && P > (INT32_MAX - 1) / n_req) return DETLM_EINVAL;
   if (n_req == 0) return DETLM_OK;
   if (drafts_dev == nullptr || !aligned(drafts_dev, 4)) return DETLM_EINVAL;
@@ -1416,6 +1430,7 @@ int detlm_head_greedy_host(detlm_head_t* h, const void* h_host, int64_t B, int32
                            void* gap_host, void* logits_host, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_host == nullptr || token_host == nullptr || gap_host == nullptr) return DETLM_EINVAL;
   const size_t hb = static_cast<size_t>(B) * h->d * elem_bytes(h->dtype);
@@ -1444,7 +1459,7 @@ int detlm_head_logprob_host(detlm_head_t* h, const void* h_host, const int32_t* 
                             int64_t B, float* logp_host, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_host == nullptr || targets_host == nullptr || logp_host == nullptr) return DETLM_EINVAL;
   const size_t hb = static_cast<size_t>(B) * h->d * elem_bytes(h->dtype);
@@ -1470,6 +1485,7 @@ int detlm_head_greedy_host_async(detlm_head_t* h, const void* h_host, int64_t B,
                                  cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
+  if (h->dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_host == nullptr || token_host == nullptr || gap_host == nullptr) return DETLM_EINVAL;
   const size_t hb = static_cast<size_t>(B) * h->d * elem_bytes(h->dtype);
@@ -1525,7 +1541,7 @@ int detlm_head_logprob_host_async(detlm_head_t* h, const void* h_host, const int
                                   int64_t B, float* logp_host, cudaStream_t stream) {
   if (h == nullptr || bad_B(B)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (B == 0) return DETLM_OK;
   if (h_host == nullptr || targets_host == nullptr || logp_host == nullptr) return DETLM_EINVAL;
   const size_t hb = static_cast<size_t>(B) * h->d * elem_bytes(h->dtype);
@@ -1618,6 +1634,7 @@ void detlm_head_destroy(detlm_head_t* h) {
   if (h->Wp) cudaFree(h->Wp);
   if (h->sws) cudaFree(h->sws);
   if (h->gws) cudaFree(h->gws);
+  if (h->bws) cudaFree(h->bws);
   if (h->err_mapped) cudaFreeHost(h->err_mapped);
   else if (h->d_err) cudaFree(h->d_err);
   if (h->err_host) cudaFreeHost(h->err_host);
@@ -1627,6 +1644,8 @@ void detlm_head_destroy(detlm_head_t* h) {
 }  // extern "C"
 
 #include "score_host.cuh"
+#include "block_host.cuh"
+#include "beam_host.cuh"
 
 // ---------------------------------------------------------------------------
 // Greedy call without any device allocation (see the header for who needs
@@ -1687,7 +1706,7 @@ extern "C" int detlm_greedy_noalloc(const void* W_dev, int64_t V, int64_t d, int
                                     const void* h_dev, int64_t B, int32_t* token_dev,
                                     float* gap_dev, float* logits_dev, int* err_dev,
                                     cudaStream_t stream) {
-  if (dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (dtype == DETLM_INT8 || dtype == DETLM_E4M3) return DETLM_EUNSUPPORTED;
   if (dtype != DETLM_BF16 && dtype != DETLM_FP16) return DETLM_EINVAL;
   if (W_dev == nullptr || !aligned(W_dev, 16)) return DETLM_EINVAL;
   if (V < 1 || V >= (int64_t{1} << 31) || d < 1 || d >= (int64_t{1} << 31)) return DETLM_EINVAL;

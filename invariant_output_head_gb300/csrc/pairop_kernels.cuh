@@ -481,24 +481,26 @@ __device__ __forceinline__ void add_targets(const PairOpParams& p, float (&acc)[
   }
 }
 
-// OP_SCALED: this thread's row n, columns vb .. (lim of them exist): the exact
-// int32 sum rounded once to fp32, one rounded product of the two scales, one
-// rounded product, and the output's own rounding. Rows that do not start on
-// 16-byte boundaries are written from the staging buffer one row at a time, a
-// 4-byte word a lane: 16-bit rows of odd origin pair elements (2 l - 1, 2 l).
-// acc: the int32 sums, or (OP_SCALED2) the fp32 integers that the tensor core
-// left; sw: the warp's 128 column scales in shared memory.
-template <typename Acc>
-__device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* tmO,
-                                            const Acc (&acc)[8][16], const float* sw, Staging& sg,
-                                            int lane, int n, int nw0, int vb, int lim) {
-  const int type = p.q.type;
-  const float sx = n < p.B ? p.q.x_scale[n] : 0.0f;
+// What a product writes: rows [B][V] of a type, by the tensor map or not.
+struct OutRows {
+  void* out;
+  int32_t B, V, type, tma;
+};
+
+// This thread's row n, columns vb .. (lim of them exist) of the output, whose
+// values(j, y) gives in fp32 for columns j .. j + 3: rounded once to the type
+// and written through the staging buffers. Rows that do not start on 16-byte
+// boundaries are written from the staging buffer one row at a time, a 4-byte
+// word a lane: 16-bit rows of odd origin pair elements (2 l - 1, 2 l).
+template <typename Values>
+__device__ __forceinline__ void store_rows(const OutRows& p, const void* tmO, Staging& sg, int lane,
+                                           int n, int nw0, int vb, int lim, Values values) {
+  const int type = p.type;
   const int rows = min(32, p.B - nw0);
   // fp32 rows that the tensor map cannot store: 32 columns of a row at a time
   auto rows32 = [&](uint32_t off, int c0) {
     const uint8_t* sb = sg.xs + off;
-    float* out = static_cast<float*>(p.q.out) + static_cast<size_t>(nw0) * p.V + c0 + lane;
+    float* out = static_cast<float*>(p.out) + static_cast<size_t>(nw0) * p.V + c0 + lane;
     if (c0 + lane < p.V) {
 #pragma unroll 8
       for (int r = 0; r < rows; ++r)
@@ -512,7 +514,7 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
   // shares a word with a neighbour goes element by element.
   auto rows16 = [&]() {
     const uint8_t* sb = sg.xs + 4 * (lane & 3);
-    uint16_t* o = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(nw0) * p.V + vb;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<size_t>(nw0) * p.V + vb;
     if (lim >= 128) {
 #pragma unroll 4
       for (int r = 0; r < rows; ++r, o += p.V) {
@@ -537,15 +539,6 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
       }
     }
   };
-  // columns j .. j + 3
-  auto values = [&](int j, float (&y)[4]) {
-    const float4 w = *reinterpret_cast<const float4*>(sw + j);
-    const float s[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = __fmul_rn(static_cast<float>(acc[(j + i) >> 4][(j + i) & 15]), __fmul_rn(sx, s[i]));
-    }
-  };
   uint4 w[8];
   float x[4], y[4];
   if (type == OUT_F32) {
@@ -563,7 +556,7 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
       const bool more = (b & 1) == 0 && 32 * (b + 1) < lim;   // the pair's second box follows
       if (more) continue;
       const int c0 = vb + 32 * (b & ~1);
-      if (p.q.tma) {
+      if (p.tma) {
         sg.store(tmO, lane, c0, c0 + 32, (b & 1) != 0, nw0);
       } else {
         __syncwarp();
@@ -574,9 +567,9 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
   } else {
     const bool f16 = type == OUT_FP16;
     // this row's origin is an odd element (and not the tensor map's to store)
-    uint16_t* mine = static_cast<uint16_t*>(p.q.out) + static_cast<size_t>(n) * p.V + vb;
+    uint16_t* mine = static_cast<uint16_t*>(p.out) + static_cast<size_t>(n) * p.V + vb;
     const uint32_t shift =
-        !p.q.tma ? static_cast<uint32_t>((reinterpret_cast<uintptr_t>(mine) >> 1) & 1) * 16u : 0u;
+        !p.tma ? static_cast<uint32_t>((reinterpret_cast<uintptr_t>(mine) >> 1) & 1) * 16u : 0u;
     uint32_t last = 0;
     sg.claim(lane);                            // (and the previous rows' reads are done)
 #pragma unroll
@@ -593,7 +586,7 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
       }
       sg.put(b, w, lane);
     }
-    if (p.q.tma) {
+    if (p.tma) {
       sg.store(tmO, lane, vb, vb + 64, lim > 64, nw0);
     } else {
       // (the 128th element of a shifted row has no word)
@@ -602,6 +595,26 @@ __device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* t
       rows16();
     }
   }
+}
+
+// OP_SCALED: the exact int32 sum rounded once to fp32, one rounded product of
+// the two scales, one rounded product, and the output's own rounding. acc: the
+// int32 sums, or (OP_SCALED2) the fp32 integers that the tensor core left; sw:
+// the warp's 128 column scales in shared memory.
+template <typename Acc>
+__device__ __forceinline__ void scaled_tail(const PairOpParams& p, const void* tmO,
+                                            const Acc (&acc)[8][16], const float* sw, Staging& sg,
+                                            int lane, int n, int nw0, int vb, int lim) {
+  const float sx = n < p.B ? p.q.x_scale[n] : 0.0f;
+  const OutRows out{p.q.out, p.B, p.V, p.q.type, p.q.tma};
+  store_rows(out, tmO, sg, lane, n, nw0, vb, lim, [&](int j, float (&y)[4]) {
+    const float4 w = *reinterpret_cast<const float4*>(sw + j);
+    const float s[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = __fmul_rn(static_cast<float>(acc[(j + i) >> 4][(j + i) & 15]), __fmul_rn(sx, s[i]));
+    }
+  });
 }
 
 template <int OP>

@@ -219,6 +219,24 @@ bool is_device_memory(const void* p) {
   return a.type == cudaMemoryTypeDevice;
 }
 
+// OUT_* of a header dtype.
+bool out_type(int dtype, int* type) {
+  if (dtype != DETLM_FP32 && dtype != DETLM_BF16 && dtype != DETLM_FP16) return false;
+  *type = dtype == DETLM_FP32 ? OUT_F32 : dtype == DETLM_BF16 ? OUT_BF16 : OUT_FP16;
+  return true;
+}
+
+// The tensor map of an output [B][V] that the pair products' staging buffers
+// leave by: whole 16-byte rows of device memory (false: plain stores).
+bool encode_out(CUtensorMap* m, int type, void* out, int64_t V, int64_t B) {
+  const CUtensorMapDataType t = type == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : type == OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int size = type == OUT_F32 ? 4 : 2;
+  return (V * size) % 16 == 0 && aligned(out, 16) && is_device_memory(out) &&
+         encode_box(m, t, out, V, B, V * size, 128u / size, 32, CU_TENSOR_MAP_SWIZZLE_128B, false);
+}
+
 void time_start(detlm_head* h, cudaStream_t stream) {
   if (h->t_start) cudaEventRecord(h->t_start, stream);
 }
@@ -759,7 +777,7 @@ int detlm_head_weights_changed(detlm_head_t* h, cudaStream_t stream) {
 
 int detlm_head_reserve_score(detlm_head_t* h, int64_t max_B, int top_k) {
   if (h == nullptr || bad_B(max_B) || top_k < 0 || top_k > kTopMax) return DETLM_EINVAL;
-  if (h->P > 1 || h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (h->P > 1 || !is_float(h)) return DETLM_EUNSUPPORTED;
   if (max_B == 0) return DETLM_OK;
   int pairs = 0;
   const cudaError_t e = op_pairs(h, &pairs);
@@ -780,7 +798,7 @@ int detlm_head_score(detlm_head_t* h, const void* h_dev, const int32_t* targets_
                      cudaStream_t stream) {
   if (h == nullptr || bad_B(B) || bad_temperature(temperature)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (top_k < 0 || top_k > kTopMax || top_k > h->V) return DETLM_EINVAL;
   if (B == 0) return DETLM_OK;
   if (h_dev == nullptr || !aligned(h_dev, 16)) return DETLM_EINVAL;
@@ -799,7 +817,7 @@ int detlm_head_score(detlm_head_t* h, const void* h_dev, const int32_t* targets_
 
 int detlm_head_reserve_backward(detlm_head_t* h, int64_t max_B) {
   if (h == nullptr || bad_B(max_B)) return DETLM_EINVAL;
-  if (h->P > 1 || h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (h->P > 1 || !is_float(h)) return DETLM_EUNSUPPORTED;
   if (max_B == 0) return DETLM_OK;
   int pairs = 0;
   const cudaError_t e = op_pairs(h, &pairs);
@@ -816,7 +834,7 @@ int detlm_head_score_backward(detlm_head_t* h, const void* h_dev, const int32_t*
                               cudaStream_t stream) {
   if (h == nullptr || bad_B(B) || bad_temperature(temperature)) return DETLM_EINVAL;
   if (h->P > 1) return DETLM_EUNSUPPORTED;
-  if (h->dtype == DETLM_INT8) return DETLM_EUNSUPPORTED;
+  if (!is_float(h)) return DETLM_EUNSUPPORTED;
   if (!aligned(dh_dev, 16) || !aligned(dW_dev, 16)) return DETLM_EINVAL;
   if (B == 0) {   // no rows: the weight's gradient is zero
     if (dW_dev == nullptr) return DETLM_OK;
@@ -841,10 +859,7 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   if (h->P > 1) return DETLM_EUNSUPPORTED;   // a vocabulary shard: the *_shard calls
   if (h->dtype != DETLM_INT8) return DETLM_EUNSUPPORTED;
   int type = 0;
-  if (out_dtype == DETLM_FP32) type = OUT_F32;
-  else if (out_dtype == DETLM_BF16) type = OUT_BF16;
-  else if (out_dtype == DETLM_FP16) type = OUT_FP16;
-  else return DETLM_EINVAL;
+  if (!out_type(out_dtype, &type)) return DETLM_EINVAL;
   const int size = type == OUT_F32 ? 4 : 2;
   if (B == 0) return DETLM_OK;
   if (q_dev == nullptr || !aligned(q_dev, 16)) return DETLM_EINVAL;
@@ -931,14 +946,8 @@ int detlm_head_scaled_logits(detlm_head_t* h, const int8_t* q_dev, const float* 
   p.q.w_scale = w_scale_dev;
   p.q.out = out_dev;
   p.q.type = type;
-  // whole 16-byte rows of device memory leave by the tensor map
-  const CUtensorMapDataType t = type == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                : type == OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap tmO = tmH;   // not read unless it is valid
-  p.q.tma = (h->V * size) % 16 == 0 && aligned(out_dev, 16) && is_device_memory(out_dev) &&
-            encode_box(&tmO, t, out_dev, h->V, B, h->V * size, 128u / size, 32,
-                       CU_TENSOR_MAP_SWIZZLE_128B, false);
+  p.q.tma = encode_out(&tmO, type, out_dev, h->V, B) ? 1 : 0;
   time_start(h, stream);
   e = p.nk <= 2 * kScaledChunkBoxes ? launch_pairop<OP_SCALED2>(h, tmH, h->tmW16, tmO, p, stream)
                                 : launch_pairop<OP_SCALED>(h, tmH, h->tmW16, tmO, p, stream);
