@@ -96,35 +96,53 @@ __device__ __forceinline__ int scan_cut(u64* list, int n, int M) {
   return min(n, M);
 }
 
+// A lane's share of a tile as loaded: 16 numbers of 32 bits, or eight words of
+// two neighbours of 16.
 template <int FMT>
-__device__ __forceinline__ void scan_load(const void* row, int at, int V, bool words, float (&x)[kScanPer]) {
-  if constexpr (FMT == QF_FP32) {
-    const float* p = static_cast<const float*>(row) + at + (threadIdx.x & 31);
+struct ScanTile {
+  static constexpr int kWords = FMT == QF_FP32 ? kScanPer : kScanPer / 2;
+  uint32_t w[kWords];
+  // Tile `at` of a row of V; `words`: a row of 16-bit numbers starts on a word.
+  // (A loop over the whole loads alone, so that all are under way together.)
+  __device__ __forceinline__ void load(const uint8_t* row, int at, int V, bool words) {
+    const int lane = threadIdx.x & 31;
+    if (words && at + kScanTile <= V) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + (FMT == QF_FP32 ? at : at / 2) + lane;
 #pragma unroll
-    for (int i = 0; i < kScanPer; ++i)
-      x[i] = at + 32 * i + static_cast<int>(threadIdx.x & 31) < V ? __ldg(p + 32 * i) : -INFINITY;
-  } else {
-    // two neighbours a 4-byte word, or apart where the row starts between words
-    const uint16_t* p = static_cast<const uint16_t*>(row) + at + 2 * (threadIdx.x & 31);
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(p + 32 * i);
+    } else if constexpr (FMT == QF_FP32) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
 #pragma unroll
-    for (int i = 0; i < kScanPer / 2; ++i) {
-      const int k = at + 64 * i + 2 * static_cast<int>(threadIdx.x & 31);
+      for (int i = 0; i < kWords; ++i) {
+        const int k = at + 32 * i + lane;
+        w[i] = k < V ? __ldg(p + k) : 0xFF800000u;
+      }
+    } else {
       // (beyond the row's end: the type's -inf)
       constexpr uint32_t kNone = FMT == QF_BF16 ? 0xFF80u : 0xFC00u;
-      uint32_t w;
-      if (words && k + 1 < V) {
-        w = __ldg(reinterpret_cast<const uint32_t*>(p + 64 * i));
-      } else {
-        const uint32_t lo = k < V ? __ldg(p + 64 * i) : kNone;
-        const uint32_t hi = k + 1 < V ? __ldg(p + 64 * i + 1) : kNone;
-        w = lo | (hi << 16);
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int k = at + 64 * i + 2 * lane;
+        const uint32_t lo = k < V ? __ldg(p + k) : kNone;
+        const uint32_t hi = k + 1 < V ? __ldg(p + k + 1) : kNone;
+        w[i] = lo | (hi << 16);
       }
-      const float2 v = unpack16(w, FMT == QF_FP16);
-      x[2 * i] = v.x;
-      x[2 * i + 1] = v.y;
     }
   }
-}
+  __device__ __forceinline__ void values(float (&x)[kScanPer]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (FMT == QF_FP32) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 v = unpack16(w[i], FMT == QF_FP16);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+      }
+    }
+  }
+};
 // index in the row of a lane's element i of the tile at `at`
 template <int FMT>
 __device__ __forceinline__ int scan_index(int at, int i) {
@@ -145,15 +163,14 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamScanP
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t size = FMT == QF_FP32 ? 4 : 2;
   const uint8_t* row = static_cast<const uint8_t*>(p.logits) + static_cast<size_t>(r) * p.V * size;
-  const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;
+  const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;   // (rows of 32-bit numbers always)
   // whole tiles to a part
   const int t0 = static_cast<int>(static_cast<int64_t>(p.n_tiles) * blockIdx.x / p.parts);
   const int t1 = static_cast<int>(static_cast<int64_t>(p.n_tiles) * (blockIdx.x + 1) / p.parts);
-  int n = 0;                              // entries in the list before this round
   u64 last = 0;                           // the M-th best entry at the last cut
   float above = -INFINITY;                // an entry is larger (-inf is none)
   auto cut = [&](int have) {
-    n = scan_cut(list, have, p.M);
+    const int n = scan_cut(list, have, p.M);
     if (n == p.M) {
       // (what comes later has a higher index: of equal logits it is the lower)
       last = list[p.M - 1];
@@ -164,17 +181,21 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamScanP
   };
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
+  ScanTile<FMT> next;
+  if (t0 + warp < t1) next.load(row, (t0 + warp) * kScanTile, p.V, words);
   for (int tr = t0; tr < t1; tr += kScanWarps) {
     const int t = tr + warp;
     const int at = t * kScanTile;
     float x[kScanPer];
     float m = -INFINITY;
     if (t < t1) {
-      scan_load<FMT>(row, at, p.V, words, x);
+      next.values(x);
     } else {
 #pragma unroll
       for (int i = 0; i < kScanPer; ++i) x[i] = -INFINITY;
     }
+    // the next round's tile is on its way during this one
+    if (t + kScanWarps < t1) next.load(row, at + kScanRound, p.V, words);
     {
       // (a tree: the maximum's bits are the same in any order)
       float y[kScanPer / 2];
@@ -213,14 +234,19 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamScanP
     const float wm = score_unkey(__reduce_max_sync(0xffffffffu, score_key(m)));
     // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf
     const float base = wm == -INFINITY ? 0.0f : wm;
-    float e[kScanPer];
+    float2 e[kScanPer / 2];
 #pragma unroll
-    for (int i = 0; i < kScanPer; ++i) e[i] = exp2_approx((x[i] - base) * p.c);
+    for (int i = 0; i < kScanPer / 2; ++i) {
+      float2 y = make_float2(x[2 * i], x[2 * i + 1]);
+      add2_rn(y.x, y.y, -base, -base);
+      y = mul2_rn(y, make_float2(p.c, p.c));
+      e[i] = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    }
 #pragma unroll
-    for (int o = kScanPer / 2; o > 0; o >>= 1)
+    for (int o = kScanPer / 4; o > 0; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < o; ++i) e[i] += e[i + o];
-    float sum = e[0];
+      for (int i = 0; i < o; ++i) add2_rn(e[i].x, e[i].y, e[i + o].x, e[i + o].y);
+    float sum = e[0].x + e[0].y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0 && t < t1) p.tile[static_cast<size_t>(r) * p.n_tiles + t] = make_float2(wm, sum);
@@ -236,37 +262,45 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamScanP
           over |= k >= p.cut;
         }
     }
+    // (nobody looks at the count but after this, and then nobody adds to it)
     if (__syncthreads_or(over)) {
       const int have = count;
       if (have <= kScanCap) {
         cut(have);
       } else {
         // more than the list holds (long runs of equal or rising logits): this
-        // round again after the entries before it, one element a thread at a
-        // time, cut whenever the next could run over
+        // round again, after the entries of the rounds before it (their indices
+        // are lower), one element a thread at a time, cut whenever the next
+        // could run over
+        u64 kept[kScanCap / kScanThreads];
+#pragma unroll
+        for (int i = 0; i < kScanCap / kScanThreads; ++i) kept[i] = list[threadIdx.x + i * kScanThreads];
         __syncthreads();
-        if (threadIdx.x == 0) count = n;
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        const uint32_t before = 0xFFFFFFFFu - static_cast<uint32_t>(tr * kScanTile);
+#pragma unroll
+        for (int i = 0; i < kScanCap / kScanThreads; ++i)
+          if (static_cast<uint32_t>(kept[i]) > before) list[atomicAdd(&count, 1)] = kept[i];
         __syncthreads();
         for (int i = 0; i < kScanPer; ++i) {
+          const int now = count;
+          __syncthreads();
+          if (now > kScanCap - kScanThreads) cut(now);
           float y = -INFINITY;
 #pragma unroll
           for (int k = 0; k < kScanPer; ++k) y = k == i ? x[k] : y;
           const u64 word = order_word(score_key(y), scan_index<FMT>(at, i));
           if (y > -INFINITY && word > last) list[atomicAdd(&count, 1)] = word;
           __syncthreads();
-          const int now = count;
-          __syncthreads();
-          if (now > kScanCap - kScanThreads) cut(now);
         }
         cut(count);
       }
-    } else {
-      n = count;
-      __syncthreads();
     }
   }
   // the part's best, sorted; nothing behind the last
-  n = scan_cut(list, n, p.M);
+  __syncthreads();
+  const int n = scan_cut(list, count, p.M);
   u64* out = p.best + (static_cast<size_t>(r) * p.parts + blockIdx.x) * p.M;
   for (int i = threadIdx.x; i < p.M; i += kScanThreads) out[i] = i < n ? list[i] : 0;
 }

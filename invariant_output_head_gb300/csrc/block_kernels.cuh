@@ -373,13 +373,13 @@ struct BlockPairLayout {
   uint32_t stage_bytes, ctrl_off, xs_off, total;
 };
 // Stage s: this CTA's 128 hidden rows [128 x 128 B], its 128 vocabulary rows;
-// barriers (full[S], empty[S], slot_full[2], slot_empty[2], never, drain), the
+// barriers (full[S], empty[S], slot_full[2], slot_empty[2], never, drain[2]), the
 // TMEM address holder and the abort flag; the epilogue warps' staging buffers.
 __host__ __device__ inline BlockPairLayout block_pair_layout(int stages) {
   BlockPairLayout L;
   L.stage_bytes = 2u * kRowsHalf * kRowBytes;
   L.ctrl_off = static_cast<uint32_t>(stages) * L.stage_bytes;
-  L.xs_off = (L.ctrl_off + (2u * stages + 6u) * 8u + 16u + 1023u) & ~1023u;
+  L.xs_off = (L.ctrl_off + (2u * stages + 7u) * 8u + 16u + 1023u) & ~1023u;
   L.total = L.xs_off + 8u * kOpXsBytes;
   return L;
 }
@@ -404,8 +404,8 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   auto accf_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
   auto acce_bar = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
   const uint32_t never_bar = bar0 + 8u * (2 * S + 4);
-  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 6) * 8);
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);      // and the next
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 7) * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const uint32_t smem_base = smem_u32(smem);
   auto sX = [&](int s) { return smem_base + static_cast<uint32_t>(s) * L.stage_bytes; };
@@ -422,6 +422,7 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     }
     mbar_init(never_bar, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(drain_bar + 8u, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
@@ -483,17 +484,25 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------- MMA issuer
+  } else if (warp < 3) {
+    // ------------------------------------------------------ MMA issuers
+    // One thread's waits, four MMAs and two commits take some 950 cycles a
+    // block of K, the MMAs themselves 512: warps 1 and 2 issue every second
+    // block, each into its own accumulator slot. A thread waits for its slot
+    // before it looks at the stage: the slot is free once the block before the
+    // last is drained, and so, as blocks are drained in order, is the one that
+    // was in the stage before; the stage's parity then means this block.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
     if (lane == 0 && rank == 0) {
-      uint32_t stage = 0, phase = 0, slot = 0, sph = 0;
+      const uint32_t slot = static_cast<uint32_t>(warp - 1);
+      uint32_t stage = slot, phase = 0, sph = 0;
       bool ok = true;
       if (p.stall) ok = mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
+      int c = static_cast<int>(slot);            // this thread's block in the unit
       for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
-        for (int c = 0; c < p.nk; ++c) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
+        for (; c < p.nk; c += 2) {
           if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = sdesc_sw128(sX(stage));
           const uint64_t db = sdesc_sw128(sW(stage));
@@ -502,21 +511,23 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             mma_f8_pair(tmem_base + slot * 256u, da + 2u * k, db + 2u * k, p.idesc, k != 0);
           mma_commit_pair(accf_bar(slot), 3);
           mma_commit_pair(empty_bar(stage), 3);
-          if (++stage == static_cast<uint32_t>(S)) { stage = 0; phase ^= 1u; }
-          if (++slot == 2u) { slot = 0; sph ^= 1u; }
+          sph ^= 1u;
+          stage += 2;
+          if (stage >= static_cast<uint32_t>(S)) { stage -= static_cast<uint32_t>(S); phase ^= 1u; }
         }
+        c -= p.nk;                               // blocks alternate over the units' ends
       }
       if (!ok) {
         *abort_flag = 1;
         atomicOr(p.err, ERR_TIMEOUT);
       }
-      mma_commit_pair(drain_bar, 1);
+      mma_commit_pair(drain_bar + 8u * slot, 1);
       const int zero = 0;
-      mbar_wait(drain_bar, 0, &zero, p.timeout_ns);
+      mbar_wait(drain_bar + 8u * slot, 0, &zero, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp < 4) {
-    // warps 2 and 3: no role, fewer registers
+    // warp 3: no role, fewer registers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
   } else {
     // --------------------------------------------------------- epilogue
