@@ -466,21 +466,24 @@ int detlm_head_reserve_beams(detlm_head_t* head, int64_t max_rows, int n_out);
 
 /* A tensor whose rows belong to beams: row n is n_seg pieces of seg_bytes
  * contiguous bytes, *_seg bytes apart, and rows are *_row bytes apart (device
- * memory; strides in bytes, any alignment, 16 bytes fastest). A cache [rows,
- * heads, room, size] of which `used` positions are filled has n_seg = heads and
- * seg_bytes = used * size * element. */
+ * memory; strides in bytes, any alignment, 16 bytes fastest). Where a piece is a
+ * run of positions of which a call may move the first few, position_bytes is the
+ * size of one, else 0: a cache [rows, heads, room, size] has n_seg = heads,
+ * position_bytes = size * element and seg_bytes = room * position_bytes. */
 typedef struct {
   const void* src;
   void* dst;
   int64_t src_row, dst_row;
   int64_t src_seg, dst_seg;
-  int64_t n_seg, seg_bytes;
+  int64_t n_seg, seg_bytes, position_bytes;
 } detlm_beam_state_t;
 
 /* Move the beams' states to where a selection put them: row s * beams_out + j
  * of every state's dst becomes row s * beams_in + parent_dev[s, j] of its src.
  * parent_dev int32 [n_seq, beams_out] on the device; an entry outside [0,
- * beams_in) leaves its row as it was. src == dst (with the same strides and
+ * beams_in) leaves its row as it was. Of states with position_bytes the first
+ * used * position_bytes of each piece move (seg_bytes at most; used < 0: all),
+ * of the others all. src == dst (with the same strides and
  * beams_in == beams_out) moves the rows in place; otherwise a state's dst
  * overlaps no src. Different states overlap nowhere. 1 <= beams_in, beams_out
  * <= DETLM_MAX_BEAMS. A row has fewer than 2^31 columns of the widest of 16, 8,
@@ -489,7 +492,7 @@ typedef struct {
  * returns. No handle: the call allocates nothing. */
 int detlm_beam_reorder(const detlm_beam_state_t* states, int n_states,
                        const int32_t* parent_dev, int64_t n_seq, int beams_in,
-                       int beams_out, cudaStream_t stream);
+                       int beams_out, int64_t used, cudaStream_t stream);
 
 /* Wait for the stream and for the copies of the handle's pending
  * asynchronous host-buffer calls, read and clear the handle's device error

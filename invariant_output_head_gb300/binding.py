@@ -47,7 +47,7 @@ _SIGS = {
     "detlm_head_beam_select": (_i32, [_vp, _vp, _i32, _vp, _vp, ctypes.c_int32, _i64, _i32, _i32,
                                       ctypes.c_float, _vp, _vp, _vp, _vp]),
     "detlm_head_reserve_beams": (_i32, [_vp, _i64, _i32]),
-    "detlm_beam_reorder": (_i32, [_vp, _i32, _vp, _i64, _i32, _i32, _vp]),
+    "detlm_beam_reorder": (_i32, [_vp, _i32, _vp, _i64, _i32, _i32, _i64, _vp]),
     "detlm_quantize_rows": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_from_float": (_i32, [_vp, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "detlm_head_greedy_host": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
@@ -73,12 +73,17 @@ _SIGS = {
 _lib = None
 
 
-def _float_dtype_code(x) -> int:
+@functools.lru_cache(None)
+def _float_codes():
     import torch
-    codes = {torch.bfloat16: DETLM_BF16, torch.float16: DETLM_FP16, torch.float32: DETLM_FP32}
-    if x.dtype not in codes:
+    return {torch.bfloat16: DETLM_BF16, torch.float16: DETLM_FP16, torch.float32: DETLM_FP32}
+
+
+def _float_dtype_code(x) -> int:
+    code = _float_codes().get(x.dtype)
+    if code is None:
         raise ValueError("float rows must be bfloat16, float16 or float32")
-    return codes[x.dtype]
+    return code
 
 
 def _on_its_stream(call):
@@ -303,10 +308,10 @@ def detlm_head_reserve_beams(handle, max_rows, n_out) -> None:
            "detlm_head_reserve_beams")
 
 
-def detlm_beam_reorder(states_ptr, n_states, parent_ptr, n_seq, beams_in, beams_out,
+def detlm_beam_reorder(states_ptr, n_states, parent_ptr, n_seq, beams_in, beams_out, used,
                        stream) -> None:
     _check(load_library().detlm_beam_reorder(states_ptr, n_states, parent_ptr, n_seq, beams_in,
-                                             beams_out, stream),
+                                             beams_out, used, stream),
            "detlm_beam_reorder")
 
 
@@ -439,9 +444,11 @@ def _ptr(t):
 
 
 def _stream_ptr(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # (torch.cuda.current_stream() makes an object, which takes longer than a launch)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class Score(NamedTuple):
@@ -823,7 +830,8 @@ class Head:
 
 class _State(ctypes.Structure):       # detlm_beam_state_t
     _fields_ = [("src", _vp), ("dst", _vp), ("src_row", _i64), ("dst_row", _i64),
-                ("src_seg", _i64), ("dst_seg", _i64), ("n_seg", _i64), ("seg_bytes", _i64)]
+                ("src_seg", _i64), ("dst_seg", _i64), ("n_seg", _i64), ("seg_bytes", _i64),
+                ("position_bytes", _i64)]
 
 
 def _pieces(t, axis):
@@ -896,7 +904,8 @@ class BeamStates:
         self.device = states[0].device
         self.rows_in, self.rows_out = int(states[0].shape[0]), int(outs[0].shape[0])
         self._table = (_State * len(states))()
-        self._each, self._full, self.positions = [], [], None
+        self._address = ctypes.addressof(self._table)
+        self.positions = None
         for e, s, o, dim in zip(self._table, states, outs, dims):
             for t, rows in ((s, self.rows_in), (o, self.rows_out)):
                 if not t.is_cuda or t.device != self.device or t.dim() < 1 or t.shape[0] != rows:
@@ -917,8 +926,7 @@ class BeamStates:
             e.seg_bytes = each * positions
             if s.numel() == 0:
                 e.n_seg = 0
-            self._full.append(each * positions)
-            self._each.append(each if dim is not None else None)
+            e.position_bytes = each if dim is not None else 0
             if dim is not None:
                 self.positions = positions if self.positions is None else min(positions, self.positions)
         self._check_overlap(out is None)
@@ -952,11 +960,9 @@ class BeamStates:
             return
         if used is not None and (self.positions is None or not 0 <= used <= self.positions):
             raise ValueError("used must be a number of the states' positions")
-        for e, each, full in zip(self._table, self._each, self._full):
-            e.seg_bytes = full if used is None or each is None else used * each
         _on_device(parent, lambda: detlm_beam_reorder(
-            ctypes.addressof(self._table), len(self._table), parent.data_ptr(), n_seq,
-            self.rows_in // n_seq, beams, _stream_ptr(stream)))
+            self._address, len(self._table), parent.data_ptr(), n_seq, self.rows_in // n_seq,
+            beams, -1 if used is None else used, _stream_ptr(stream)))
 
 
 # ---- vocabulary-parallel heads -------------------------------------------

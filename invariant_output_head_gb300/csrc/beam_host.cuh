@@ -112,14 +112,19 @@ int detlm_head_beam_select(detlm_head_t* h, const void* logits_dev, int logits_d
 }
 
 int detlm_beam_reorder(const detlm_beam_state_t* states, int n_states, const int32_t* parent_dev,
-                       int64_t n_seq, int beams_in, int beams_out, cudaStream_t stream) {
+                       int64_t n_seq, int beams_in, int beams_out, int64_t used, cudaStream_t stream) {
   if (n_states < 0 || (n_states > 0 && states == nullptr) || bad_B(n_seq)) return DETLM_EINVAL;
   if (beams_in < 1 || beams_in > kBeamMax || beams_out < 1 || beams_out > kBeamMax) return DETLM_EINVAL;
   if (n_seq * beams_in >= (int64_t{1} << 31) || n_seq * beams_out >= (int64_t{1} << 31)) return DETLM_EINVAL;
   bool in_place = false;
+  // bytes of each piece that move
+  auto moved = [&](const detlm_beam_state_t& s) {
+    if (used < 0 || s.position_bytes == 0) return s.seg_bytes;
+    return used >= s.seg_bytes / s.position_bytes ? s.seg_bytes : used * s.position_bytes;
+  };
   for (int i = 0; i < n_states; ++i) {
     const detlm_beam_state_t& s = states[i];
-    if (s.n_seg < 0 || s.seg_bytes < 0) return DETLM_EINVAL;
+    if (s.n_seg < 0 || s.seg_bytes < 0 || s.position_bytes < 0) return DETLM_EINVAL;
     if (s.n_seg == 0 || s.seg_bytes == 0) continue;
     if (n_seq > 0 && (s.src == nullptr || s.dst == nullptr)) return DETLM_EINVAL;
     if (s.src == s.dst) {
@@ -150,15 +155,16 @@ int detlm_beam_reorder(const detlm_beam_state_t* states, int n_states, const int
   for (int pass = 0; pass < 2; ++pass) {        // checked whole before the first launch
     for (int i = 0; i < n_states; ++i) {
       const detlm_beam_state_t& s = states[i];
-      if (s.n_seg == 0 || s.seg_bytes == 0) continue;
+      const int64_t bytes = moved(s);
+      if (s.n_seg == 0 || bytes == 0) continue;
       // the widest column that every address of the state is a multiple of
-      const uint64_t all = static_cast<uint64_t>(s.seg_bytes) | reinterpret_cast<uintptr_t>(s.src) |
+      const uint64_t all = static_cast<uint64_t>(bytes) | reinterpret_cast<uintptr_t>(s.src) |
                            reinterpret_cast<uintptr_t>(s.dst) | static_cast<uint64_t>(s.src_row) |
                            static_cast<uint64_t>(s.dst_row) |
                            (s.n_seg > 1 ? static_cast<uint64_t>(s.src_seg) | static_cast<uint64_t>(s.dst_seg) : 0u);
       uint32_t grain = 16;
       while (all % grain != 0) grain /= 2;
-      const uint64_t cols = static_cast<uint64_t>(s.seg_bytes) / grain;
+      const uint64_t cols = static_cast<uint64_t>(bytes) / grain;
       // (columns are counted in 32 bits)
       if (cols >= (uint64_t{1} << 31) / static_cast<uint64_t>(s.n_seg)) return DETLM_EINVAL;
       if (pass == 0) continue;

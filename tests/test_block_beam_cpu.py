@@ -81,8 +81,8 @@ def test_quantize_blocks_refuses(lib, args):
 
 def test_no_rows_are_no_work(lib):
     assert lib.detlm_quantize_blocks(None, 0, 0, 64, 1, None, None, None) == b.DETLM_OK
-    assert lib.detlm_beam_reorder(None, 0, None, 0, 4, 4, None) == b.DETLM_OK
-    assert lib.detlm_beam_reorder(None, 0, None, 3, 4, 4, None) == b.DETLM_OK
+    assert lib.detlm_beam_reorder(None, 0, None, 0, 4, 4, -1, None) == b.DETLM_OK
+    assert lib.detlm_beam_reorder(None, 0, None, 3, 4, 4, -1, None) == b.DETLM_OK
 
 
 def test_calls_on_null_handles(lib):
@@ -103,12 +103,12 @@ def test_create_refuses_e4m3_heads_of_other_sizes(lib):
         b.DETLM_EUNSUPPORTED
 
 
-def state(src=P, dst=P + 4096, row=1024, dst_row=None, seg=64, dst_seg=None, n_seg=2, size=32):
+def state(src=P, dst=P + 4096, row=1024, dst_row=None, seg=64, dst_seg=None, n_seg=2, size=32, position=0):
     s = (b._State * 1)()
     s[0].src, s[0].dst = src, dst
     s[0].src_row, s[0].dst_row = row, row if dst_row is None else dst_row
     s[0].src_seg, s[0].dst_seg = seg, seg if dst_seg is None else dst_seg
-    s[0].n_seg, s[0].seg_bytes = n_seg, size
+    s[0].n_seg, s[0].seg_bytes, s[0].position_bytes = n_seg, size, position
     return s
 
 
@@ -124,6 +124,7 @@ def state(src=P, dst=P + 4096, row=1024, dst_row=None, seg=64, dst_seg=None, n_s
     (state(dst=None), P, 1, 4, 4),
     (state(n_seg=-1), P, 1, 4, 4),
     (state(size=-1), P, 1, 4, 4),
+    (state(position=-4), P, 1, 4, 4),
     (state(dst=P), P, 1, 4, 5),                  # in place to more rows
     (state(dst=P, dst_row=512), P, 1, 4, 4),     # in place with another stride
     (state(dst=P, dst_seg=32), P, 1, 4, 4),
@@ -132,12 +133,12 @@ def state(src=P, dst=P + 4096, row=1024, dst_row=None, seg=64, dst_seg=None, n_s
 ])
 def test_reorder_refuses(lib, s, parent, n_seq, beams_in, beams_out):
     assert lib.detlm_beam_reorder(ctypes.addressof(s), 1, parent, n_seq, beams_in, beams_out,
-                                  None) == b.DETLM_EINVAL
+                                  -1, None) == b.DETLM_EINVAL
 
 
 def test_reorder_refuses_a_table_that_is_missing(lib):
-    assert lib.detlm_beam_reorder(None, 1, P, 1, 4, 4, None) == b.DETLM_EINVAL
-    assert lib.detlm_beam_reorder(None, -1, P, 1, 4, 4, None) == b.DETLM_EINVAL
+    assert lib.detlm_beam_reorder(None, 1, P, 1, 4, 4, -1, None) == b.DETLM_EINVAL
+    assert lib.detlm_beam_reorder(None, -1, P, 1, 4, 4, -1, None) == b.DETLM_EINVAL
 
 
 # --------------------------------------------------------------------- binding
@@ -206,13 +207,14 @@ def test_states_layouts_and_refusals(calls):
     st = b.BeamStates([cache, tokens], token_dim=[2, 1])
     st.reorder(parent, used=7)
     (_, args), = calls
-    assert args[1:6] == (2, parent.data_ptr(), 2, 4, 4)
+    assert args[1:7] == (2, parent.data_ptr(), 2, 4, 4, 7)
     e = st._table[0]
-    assert (e.src, e.dst, e.src_row, e.src_seg, e.n_seg, e.seg_bytes) == \
-        (cache.data_ptr(), cache.data_ptr(), 3 * 20 * 32, 20 * 32, 3, 7 * 32)
-    assert (st._table[1].n_seg, st._table[1].seg_bytes) == (1, 28)
-    st.reorder(parent)                                   # all of it again
-    assert (st._table[0].seg_bytes, st._table[1].seg_bytes) == (20 * 32, 80)
+    assert (e.src, e.dst, e.src_row, e.src_seg, e.n_seg, e.seg_bytes, e.position_bytes) == \
+        (cache.data_ptr(), cache.data_ptr(), 3 * 20 * 32, 20 * 32, 3, 20 * 32, 32)
+    e = st._table[1]
+    assert (e.n_seg, e.seg_bytes, e.position_bytes) == (1, 80, 4)
+    st.reorder(parent)                                   # all of it
+    assert calls.pop()[1][6] == -1
     # positions first, no positions, slices of one tensor
     assert [getattr(b.BeamStates([cache.view(8, 20, 3, 16)], token_dim=1)._table[0], k)
             for k in ("n_seg", "seg_bytes")] == [1, 20 * 96]
