@@ -4,34 +4,33 @@
 
 namespace {
 
-// Blocks that the scan of a few rows is cut into, about (as many as run at
-// once), and the least tiles of a part (one round of a block).
-constexpr int64_t kScanBlocks = 608;
-
 int beam_tiles(const detlm_head* h) { return static_cast<int>((h->V + kScanTile - 1) / kScanTile); }
-int beam_parts(const detlm_head* h, int64_t rows) {
-  int64_t parts = (kScanBlocks + rows - 1) / rows;
-  const int64_t rounds = (beam_tiles(h) + kScanWarps - 1) / kScanWarps;
-  if (parts > rounds) parts = rounds;
-  if (parts > kBeamPartsMax) parts = kBeamPartsMax;
-  return static_cast<int>(parts < 1 ? 1 : parts);
+
+// The scan's blocks: as many as run at once, with four tiles each at least (a
+// block's cuts cost as much as a round), and so few that a row has at most
+// kBeamPartsMax parts: G / rows + 2 of G blocks.
+constexpr int64_t kScanLeast = 4;
+int scan_blocks(const detlm_head* h, int64_t rows, int fmt) {
+  int64_t g = static_cast<int64_t>(h->num_sms) * scan_resident(fmt);
+  const int64_t tiles = rows * beam_tiles(h);
+  if (g > tiles / kScanLeast) g = tiles / kScanLeast;
+  if (g > rows * (kBeamPartsMax - 2)) g = rows * (kBeamPartsMax - 2);
+  return static_cast<int>(g < 1 ? 1 : g);
 }
-// The tiles' sums and the parts' lists of up to `rows` rows (parts * rows grows
-// with the rows but for rounding: at most kScanBlocks + rows).
+// The tiles' sums and the parts' lists of up to `rows` rows: at most G + 2 rows
+// lists.
 size_t beam_tile_bytes(const detlm_head* h, int64_t rows) {
   return round256(static_cast<size_t>(rows) * beam_tiles(h) * sizeof(float2));
 }
 size_t beam_bytes(const detlm_head* h, int64_t rows, int n_out) {
-  const int64_t most = rows * kBeamPartsMax < kScanBlocks + rows ? rows * kBeamPartsMax : kScanBlocks + rows;
-  return beam_tile_bytes(h, rows) + static_cast<size_t>(most) * n_out * sizeof(u64);
+  const int64_t most = static_cast<int64_t>(h->num_sms) * scan_resident(QF_BF16);
+  const int64_t lists = (rows * (kBeamPartsMax - 2) < most ? rows * (kBeamPartsMax - 2) : most) + 2 * rows;
+  return beam_tile_bytes(h, rows) + static_cast<size_t>(lists) * n_out * sizeof(u64);
 }
 
 template <int FMT>
-cudaError_t launch_beam_scan(const BeamScanParams& p, cudaStream_t stream) {
-  const unsigned y = static_cast<unsigned>(p.rows < 65535 ? p.rows : 65535);
-  const unsigned z = static_cast<unsigned>((p.rows + y - 1) / y);
-  return launch_dependent(beam_scan_kernel<FMT>, dim3(static_cast<unsigned>(p.parts), y, z), kScanThreads,
-                          stream, p);
+cudaError_t launch_beam_scan(const BeamScanParams& p, int blocks, cudaStream_t stream) {
+  return launch_dependent(beam_scan_kernel<FMT>, dim3(static_cast<unsigned>(blocks)), kScanThreads, stream, p);
 }
 
 template <int KB>
@@ -79,17 +78,18 @@ int detlm_head_beam_select(detlm_head_t* h, const void* logits_dev, int logits_d
   p.finished = finished_dev;
   p.tile = static_cast<float2*>(h->bws);
   p.best = reinterpret_cast<u64*>(static_cast<uint8_t*>(h->bws) + beam_tile_bytes(h, rows));
-  p.rows = rows;
   p.V = static_cast<int32_t>(h->V);
   p.n_tiles = beam_tiles(h);
-  p.parts = beam_parts(h, rows);
+  p.tiles = rows * p.n_tiles;
+  const int fmt = type == OUT_F32 ? QF_FP32 : type == OUT_BF16 ? QF_BF16 : QF_FP16;
+  const int blocks = scan_blocks(h, rows, fmt);
+  p.parts = static_cast<int32_t>(blocks / rows) + 2;
   p.M = n_out;
-  p.cut = 64 + 3 * n_out;
   const float inv_t = 1.0f / temperature;
   p.c = kLog2eScore * inv_t;
-  cudaError_t e = type == OUT_F32    ? launch_beam_scan<QF_FP32>(p, stream)
-                  : type == OUT_BF16 ? launch_beam_scan<QF_BF16>(p, stream)
-                                     : launch_beam_scan<QF_FP16>(p, stream);
+  cudaError_t e = fmt == QF_FP32   ? launch_beam_scan<QF_FP32>(p, blocks, stream)
+                  : fmt == QF_BF16 ? launch_beam_scan<QF_BF16>(p, blocks, stream)
+                                   : launch_beam_scan<QF_FP16>(p, blocks, stream);
   if (e != cudaSuccess) return status_from_cuda(e);
   BeamMergeParams m;
   std::memset(&m, 0, sizeof(m));
@@ -102,13 +102,27 @@ int detlm_head_beam_select(detlm_head_t* h, const void* logits_dev, int logits_d
   m.out = out_score_dev;
   m.n_tiles = p.n_tiles;
   m.parts = p.parts;
+  m.tiles = p.tiles;
+  m.blocks = blocks;
   m.M = n_out;
   m.beams = beams;
   m.end_token = end_token;
   m.c = p.c;
   m.inv_t = inv_t;
-  e = launch_dependent(beam_merge_kernel, dim3(static_cast<unsigned>(n_seq)), kMergeBeamThreads, stream, m);
-  return status_from_cuda(e);
+  e = prepare_kernel<beam_merge_kernel>(0);
+  if (e != cudaSuccess) return status_from_cuda(e);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(n_seq));
+  cfg.blockDim = dim3(kMergeBeamThreads);
+  cfg.dynamicSmemBytes = merge_smem(beams, p.parts, n_out);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return status_from_cuda(cudaLaunchKernelEx(&cfg, beam_merge_kernel, m));
 }
 
 int detlm_beam_reorder(const detlm_beam_state_t* states, int n_states, const int32_t* parent_dev,

@@ -7,25 +7,27 @@
 // logits: within a row all scores move together, so a row's candidates are its
 // n_out largest logits, and the row's sum is needed for those alone.
 //
-// beam_scan_kernel reads the logits. A block takes a part of a row in ascending
-// order, kScanWarps tiles of kScanTile a round, each element in one register. Each
-// tile leaves its maximum and sum (in an order that its elements' places in the
-// row set, so they do not depend on how rows are cut into parts). The part's
-// largest logits collect in shared memory: an element is kept if it is above the
-// smallest of the M = n_out best so far, which after the first round few are
-// (about M log(V / 4096) more in the whole row). The first threshold comes from
-// the first round itself: the M-th largest of 128 maxima of 32 elements each.
-// When the list runs full it is sorted by counting and cut to M. An element is
-// compared as a 64-bit word: its order as a number, then the lower index first.
+// beam_scan_kernel reads the logits, once. Its blocks share the tiles (1024
+// logits) of all rows evenly, so the last block ends with the first whatever the
+// rows; a row that spans blocks has a part in each. A warp takes a tile a round.
+// Each tile leaves its maximum and sum (in an order that its elements' places in
+// the row set, so they do not depend on how rows are cut). The part's largest
+// logits collect in shared memory: an element is kept if it is above the
+// smallest of the M = n_out best at the last cut, and the list is cut to M after
+// rounds 1, 2, 4, 8, ...: about M entries a span. The first threshold comes from
+// the first round itself: the M-th largest of 128 maxima of 64 elements each. An
+// element is compared as a 64-bit word: its order as a number, then the lower
+// index first. Warps meet at the cuts only.
 //
-// beam_merge_kernel, a block a sequence: a warp a beam folds the tiles' sums in
-// ascending order and merges the parts' sorted lists (one lane a list, the best
-// head taken each time), then one warp merges the beams' lists by score.
+// beam_merge_kernel, a block a sequence: a warp a beam joins the tiles' sums in
+// a fixed tree and merges the parts' sorted lists, then the block merges the
+// beams' lists by score.
 //
 // The scan is bound by instruction issue and the exponentials' unit about as
 // much as by memory: an element costs a load, its conversion, a maximum, a
 // fused multiply-add, an exponential, an addition and a comparison.
 #pragma once
+#include "quant_kernels.cuh"
 #include "score_kernels.cuh"
 
 namespace detlm {
@@ -35,10 +37,12 @@ constexpr int kBeamOutMax = 64;           // continuations a sequence can ask fo
 constexpr int kBeamPartsMax = 32;         // parts of a row (a lane each in the merge)
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanTile = 512;            // logits of a tile: 16 a lane
+constexpr int kScanTile = 1024;           // logits of a tile: 32 a lane
 constexpr int kScanPer = kScanTile / 32;
 constexpr int kScanRound = kScanWarps * kScanTile;
 constexpr int kScanCap = 1024;            // entries of the list
+// blocks of an SM (their registers: a tile and the next)
+__host__ __device__ constexpr int scan_resident(int fmt) { return fmt == QF_FP32 ? 2 : 3; }
 
 using u64 = unsigned long long;
 
@@ -48,9 +52,8 @@ struct BeamScanParams {
   const uint8_t* finished;  // optional [rows]
   float2* tile;             // [rows][n_tiles]: maximum, sum
   u64* best;                // [rows][parts][M], sorted, 0 behind the last
-  int64_t rows;
+  int64_t tiles;            // of all rows
   int32_t V, n_tiles, parts, M;
-  int32_t cut;              // entries above which the list is cut before the next round
   float c;                  // log2(e) / T
 };
 struct BeamMergeParams {
@@ -61,9 +64,18 @@ struct BeamMergeParams {
   int32_t* parent;          // [n_seq][M]
   int32_t* token;
   float* out;
+  int64_t tiles;
   int32_t n_tiles, parts, M, beams, end_token;
+  int32_t blocks;           // of the scan
   float c, inv_t;
 };
+
+// The scan's block b takes tiles [scan_first(b), scan_first(b + 1)) of all rows';
+// scan_block is the block that a tile falls to.
+__device__ __forceinline__ int64_t scan_first(int64_t tiles, int blocks, int b) { return tiles * b / blocks; }
+__device__ __forceinline__ int scan_block(int64_t tiles, int blocks, int64_t t) {
+  return static_cast<int>(((t + 1) * blocks - 1) / tiles);
+}
 
 // A beam that proposes continuations of its own.
 __device__ __forceinline__ bool beam_open(const float* score, const uint8_t* finished, int64_t r) {
@@ -96,14 +108,20 @@ __device__ __forceinline__ int scan_cut(u64* list, int n, int M) {
   return min(n, M);
 }
 
-// A lane's share of a tile as loaded: 16 numbers of 32 bits, or eight words of
-// two neighbours of 16.
+// A lane's share of a tile as loaded: 32 numbers of 32 bits, or 16 words of two
+// neighbours of 16.
 template <int FMT>
 struct ScanTile {
   static constexpr int kWords = FMT == QF_FP32 ? kScanPer : kScanPer / 2;
   uint32_t w[kWords];
+  // nothing: the type's -inf
+  static constexpr uint32_t kNone = FMT == QF_FP32 ? 0xFF800000u : FMT == QF_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = kNone;
+  }
   // Tile `at` of a row of V; `words`: a row of 16-bit numbers starts on a word.
-  // (A loop over the whole loads alone, so that all are under way together.)
+  // (The loads stand alone, so that all are under way together.)
   __device__ __forceinline__ void load(const uint8_t* row, int at, int V, bool words) {
     const int lane = threadIdx.x & 31;
     if (words && at + kScanTile <= V) {
@@ -115,32 +133,62 @@ struct ScanTile {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int k = at + 32 * i + lane;
-        w[i] = k < V ? __ldg(p + k) : 0xFF800000u;
+        w[i] = k < V ? __ldg(p + k) : kNone;
       }
     } else {
-      // (beyond the row's end: the type's -inf)
-      constexpr uint32_t kNone = FMT == QF_BF16 ? 0xFF80u : 0xFC00u;
       const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+      if (at + kScanTile <= V) {           // (between words: element by element)
+        p += at + 2 * lane;
+        uint16_t lo[kWords], hi[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          lo[i] = __ldg(p + 64 * i);
+          hi[i] = __ldg(p + 64 * i + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = lo[i] | (static_cast<uint32_t>(hi[i]) << 16);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int k = at + 64 * i + 2 * lane;
-        const uint32_t lo = k < V ? __ldg(p + k) : kNone;
-        const uint32_t hi = k + 1 < V ? __ldg(p + k + 1) : kNone;
+        const uint32_t lo = k < V ? __ldg(p + k) : kNone & 0xFFFFu;
+        const uint32_t hi = k + 1 < V ? __ldg(p + k + 1) : kNone & 0xFFFFu;
         w[i] = lo | (hi << 16);
       }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[kScanPer]) const {
+  // elements 2 i and 2 i + 1 of the lane
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (FMT == QF_FP32)
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else
+      return unpack16(w[i], FMT == QF_FP16);
+  }
+  // the largest of each eight elements, NaN aside
+  __device__ __forceinline__ void maxima(float (&m)[kScanPer / 8]) const {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
+    for (int g = 0; g < kScanPer / 8; ++g) {
       if constexpr (FMT == QF_FP32) {
-        x[i] = __uint_as_float(w[i]);
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[i] = fmaxf(__uint_as_float(w[8 * g + i]), __uint_as_float(w[8 * g + 4 + i]));
+        m[g] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
       } else {
-        const float2 v = unpack16(w[i], FMT == QF_FP16);
-        x[2 * i] = v.x;
-        x[2 * i + 1] = v.y;
+        const uint32_t y = max2(max2(w[4 * g], w[4 * g + 1]), max2(w[4 * g + 2], w[4 * g + 3]));
+        const float2 v = unpack16(y, FMT == QF_FP16);
+        m[g] = fmaxf(v.x, v.y);
       }
     }
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    if constexpr (FMT == QF_BF16) {
+      const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
   }
 };
 // index in the row of a lane's element i of the tile at `at`
@@ -151,158 +199,162 @@ __device__ __forceinline__ int scan_index(int at, int i) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamScanParams p) {
-  grid_dep_launch();
-  grid_dep_wait();
+__global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_kernel(const BeamScanParams p) {
   __shared__ u64 list[kScanCap];
   __shared__ __align__(16) uint32_t top[128];
   __shared__ int count;
   __shared__ uint32_t level;
-  const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
-  if (r >= p.rows || !beam_open(p.score, p.finished, r)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t size = FMT == QF_FP32 ? 4 : 2;
-  const uint8_t* row = static_cast<const uint8_t*>(p.logits) + static_cast<size_t>(r) * p.V * size;
-  const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;   // (rows of 32-bit numbers always)
-  // whole tiles to a part
-  const int t0 = static_cast<int>(static_cast<int64_t>(p.n_tiles) * blockIdx.x / p.parts);
-  const int t1 = static_cast<int>(static_cast<int64_t>(p.n_tiles) * (blockIdx.x + 1) / p.parts);
-  u64 last = 0;                           // the M-th best entry at the last cut
-  float above = -INFINITY;                // an entry is larger (-inf is none)
-  auto cut = [&](int have) {
-    const int n = scan_cut(list, have, p.M);
-    if (n == p.M) {
-      // (what comes later has a higher index: of equal logits it is the lower)
-      last = list[p.M - 1];
-      above = score_unkey(static_cast<uint32_t>(last >> 32));
+  const int blocks = static_cast<int>(gridDim.x);
+  const int64_t end = scan_first(p.tiles, blocks, blockIdx.x + 1);
+  grid_dep_wait();
+  for (int64_t from = scan_first(p.tiles, blocks, blockIdx.x); from < end;) {
+    // the block's part of row r: tiles [t0, t1)
+    const int64_t r = from / p.n_tiles;
+    const int t0 = static_cast<int>(from - r * p.n_tiles);
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(p.n_tiles), t0 + end - from));
+    from += t1 - t0;
+    if (!beam_open(p.score, p.finished, r)) continue;
+    const uint8_t* row = static_cast<const uint8_t*>(p.logits) + static_cast<size_t>(r) * p.V * size;
+    const bool words = (reinterpret_cast<uintptr_t>(row) & 3) == 0;   // (rows of 32-bit numbers always)
+    ScanTile<FMT> next;
+    if (t0 + warp < t1) next.load(row, (t0 + warp) * kScanTile, p.V, words);
+    u64 last = 0;                         // the M-th best entry at the last cut
+    float above = -INFINITY;              // an entry is larger (-inf is none)
+    int n = 0;                            // entries after the last cut
+    auto cut = [&]() {
+      n = scan_cut(list, count, p.M);
+      if (n == p.M) {
+        // (what comes later has a higher index: of equal logits it is the lower)
+        last = list[p.M - 1];
+        above = score_unkey(static_cast<uint32_t>(last >> 32));
+      }
+      if (threadIdx.x == 0) count = n;
+      __syncthreads();
+    };
+    __syncthreads();                      // the previous part is written
+    if (threadIdx.x == 0) {
+      count = 0;
+      level = 0;
     }
-    if (threadIdx.x == 0) count = n;
     __syncthreads();
-  };
-  if (threadIdx.x == 0) count = 0;
-  __syncthreads();
-  ScanTile<FMT> next;
-  if (t0 + warp < t1) next.load(row, (t0 + warp) * kScanTile, p.V, words);
-  for (int tr = t0; tr < t1; tr += kScanWarps) {
-    const int t = tr + warp;
-    const int at = t * kScanTile;
-    float x[kScanPer];
-    float m = -INFINITY;
-    if (t < t1) {
-      next.values(x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kScanPer; ++i) x[i] = -INFINITY;
-    }
-    // the next round's tile is on its way during this one
-    if (t + kScanWarps < t1) next.load(row, at + kScanRound, p.V, words);
-    {
-      // (a tree: the maximum's bits are the same in any order)
-      float y[kScanPer / 2];
-#pragma unroll
-      for (int i = 0; i < kScanPer / 2; ++i) y[i] = fmaxf(x[i], x[i + kScanPer / 2]);
-#pragma unroll
-      for (int o = kScanPer / 4; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < o; ++i) y[i] = fmaxf(y[i], y[i + o]);
-      m = y[0];
-    }
-    const float lane_max = m;             // NaN aside
-    if (tr == t0) {
-      // the first threshold: the M-th largest maximum of two lanes
-      const float pm = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      if ((lane & 1) == 0) top[warp * 16 + (lane >> 1)] = score_key(pm);
-      if (threadIdx.x == 0) level = 0;
-      __syncthreads();
-      if (threadIdx.x < 128) {
-        const uint32_t me = top[threadIdx.x];
-        int larger = 0, equal = 0;
+    const int rounds = (t1 - t0 + kScanWarps - 1) / kScanWarps;
+    for (int done = 0; done < rounds;) {
+      // a span: rounds 0, 1, 2 to 3, 4 to 7, ...
+      const int stop = min(rounds, max(1, 2 * done));
+      bool over = false;
+      for (int k = done; k < stop; ++k) {
+        const int t = t0 + k * kScanWarps + warp;
+        const int at = t * kScanTile;
+        ScanTile<FMT> x;
+        if (t < t1) x = next;
+        else x.none();
+        // the next round's tile is on its way during this one
+        if (t + kScanWarps < t1) next.load(row, at + kScanRound, p.V, words);
+        float g[kScanPer / 8];
+        x.maxima(g);
+        float m = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
+        if (k == 0) {
+          // the first threshold: the M-th largest maximum of two lanes
+          const float pm = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          if ((lane & 1) == 0) top[warp * 16 + (lane >> 1)] = score_key(pm);
+          __syncthreads();
+          if (threadIdx.x < 128) {
+            const uint32_t me = top[threadIdx.x];
+            int larger = 0, equal = 0;
 #pragma unroll 8
-        for (int j = 0; j < 128; j += 4) {
-          const uint4 o = *reinterpret_cast<const uint4*>(&top[j]);
-          larger += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
-          equal += (o.x == me) + (o.y == me) + (o.z == me) + (o.w == me);
-        }
-        if (larger < p.M && p.M <= larger + equal) level = me;
-      }
-      __syncthreads();
-      // one step below it, so that its equals are entries (below +0 comes the
-      // first negative number: keys know no -0); -inf stays
-      const uint32_t key = level;
-      if (key > score_key(-INFINITY)) above = score_unkey(key == 0x80000000u ? key - 2 : key - 1);
-    }
-    const float wm = score_unkey(__reduce_max_sync(0xffffffffu, score_key(m)));
-    // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf
-    const float base = wm == -INFINITY ? 0.0f : wm;
-    float2 e[kScanPer / 2];
-#pragma unroll
-    for (int i = 0; i < kScanPer / 2; ++i) {
-      float2 y = make_float2(x[2 * i], x[2 * i + 1]);
-      add2_rn(y.x, y.y, -base, -base);
-      y = mul2_rn(y, make_float2(p.c, p.c));
-      e[i] = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-    }
-#pragma unroll
-    for (int o = kScanPer / 4; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < o; ++i) add2_rn(e[i].x, e[i].y, e[i + o].x, e[i + o].y);
-    float sum = e[0].x + e[0].y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && t < t1) p.tile[static_cast<size_t>(r) * p.n_tiles + t] = make_float2(wm, sum);
-
-    // entries above the threshold
-    bool over = false;
-    if (lane_max > above) {
-#pragma unroll
-      for (int i = 0; i < kScanPer; ++i)
-        if (x[i] > above) {
-          const int k = atomicAdd(&count, 1);
-          if (k < kScanCap) list[k] = order_word(score_key(x[i]), scan_index<FMT>(at, i));
-          over |= k >= p.cut;
-        }
-    }
-    // (nobody looks at the count but after this, and then nobody adds to it)
-    if (__syncthreads_or(over)) {
-      const int have = count;
-      if (have <= kScanCap) {
-        cut(have);
-      } else {
-        // more than the list holds (long runs of equal or rising logits): this
-        // round again, after the entries of the rounds before it (their indices
-        // are lower), one element a thread at a time, cut whenever the next
-        // could run over
-        u64 kept[kScanCap / kScanThreads];
-#pragma unroll
-        for (int i = 0; i < kScanCap / kScanThreads; ++i) kept[i] = list[threadIdx.x + i * kScanThreads];
-        __syncthreads();
-        if (threadIdx.x == 0) count = 0;
-        __syncthreads();
-        const uint32_t before = 0xFFFFFFFFu - static_cast<uint32_t>(tr * kScanTile);
-#pragma unroll
-        for (int i = 0; i < kScanCap / kScanThreads; ++i)
-          if (static_cast<uint32_t>(kept[i]) > before) list[atomicAdd(&count, 1)] = kept[i];
-        __syncthreads();
-        for (int i = 0; i < kScanPer; ++i) {
-          const int now = count;
+            for (int j = 0; j < 128; j += 4) {
+              const uint4 o = *reinterpret_cast<const uint4*>(&top[j]);
+              larger += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
+              equal += (o.x == me) + (o.y == me) + (o.z == me) + (o.w == me);
+            }
+            if (larger < p.M && p.M <= larger + equal) level = me;
+          }
           __syncthreads();
-          if (now > kScanCap - kScanThreads) cut(now);
-          float y = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < kScanPer; ++k) y = k == i ? x[k] : y;
-          const u64 word = order_word(score_key(y), scan_index<FMT>(at, i));
-          if (y > -INFINITY && word > last) list[atomicAdd(&count, 1)] = word;
-          __syncthreads();
+          // one step below it, so that its equals are entries (below +0 comes
+          // the first negative number: keys know no -0); -inf stays
+          const uint32_t key = level;
+          if (key > score_key(-INFINITY)) above = score_unkey(key == 0x80000000u ? key - 2 : key - 1);
         }
-        cut(count);
+        // entries above the threshold
+        if (m > above) {
+          auto add = [&](float y, int i) {
+            const int to = atomicAdd(&count, 1);
+            if (to < kScanCap) list[to] = order_word(score_key(y), scan_index<FMT>(at, i));
+            else over = true;
+          };
+#pragma unroll
+          for (int j = 0; j < kScanPer / 8; ++j) {
+            if (!(g[j] > above)) continue;
+#pragma unroll
+            for (int i = 4 * j; i < 4 * j + 4; ++i) {
+              const float2 v = x.pair(i);
+              if (v.x > above) add(v.x, 2 * i);
+              if (v.y > above) add(v.y, 2 * i + 1);
+            }
+          }
+        }
+        // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf
+        m = score_unkey(__reduce_max_sync(0xffffffffu, score_key(m)));
+        const float base = m == -INFINITY ? 0.0f : m;
+        float2 e[4];
+#pragma unroll
+        for (int i = 0; i < kScanPer / 2; ++i) {
+          float2 y = x.pair(i);
+          add2_rn(y.x, y.y, -base, -base);
+          y = mul2_rn(y, make_float2(p.c, p.c));
+          y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          if (i < 4) e[i] = y;
+          else add2_rn(e[i & 3].x, e[i & 3].y, y.x, y.y);
+        }
+        add2_rn(e[0].x, e[0].y, e[1].x, e[1].y);
+        add2_rn(e[2].x, e[2].y, e[3].x, e[3].y);
+        add2_rn(e[0].x, e[0].y, e[2].x, e[2].y);
+        float sum = e[0].x + e[0].y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0 && t < t1) p.tile[static_cast<size_t>(r) * p.n_tiles + t] = make_float2(m, sum);
       }
+      // (nobody looks at the count but after this, and then nobody adds to it)
+      if (__syncthreads_or(over)) {
+        // more than the list holds (long runs of equal or rising logits): the
+        // span again, after the n entries before it, one element a thread at a
+        // time, cut whenever the next could run over
+        if (threadIdx.x == 0) count = n;
+        __syncthreads();
+        for (int k = done; k < stop; ++k) {
+          const int t = t0 + k * kScanWarps + warp;
+          ScanTile<FMT> x;
+          if (t < t1) x.load(row, t * kScanTile, p.V, words);
+          else x.none();
+          for (int i = 0; i < kScanPer; ++i) {
+            const int now = count;
+            __syncthreads();
+            if (now > kScanCap - kScanThreads) cut();
+            float y = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kScanPer / 2; ++j) {
+              const float2 v = x.pair(j);
+              y = 2 * j == i ? v.x : 2 * j + 1 == i ? v.y : y;
+            }
+            const u64 word = order_word(score_key(y), scan_index<FMT>(t * kScanTile, i));
+            if (y > -INFINITY && word > last) list[atomicAdd(&count, 1)] = word;
+            __syncthreads();
+          }
+        }
+      }
+      cut();
+      done = stop;
     }
+    // the part's best, sorted; nothing behind the last
+    const int part = static_cast<int>(blockIdx.x) - scan_block(p.tiles, blocks, r * p.n_tiles);
+    u64* out = p.best + (static_cast<size_t>(r) * p.parts + part) * p.M;
+    for (int i = threadIdx.x; i < p.M; i += kScanThreads) out[i] = i < n ? list[i] : 0;
   }
-  // the part's best, sorted; nothing behind the last
-  __syncthreads();
-  const int n = scan_cut(list, count, p.M);
-  u64* out = p.best + (static_cast<size_t>(r) * p.parts + blockIdx.x) * p.M;
-  for (int i = threadIdx.x; i < p.M; i += kScanThreads) out[i] = i < n ? list[i] : 0;
+  // (only now: blocks of the merge that wait would take the place of blocks that
+  // read)
+  grid_dep_launch();
 }
 
 // Two tiles' maximum and sum as one (the same bits in either order).
@@ -315,25 +367,46 @@ __device__ __forceinline__ float2 tile_join(float2 a, float2 b, float c) {
 
 constexpr int kMergeBeamThreads = 256;
 
+// The block's shared memory: a warp's lists of a beam, for as many warps as have
+// one (later the merge's entries, 8 bytes each too); then every beam's candidates [beams][M]: scores, tokens, and their number.
+__host__ __device__ inline size_t merge_lists(int beams, int parts, int M) {
+  const int warps = beams < kMergeBeamThreads / 32 ? beams : kMergeBeamThreads / 32;
+  return static_cast<size_t>(warps * parts > beams ? warps * parts : beams) * M;
+}
+__host__ __device__ inline size_t merge_smem(int beams, int parts, int M) {
+  return merge_lists(beams, parts, M) * sizeof(u64) + static_cast<size_t>(beams) * (M * 8 + 4) +
+         (kMergeBeamThreads / 32 + 1) * 4;
+}
+
+// Both merges place an entry by counting those before it, once a threshold has
+// taken most of the others out. (Taking the best head M times over, or counting
+// by bisection in each list, takes longer: every step waits for the one before.)
 __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const BeamMergeParams p) {
   grid_dep_launch();
   grid_dep_wait();
-  __shared__ float score[kBeamMax][kBeamOutMax];
-  __shared__ int32_t token[kBeamMax][kBeamOutMax];
-  __shared__ int found[kBeamMax];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t seq = blockIdx.x;
+  const int M = p.M;
+  u64* list = reinterpret_cast<u64*>(smem_raw) + static_cast<size_t>(warp) * p.parts * M;
+  float* score = reinterpret_cast<float*>(reinterpret_cast<u64*>(smem_raw) + merge_lists(p.beams, p.parts, M));
+  int32_t* token = reinterpret_cast<int32_t*>(score + p.beams * M);
+  int* found = token + p.beams * M;
+  int* count = found + p.beams;                // a number of each warp
+  int& kept = count[kMergeBeamThreads / 32];
+  if (threadIdx.x < p.beams) found[threadIdx.x] = 0;
+  __syncthreads();
   for (int b = warp; b < p.beams; b += kMergeBeamThreads / 32) {
     const int64_t r = seq * p.beams + b;
     const float own = p.score[r];
-    int n = 0;
     if (beam_open(p.score, p.finished, r)) {
-      // the first entries of the parts' lists are on their way meanwhile
-      const u64* lists = p.best + static_cast<size_t>(r) * p.parts * p.M;
-      const u64* mine = lists + static_cast<size_t>(min(lane, p.parts - 1)) * p.M;
-      u64 head = lane < p.parts ? mine[0] : 0;
-      u64 next = lane < p.parts && p.M > 1 ? mine[1] : 0;
-      int at = 2;
+      // the row's parts
+      const int parts = scan_block(p.tiles, p.blocks, (r + 1) * p.n_tiles - 1) -
+                        scan_block(p.tiles, p.blocks, r * p.n_tiles) + 1;
+      const u64* best = p.best + static_cast<size_t>(r) * p.parts * M;
+      __syncwarp();                            // the beam before has been read
+#pragma unroll 4
+      for (int i = lane; i < parts * M; i += 32) list[i] = best[i];
       float2 t = make_float2(-INFINITY, 0.0f);
       const float2* tiles = p.tile + static_cast<size_t>(r) * p.n_tiles;
 #pragma unroll 4
@@ -342,69 +415,109 @@ __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const Bea
       for (int o = 16; o > 0; o >>= 1)
         t = tile_join(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, o),
                                      __shfl_xor_sync(0xffffffffu, t.y, o)), p.c);
+      __syncwarp();
       // a row with a NaN or +inf, or with nothing but -inf, proposes nothing
+      if (!(t.y > 0.0f && isfinite(t.y))) continue;
       const float log_s = logf(t.y);
-      if (t.y > 0.0f && isfinite(t.y)) {
-        for (int j = 0; j < p.M; ++j) {
-          u64 best;
-          if (p.parts == 1) {
-            best = mine[j];
-          } else {
-            const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(head >> 32));
-            const uint32_t low = static_cast<uint32_t>(head >> 32) == hi ? static_cast<uint32_t>(head) : 0u;
-            const uint32_t lo = __reduce_max_sync(0xffffffffu, low);
-            best = (static_cast<u64>(hi) << 32) | lo;
-            if (head == best && best != 0) {
-              head = next;
-              next = at < p.M ? mine[at] : 0;
-              ++at;
-            }
-          }
-          if (best == 0) break;
-          const float z = score_unkey(static_cast<uint32_t>(best >> 32));
-          const float s = __fadd_rn(own, __fsub_rn(__fmul_rn(__fsub_rn(z, t.x), p.inv_t), log_s));
-          if (!(s > -INFINITY)) break;         // (and those behind it score no more)
-          if (lane == 0) {
-            score[b][j] = s;
-            token[b][j] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-          }
-          n = j + 1;
-        }
+      // entries below either bound are not among the M best: the least of the
+      // lists' j-th entries, as j of each make M; the largest M-th entry
+      const uint32_t* key = reinterpret_cast<const uint32_t*>(list) + 1;
+      const int j = (M + parts - 1) / parts - 1;
+      const uint32_t low = __reduce_min_sync(0xffffffffu, lane < parts ? key[2 * (lane * M + j)] : 0xFFFFFFFFu);
+      const uint32_t high = __reduce_max_sync(0xffffffffu, lane < parts ? key[2 * (lane * M + M - 1)] : 0u);
+      const uint32_t least = max(max(low, high), 1u);
+      int n = 0;
+      for (int i0 = 0; i0 < parts * M; i0 += 32) {
+        const u64 word = i0 + lane < parts * M ? list[i0 + lane] : 0;
+        const bool stays = static_cast<uint32_t>(word >> 32) >= least;
+        const uint32_t stay = __ballot_sync(0xffffffffu, stays);     // (all have read)
+        if (stays) list[n + __popc(stay & ((1u << lane) - 1))] = word;
+        n += __popc(stay);
       }
-    } else if (isfinite(own)) {                // finished: stays as it is
-      if (lane == 0) {
-        score[b][0] = own;
-        token[b][0] = p.end_token;
+      __syncwarp();
+      for (int i = lane; i < n; i += 32) {
+        const u64 word = list[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) rank += list[k] > word;
+        if (rank >= M) continue;
+        const float z = score_unkey(static_cast<uint32_t>(word >> 32));
+        const float s = __fadd_rn(own, __fsub_rn(__fmul_rn(__fsub_rn(z, t.x), p.inv_t), log_s));
+        if (!(s > -INFINITY)) continue;        // (and those behind it score no more)
+        score[b * M + rank] = s;
+        token[b * M + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(word));
+        atomicMax(&found[b], rank + 1);
       }
-      n = 1;
+    } else if (isfinite(own) && lane == 0) {   // finished: stays as it is
+      score[b * M] = own;
+      token[b * M] = p.end_token;
+      found[b] = 1;
     }
-    if (lane == 0) found[b] = n;
   }
   __syncthreads();
-  if (warp != 0) return;
-  // the beams' lists, each in falling order; of equal scores the lower beam's
-  const int mine = lane < p.beams ? found[lane] : 0;
-  int at = 0;
-  uint32_t head = mine > 0 ? score_key(score[lane][0]) : 0u;
-  const size_t o = static_cast<size_t>(seq) * p.M;
-  for (int j = 0; j < p.M; ++j) {
-    const uint32_t best = __reduce_max_sync(0xffffffffu, head);
-    const int who = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
-    if (best == 0u) {                          // no candidate is left
-      for (int k = j + lane; k < p.M; k += 32) {
-        p.parent[o + k] = -1;
-        p.token[o + k] = -1;
-        p.out[o + k] = -INFINITY;
-      }
-      break;
+  // The beams' candidates, each beam's in falling order: score, then beam, then
+  // place. The M-th best score by bisection of its bits, where the candidates
+  // are many.
+  const size_t o = static_cast<size_t>(seq) * M;
+  const int all_places = p.beams * M;
+  uint32_t least = 1;
+  if (all_places > 2 * kMergeBeamThreads) {
+    constexpr int kMine = kBeamMax * kBeamOutMax / kMergeBeamThreads;
+    uint32_t mine[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = threadIdx.x + k * kMergeBeamThreads;
+      mine[k] = i < all_places && i % M < found[i / M] ? score_key(score[i]) : 0u;
     }
-    if (lane == who) {
-      p.parent[o + j] = lane;
-      p.token[o + j] = token[lane][at];
-      p.out[o + j] = score[lane][at];
-      ++at;
-      head = at < mine ? score_key(score[lane][at]) : 0u;
+    least = 0;
+    for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+      const uint32_t at = least | bit;
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) n += mine[k] >= at;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) count[warp] = n;
+      __syncthreads();
+      int all = 0;
+#pragma unroll
+      for (int k = 0; k < kMergeBeamThreads / 32; ++k) all += count[k];
+      if (all >= M) least = at;
+      __syncthreads();
     }
+    least = max(least, 1u);
+  }
+  // those at least as good, in order of their places
+  if (threadIdx.x == 0) kept = 0;
+  __syncthreads();
+  uint2* entry = reinterpret_cast<uint2*>(smem_raw);      // score, place (the lists are done with)
+  for (int i = threadIdx.x; i < all_places; i += kMergeBeamThreads) {
+    if (i % M >= found[i / M]) continue;
+    const uint32_t x = score_key(score[i]);
+    if (x >= least) entry[atomicAdd(&kept, 1)] = make_uint2(x, static_cast<uint32_t>(i));
+  }
+  __syncthreads();
+  const int n = kept;
+  for (int i = threadIdx.x; i < n; i += kMergeBeamThreads) {
+    const uint2 me = entry[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const uint2 x = entry[k];
+      rank += x.x > me.x || (x.x == me.x && x.y < me.y);
+    }
+    if (rank >= M) continue;
+    const int place = static_cast<int>(me.y);
+    p.parent[o + rank] = place / M;
+    p.token[o + rank] = token[place];
+    p.out[o + rank] = score[place];
+  }
+  // places without a candidate
+  int all = 0;
+  for (int k = 0; k < p.beams; ++k) all += found[k];
+  for (int j = all + threadIdx.x; j < M; j += kMergeBeamThreads) {
+    p.parent[o + j] = -1;
+    p.token[o + j] = -1;
+    p.out[o + j] = -INFINITY;
   }
 }
 
