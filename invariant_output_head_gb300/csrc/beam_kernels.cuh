@@ -14,7 +14,7 @@
 // the row set, so they do not depend on how rows are cut). The part's largest
 // logits collect in shared memory: an element is kept if it is above the
 // smallest of the M = n_out best at the last cut, and the list is cut to M after
-// rounds 1, 2, 4, 8, ...: about M entries a span. The first threshold comes from
+// rounds 4, 16, 64: about 3 M entries a span. The first threshold comes from
 // the first round itself: the M-th largest of 128 maxima of 64 elements each. An
 // element is compared as a 64-bit word: its order as a number, then the lower
 // index first. Warps meet at the cuts only.
@@ -198,6 +198,23 @@ __device__ __forceinline__ int scan_index(int at, int i) {
   return FMT == QF_FP32 ? at + 32 * i + lane : at + 64 * (i >> 1) + 2 * lane + (i & 1);
 }
 
+// The sum of 2^f over a lane's elements, in a fixed order.
+template <int FMT, typename F>
+__device__ __forceinline__ float scan_sum(const ScanTile<FMT>& x, F f) {
+  float2 e[4];
+#pragma unroll
+  for (int i = 0; i < kScanPer / 2; ++i) {
+    float2 y = f(x.pair(i));
+    y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    if (i < 4) e[i] = y;
+    else add2_rn(e[i & 3].x, e[i & 3].y, y.x, y.y);
+  }
+  add2_rn(e[0].x, e[0].y, e[1].x, e[1].y);
+  add2_rn(e[2].x, e[2].y, e[3].x, e[3].y);
+  add2_rn(e[0].x, e[0].y, e[2].x, e[2].y);
+  return e[0].x + e[0].y;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_kernel(const BeamScanParams p) {
   __shared__ u64 list[kScanCap];
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
     if (t0 + warp < t1) next.load(row, (t0 + warp) * kScanTile, p.V, words);
     u64 last = 0;                         // the M-th best entry at the last cut
     float above = -INFINITY;              // an entry is larger (-inf is none)
-    int n = 0;                            // entries after the last cut
+    int n = 0;                            // entries before this span
     auto cut = [&]() {
       n = scan_cut(list, count, p.M);
       if (n == p.M) {
@@ -236,13 +253,13 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
     __syncthreads();                      // the previous part is written
     if (threadIdx.x == 0) {
       count = 0;
-      level = 0;
+      level = 0xFFFFFFFFu;
     }
     __syncthreads();
     const int rounds = (t1 - t0 + kScanWarps - 1) / kScanWarps;
     for (int done = 0; done < rounds;) {
-      // a span: rounds 0, 1, 2 to 3, 4 to 7, ...
-      const int stop = min(rounds, max(1, 2 * done));
+      // a span: rounds 0 to 3, 4 to 15, 16 to 63, ...
+      const int stop = min(rounds, max(4, 4 * done));
       bool over = false;
       for (int k = done; k < stop; ++k) {
         const int t = t0 + k * kScanWarps + warp;
@@ -256,20 +273,25 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
         x.maxima(g);
         float m = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
         if (k == 0) {
-          // the first threshold: the M-th largest maximum of two lanes
-          const float pm = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          if ((lane & 1) == 0) top[warp * 16 + (lane >> 1)] = score_key(pm);
+          // the first threshold: the M-th largest maximum of two lanes (four
+          // where M is small: a quarter of the comparisons for an entry more or two)
+          const int groups = p.M <= 24 ? 64 : 128;
+          float pm = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          if (groups == 64) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
+          const int gl = groups / kScanWarps, step = 32 / gl;      // a warp's; lanes of one
+          if (lane % step == 0) top[warp * gl + lane / step] = score_key(pm);
           __syncthreads();
-          if (threadIdx.x < 128) {
+          if (threadIdx.x < groups) {
             const uint32_t me = top[threadIdx.x];
-            int larger = 0, equal = 0;
+            int larger = 0;
 #pragma unroll 8
-            for (int j = 0; j < 128; j += 4) {
+            for (int j = 0; j < groups; j += 4) {
               const uint4 o = *reinterpret_cast<const uint4*>(&top[j]);
               larger += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
-              equal += (o.x == me) + (o.y == me) + (o.z == me) + (o.w == me);
             }
-            if (larger < p.M && p.M <= larger + equal) level = me;
+            // (the least of those with fewer than M above them)
+            const uint32_t least = __reduce_min_sync(0xffffffffu, larger < p.M ? me : 0xFFFFFFFFu);
+            if (lane == 0) atomicMin(&level, least);
           }
           __syncthreads();
           // one step below it, so that its equals are entries (below +0 comes
@@ -298,20 +320,18 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
         // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf
         m = score_unkey(__reduce_max_sync(0xffffffffu, score_key(m)));
         const float base = m == -INFINITY ? 0.0f : m;
-        float2 e[4];
-#pragma unroll
-        for (int i = 0; i < kScanPer / 2; ++i) {
-          float2 y = x.pair(i);
-          add2_rn(y.x, y.y, -base, -base);
-          y = mul2_rn(y, make_float2(p.c, p.c));
-          y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          if (i < 4) e[i] = y;
-          else add2_rn(e[i & 3].x, e[i & 3].y, y.x, y.y);
+        const float e0 = __fmul_rn(base, p.c);
+        float sum;
+        if (fabsf(e0) < INFINITY) {
+          // x c - e0 in one rounding; e0 is off base c by what the factor puts back
+          sum = scan_sum(x, [&](float2 v) {
+            return fma2_rn(v, make_float2(p.c, p.c), make_float2(-e0, -e0));
+          }) * exp2_approx(-fmaf(base, p.c, -e0));
+        } else {
+          sum = scan_sum(x, [&](float2 v) {
+            return make_float2(__fmul_rn(v.x - base, p.c), __fmul_rn(v.y - base, p.c));
+          });
         }
-        add2_rn(e[0].x, e[0].y, e[1].x, e[1].y);
-        add2_rn(e[2].x, e[2].y, e[3].x, e[3].y);
-        add2_rn(e[0].x, e[0].y, e[2].x, e[2].y);
-        float sum = e[0].x + e[0].y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0 && t < t1) p.tile[static_cast<size_t>(r) * p.n_tiles + t] = make_float2(m, sum);
@@ -344,7 +364,14 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
           }
         }
       }
-      cut();
+      // (a few more than M would not raise the threshold by much)
+      const int have = count;
+      if (stop == rounds || have > 2 * p.M) {
+        cut();
+      } else {
+        n = have;
+        __syncthreads();
+      }
       done = stop;
     }
     // the part's best, sorted; nothing behind the last
