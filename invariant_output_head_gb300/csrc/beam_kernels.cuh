@@ -218,7 +218,7 @@ __device__ __forceinline__ float scan_sum(const ScanTile<FMT>& x, F f) {
 template <int FMT>
 __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_kernel(const BeamScanParams p) {
   __shared__ u64 list[kScanCap];
-  __shared__ __align__(16) uint32_t top[128];
+  __shared__ __align__(16) uint32_t top[kScanWarps * 128];
   __shared__ int count;
   __shared__ uint32_t level;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -273,30 +273,43 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
         x.maxima(g);
         float m = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
         if (k == 0) {
-          // the first threshold: the M-th largest maximum of two lanes (four
-          // where M is small: a quarter of the comparisons for an entry more or two)
-          const int groups = p.M <= 24 ? 64 : 128;
-          float pm = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          if (groups == 64) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
-          const int gl = groups / kScanWarps, step = 32 / gl;      // a warp's; lanes of one
-          if (lane % step == 0) top[warp * gl + lane / step] = score_key(pm);
+          // the first threshold: the M-th largest of maxima of as few and large
+          // groups as hold twice M in the round's tiles: of four lanes, two, one, or
+          // of eight elements
+          const int tiles = min(t1 - t0, kScanWarps);
+          int each = 8;                                  // groups of a tile
+          while (each < 128 && tiles * each < 2 * p.M) each = each == 32 ? 128 : 2 * each;
+          if (t < t1) {
+            if (each == 128) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top[warp * 128 + 4 * lane + j] = score_key(g[j]);
+            } else {
+              float pm = m;
+              if (each < 32) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 1));
+              if (each < 16) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 2));
+              const int step = 32 / each;
+              if (lane % step == 0) top[warp * each + lane / step] = score_key(pm);
+            }
+          }
           __syncthreads();
-          if (threadIdx.x < groups) {
-            const uint32_t me = top[threadIdx.x];
+          const int groups = tiles * each;
+          for (int i = threadIdx.x; i < (groups + 31) / 32 * 32; i += kScanThreads) {
+            const uint32_t me = i < groups ? top[i] : 0u;
             int larger = 0;
-#pragma unroll 8
+#pragma unroll 4
             for (int j = 0; j < groups; j += 4) {
               const uint4 o = *reinterpret_cast<const uint4*>(&top[j]);
               larger += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
             }
             // (the least of those with fewer than M above them)
-            const uint32_t least = __reduce_min_sync(0xffffffffu, larger < p.M ? me : 0xFFFFFFFFu);
+            const uint32_t least =
+                __reduce_min_sync(0xffffffffu, i < groups && larger < p.M ? me : 0xFFFFFFFFu);
             if (lane == 0) atomicMin(&level, least);
           }
           __syncthreads();
           // one step below it, so that its equals are entries (below +0 comes
           // the first negative number: keys know no -0); -inf stays
-          const uint32_t key = level;
+          const uint32_t key = groups >= p.M ? level : 0u;
           if (key > score_key(-INFINITY)) above = score_unkey(key == 0x80000000u ? key - 2 : key - 1);
         }
         // entries above the threshold
