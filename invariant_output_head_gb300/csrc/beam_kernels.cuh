@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const Bea
                         scan_block(p.tiles, p.blocks, r * p.n_tiles) + 1;
       const u64* best = p.best + static_cast<size_t>(r) * p.parts * M;
       __syncwarp();                            // the beam before has been read
-#pragma unroll 4
+#pragma unroll 8
       for (int i = lane; i < parts * M; i += 32) list[i] = best[i];
       float2 t = make_float2(-INFINITY, 0.0f);
       const float2* tiles = p.tile + static_cast<size_t>(r) * p.n_tiles;
@@ -465,7 +465,32 @@ __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const Bea
       const int j = (M + parts - 1) / parts - 1;
       const uint32_t low = __reduce_min_sync(0xffffffffu, lane < parts ? key[2 * (lane * M + j)] : 0xFFFFFFFFu);
       const uint32_t high = __reduce_max_sync(0xffffffffu, lane < parts ? key[2 * (lane * M + M - 1)] : 0u);
-      const uint32_t least = max(max(low, high), 1u);
+      uint32_t least = max(max(low, high), 1u);
+      // A short part's entries make the first bound a low one: then the M-th best
+      // of all, closed in on by counting in every list until few more than M stay.
+      auto at_least = [&](uint32_t v) {
+        int a = 0, z = lane < parts ? M : 0;
+        while (a < z) {
+          const int mid = (a + z) >> 1;
+          if (key[2 * (lane * M + mid)] >= v) a = mid + 1;
+          else z = mid;
+        }
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, a));
+      };
+      if (parts > 2) {
+        uint32_t above = __reduce_max_sync(0xffffffffu, lane < parts ? key[2 * lane * M] : 0u) + 1;
+        int stay = at_least(least);
+        while (stay > 2 * M && above - least > 1) {
+          const uint32_t mid = least + ((above - least) >> 1);
+          const int c = at_least(mid);
+          if (c >= M) {
+            least = mid;
+            stay = c;
+          } else {
+            above = mid;
+          }
+        }
+      }
       int n = 0;
       for (int i0 = 0; i0 < parts * M; i0 += 32) {
         const u64 word = i0 + lane < parts * M ? list[i0 + lane] : 0;
