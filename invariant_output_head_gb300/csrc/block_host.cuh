@@ -23,7 +23,7 @@ cudaError_t launch_block_gemm(const CUtensorMap& w, const CUtensorMap& g, const 
   std::memset(&cfg, 0, sizeof(cfg));
   const int64_t groups = (p.V + kBlockGroup - 1) / kBlockGroup;
   cfg.gridDim = dim3(static_cast<unsigned>(groups < sms ? groups : sms));
-  cfg.blockDim = dim3(kBlockThreads);
+  cfg.blockDim = dim3(block_threads(N));
   cfg.dynamicSmemBytes = block_layout(N, p.stages, p.nk).total + 1024u;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -43,7 +43,7 @@ cudaError_t launch_block_pair(detlm_head* h, const CUtensorMap& x, const CUtenso
   if (e != cudaSuccess) return e;
   p.idesc = idesc_e4m3(kRowsM, kRowsN);
   p.stages = kBlockPairMaxStages;
-  while (p.stages > 2 && block_pair_layout(p.stages).total + 1024u > kSmemLimit) --p.stages;
+  while (p.stages > 4 && block_pair_layout(p.stages).total + 1024u > kSmemLimit) --p.stages;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.blockDim = dim3(kRowsThreads);
@@ -66,8 +66,12 @@ template <int FMT>
 cudaError_t launch_quantize_blocks(const BlockQuantParams& p, int block_rows, cudaStream_t stream) {
   if (block_rows == kBQBlock) {
     const int64_t tiles = (p.B + kBQBlock - 1) / kBQBlock * p.nb;
-    return launch_dependent(quantize_tiles_kernel<FMT>, dim3(static_cast<unsigned>(tiles)), kBQThreads,
-                            stream, p);
+    const cudaError_t e = launch_dependent(quantize_tiles_kernel<FMT>, dim3(static_cast<unsigned>(tiles)),
+                                           kBQThreads, stream, p);
+    if (e != cudaSuccess) return e;
+    // a weight: calls of a head on it request its boxes before they wait
+    weights_fence_kernel<<<1, 32, 0, stream>>>();
+    return cudaGetLastError();
   }
   const int64_t per = kBQPer * (kBQThreads / 16);
   return launch_dependent(quantize_blocks_kernel<FMT>,

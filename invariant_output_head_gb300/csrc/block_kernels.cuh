@@ -34,7 +34,6 @@ namespace detlm {
 constexpr int kBlockK = 128;               // elements of K a scale covers
 constexpr int kBlockMaxD = 16384;          // bounds the row scales in shared memory
 constexpr int kBlockGroup = 32;            // vocabulary rows of a group
-constexpr int kBlockThreads = 192;
 constexpr int kBlockMaxStages = 12;
 constexpr int kBlockMaxSlots = 8;
 
@@ -99,6 +98,10 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float x, int typ
 // K boxes of a stage (and of an accumulator slot): two while a slot ring of
 // four fits, which halves the barriers a byte of W passes.
 __host__ __device__ constexpr int block_kps(int N) { return N <= 64 ? 2 : 1; }
+// Epilogue warps: a warp's drain of more than 64 columns takes longer than W's
+// box takes to come (96 rows x 128256 x 4096: 125 us with four, 98 with eight), so two share a quarter's columns there.
+__host__ __device__ constexpr int block_warps(int N) { return N <= 64 ? 4 : 8; }
+__host__ __device__ constexpr int block_threads(int N) { return 64 + 32 * block_warps(N); }
 
 struct BlockLayout {
   uint32_t stage_bytes, ctrl_off, sx_off, total;
@@ -119,11 +122,14 @@ __host__ __device__ inline BlockLayout block_layout(int N, int stages, int nk) {
 // tmW: box of 128 vocabulary rows; tmG: of one group; tmX: of the hidden rows
 // (as many as there are, in whole 8-row swizzle atoms: h_rows).
 template <int NBLK>
-__global__ void __launch_bounds__(kBlockThreads, 1)
+__global__ void __launch_bounds__(block_threads(16 * NBLK), 1)
 block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmG,
                   const __grid_constant__ CUtensorMap tmX, const BlockParams p) {
   constexpr int N = 16 * NBLK;
   constexpr int KPS = block_kps(N);
+  constexpr int EW = block_warps(N), ET = 32 * EW;
+  constexpr int NW = N * 4 / EW;                   // columns of an epilogue warp
+  static_assert(NW % 16 == 0, "whole 16-column blocks");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -151,6 +157,40 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     return sW(s, KPS) + static_cast<uint32_t>(b) * (N * kRowBytes);
   };
 
+  const int64_t groups = (p.V + kBlockGroup - 1) / kBlockGroup;
+  const int g0 = static_cast<int>(groups * blockIdx.x / gridDim.x);
+  const int g1 = static_cast<int>(groups * (blockIdx.x + 1) / gridDim.x);
+  const int steps = (p.nk + KPS - 1) / KPS;
+  const uint64_t pol_w = policy_evict_first();
+  const uint64_t pol_x = policy_evict_last();
+  const uint32_t x_bytes = static_cast<uint32_t>((p.B + 7) / 8 * 8) * kRowBytes;
+  // boxes of a step: W's (and the bytes that the step's barrier waits for),
+  // the hidden rows'
+  auto load_w = [&](uint32_t stage, int g, int st) {
+    const int ng = min(4, g1 - g), nb = min(KPS, p.nk - st * KPS);
+    mbar_expect_tx(full_bar(stage), nb * (static_cast<uint32_t>(ng) * kBlockGroup * kRowBytes + x_bytes));
+    for (int b = 0; b < nb; ++b) {
+      const int k = (st * KPS + b) * kBlockK;
+      if (ng == 4) {
+        tma_load_2d(sW(stage, b), &tmW, k, g * kBlockGroup, full_bar(stage), pol_w);
+      } else {
+        for (int i = 0; i < ng; ++i)
+          tma_load_2d(sW(stage, b) + i * (kBlockGroup * kRowBytes), &tmG, k, (g + i) * kBlockGroup,
+                      full_bar(stage), pol_w);
+      }
+    }
+  };
+  auto load_x = [&](uint32_t stage, int st) {
+    const int nb = min(KPS, p.nk - st * KPS);
+    for (int b = 0; b < nb; ++b)
+      tma_load_2d(sX(stage, b), &tmX, (st * KPS + b) * kBlockK, 0, full_bar(stage), pol_x);
+    mbar_arrive(full_bar(stage));
+  };
+  // W is read-only between announced changes: the first stages' boxes of it are
+  // requested before the previous kernels on the stream are done, and before
+  // anything else here
+  const int pre = min(S, (g1 - g0 + 3) / 4 * steps);
+
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
@@ -158,14 +198,13 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     }
     for (int b = 0; b < SL; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), 4);       // four epilogue warps
+      mbar_init(acce_bar(b), EW);      // the epilogue warps
     }
     mbar_init(never_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmG);
+    for (int j = 0; j < pre; ++j) load_w(j, g0 + j / steps * 4, j % steps);
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
@@ -178,41 +217,21 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   const uint32_t tmem_base = *tmem_holder;
   // the call after this one may start its prologue on SMs that are free
   grid_dep_launch();
-  // W may come from an earlier kernel on the stream (one that quantised it, a
-  // copy): nothing of it is requested before the wait
-  grid_dep_wait();
-
-  const int64_t groups = (p.V + kBlockGroup - 1) / kBlockGroup;
-  const int g0 = static_cast<int>(groups * blockIdx.x / gridDim.x);
-  const int g1 = static_cast<int>(groups * (blockIdx.x + 1) / gridDim.x);
-  const int steps = (p.nk + KPS - 1) / KPS;
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
-      const uint64_t pol_w = policy_evict_first();
-      const uint64_t pol_x = policy_evict_last();
-      const uint32_t x_bytes = static_cast<uint32_t>((p.B + 7) / 8 * 8) * kRowBytes;
+      grid_dep_wait();
       uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
       bool ok = true;
+      int j = 0;
       for (int g = g0; g < g1 && ok; g += 4) {
-        const int ng = min(4, g1 - g);
-        for (int st = 0; st < steps; ++st) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
-          const int nb = min(KPS, p.nk - st * KPS);
-          mbar_arrive_expect_tx(full_bar(stage),
-                                nb * (static_cast<uint32_t>(ng) * kBlockGroup * kRowBytes + x_bytes));
-          for (int b = 0; b < nb; ++b) {
-            const int k = (st * KPS + b) * kBlockK;
-            if (ng == 4) {
-              tma_load_2d(sW(stage, b), &tmW, k, g * kBlockGroup, full_bar(stage), pol_w);
-            } else {
-              for (int i = 0; i < ng; ++i)
-                tma_load_2d(sW(stage, b) + i * (kBlockGroup * kRowBytes), &tmG, k,
-                            (g + i) * kBlockGroup, full_bar(stage), pol_w);
-            }
-            tma_load_2d(sX(stage, b), &tmX, k, 0, full_bar(stage), pol_x);
+        for (int st = 0; st < steps; ++st, ++j) {
+          if (j >= pre) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
+            load_w(stage, g, st);
           }
+          load_x(stage, st);
           outstanding |= 1u << stage;
           out_par = (out_par & ~(1u << stage)) | (phase << stage);
           if (++stage == static_cast<uint32_t>(S)) { stage = 0; phase ^= 1u; }
@@ -267,22 +286,23 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   } else {
     // --------------------------------------------------------- epilogue
     const int q = warp & 3;                    // TMEM lane quarter: the tile's group
+    const int n_first = (warp - 2) / 4 * NW;   // first column: a hidden row
     const int et = threadIdx.x - 64;
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    for (int i = et; i < p.nk * N; i += 128) {
+    for (int i = et; i < p.nk * N; i += ET) {
       const int c = i / N, n = i - (i / N) * N;
       sx[i] = n < p.B ? p.x_scale[static_cast<size_t>(n) * p.nk + c] : 0.0f;
     }
-    named_bar_sync(1, 128);
+    named_bar_sync(1, ET);
     uint32_t slot = 0, sph = 0;
     bool failed = false;
     for (int g = g0; g < g1; g += 4) {
       const bool mine = g + q < g1;            // this warp's group exists
       const int v = (g + q) * kBlockGroup + lane;
       const float* ws = p.w_scale + static_cast<size_t>(mine ? (g + q) / (kBM / kBlockGroup) : 0) * p.nk;
-      float2 acc[N / 2];
+      float2 acc[NW / 2];
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < NW / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       float sw[KPS];
 #pragma unroll
       for (int b = 0; b < KPS; ++b) sw[b] = b < p.nk ? __ldg(ws + b) : 0.0f;
@@ -306,8 +326,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
           for (int b = 0; b < KPS; ++b) {
             const int c = st * KPS + b;
             if (c >= p.nk) break;
-            const uint32_t at = tmem_base + tlane + (cur * KPS + b) * static_cast<uint32_t>(N);
-            const float* s = sx + c * N;
+            const uint32_t at = tmem_base + tlane + (cur * KPS + b) * static_cast<uint32_t>(N) +
+                                static_cast<uint32_t>(n_first);
+            const float* s = sx + c * N + n_first;
             const float2 w2 = make_float2(sw[b], sw[b]);
             auto add16 = [&](const uint32_t* r, int n0) {
 #pragma unroll
@@ -320,14 +341,14 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                                mul2_rn(make_float2(x.z, x.w), w2), a[1]);
               }
             };
-            if constexpr (NBLK % 2 == 1) {
+            if constexpr (NW % 32 != 0) {
               uint32_t r[16];
-              tmem_ld16(at + (NBLK - 1) * 16, r);
+              tmem_ld16(at + NW - 16, r);
               tmem_wait_ld();
-              add16(r, (NBLK - 1) * 16);
+              add16(r, NW - 16);
             }
 #pragma unroll
-            for (int h = 0; h < NBLK / 2; ++h) {
+            for (int h = 0; h < NW / 32; ++h) {
               uint32_t r[32];
               tmem_ld32(at + h * 32, r);
               tmem_wait_ld_of(r);
@@ -349,11 +370,10 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         break;
       }
       if (mine && v < p.V) {
+        size_t at = static_cast<size_t>(n_first) * p.V + v;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (n < p.B)
-            store_out(p.out, static_cast<size_t>(n) * p.V + v, (n & 1) ? acc[n / 2].y : acc[n / 2].x,
-                      p.type);
+        for (int n = 0; n < NW; ++n, at += p.V)
+          if (n_first + n < p.B) store_out(p.out, at, (n & 1) ? acc[n / 2].y : acc[n / 2].x, p.type);
       }
     }
   }
@@ -501,8 +521,8 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       int c = static_cast<int>(slot);            // this thread's block in the unit
       for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
         for (; c < p.nk; c += 2) {
-          if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
+          if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = sdesc_sw128(sX(stage));
           const uint64_t db = sdesc_sw128(sW(stage));
