@@ -91,7 +91,7 @@ int detlm_quantize_blocks(const void* x_dev, int dtype, int64_t B, int64_t d, in
   p.x = x_dev;
   p.B = B;
   p.d = d;
-  p.nb = (d + kBQBlock - 1) / kBQBlock;
+  p.nb = static_cast<int32_t>((d + kBQBlock - 1) / kBQBlock);
   p.q = static_cast<uint8_t*>(q_dev);
   p.scale = scale_dev;
   // (a launch has fewer than 2^31 blocks)

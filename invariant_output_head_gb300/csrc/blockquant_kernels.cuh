@@ -29,7 +29,7 @@ constexpr int kBQBlock = 128;
 struct BlockQuantParams {
   const void* x;
   int64_t B, d;
-  int64_t nb;            // blocks of a row
+  int32_t nb;            // blocks of a row
   uint8_t* q;            // [B, d] e4m3
   float* scale;          // [B or ceil(B / 128), nb]
 };
@@ -121,23 +121,23 @@ template <int FMT>
 __global__ void __launch_bounds__(kBQThreads) quantize_blocks_kernel(const BlockQuantParams p) {
   grid_dep_launch();
   grid_dep_wait();
-  const int64_t total = p.B * p.nb;
-  const int l = threadIdx.x & 15;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kBQPer) * (kBQThreads / 16) + (threadIdx.x >> 4);
+  const uint32_t total = static_cast<uint32_t>(p.B) * static_cast<uint32_t>(p.nb);   // (below 2^31)
+  const uint32_t l = threadIdx.x & 15;
+  const uint32_t first = blockIdx.x * (kBQPer * (kBQThreads / 16)) + (threadIdx.x >> 4);
   Eight<FMT> x[kBQPer];
   size_t at[kBQPer];
 #pragma unroll
   for (int i = 0; i < kBQPer; ++i) {
-    const int64_t b = first + i * (kBQThreads / 16);
-    const int64_t n = b / p.nb;
-    const int64_t k = (b - n * p.nb) * kBQBlock + 8 * l;
+    const uint32_t b = first + i * (kBQThreads / 16);
+    const uint32_t n = b / static_cast<uint32_t>(p.nb);
+    const int64_t k = static_cast<int64_t>(b - n * p.nb) * kBQBlock + 8 * l;
     at[i] = b < total && k < p.d ? static_cast<size_t>(n * p.d + k) : SIZE_MAX;
     if (at[i] != SIZE_MAX) x[i].load(p.x, at[i]);
     else x[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < kBQPer; ++i) {
-    const int64_t b = first + i * (kBQThreads / 16);
+    const uint32_t b = first + i * (kBQThreads / 16);
     const BlockScale s(max16(x[i].amax()));
     if (at[i] != SIZE_MAX)
       *reinterpret_cast<uint2*>(p.q + at[i]) =
@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(kBQThreads) quantize_blocks_kernel(const Block
 // 128 x 128: one block of threads a tile, eight rows of it a thread. (No early
 // start for what follows: a head's calls read the weight it writes.)
 template <int FMT>
-__global__ void __launch_bounds__(kBQThreads) quantize_tiles_kernel(const BlockQuantParams p) {
+__global__ void __launch_bounds__(kBQThreads, 3) quantize_tiles_kernel(const BlockQuantParams p) {
   grid_dep_wait();
-  const int64_t tile = blockIdx.x;
-  const int64_t ti = tile / p.nb, tj = tile - ti * p.nb;
-  const int64_t k = tj * kBQBlock + 8 * (threadIdx.x & 15);
-  const int64_t n0 = ti * kBQBlock + (threadIdx.x >> 4);
+  const uint32_t tile = blockIdx.x;
+  const uint32_t ti = tile / static_cast<uint32_t>(p.nb), tj = tile - ti * p.nb;
+  const int64_t k = static_cast<int64_t>(tj) * kBQBlock + 8 * (threadIdx.x & 15);
+  const int64_t n0 = static_cast<int64_t>(ti) * kBQBlock + (threadIdx.x >> 4);
   constexpr int kRows = kBQBlock * 16 / kBQThreads;
   Eight<FMT> x[kRows];
   uint32_t m = 0;
