@@ -14,7 +14,8 @@
 // the row set, so they do not depend on how rows are cut). The part's largest
 // logits collect in shared memory: an element is kept if it is above the
 // smallest of the M = n_out best at the last cut, and the list is cut to M after
-// rounds 4, 16, 64: about 3 M entries a span. The first threshold comes from
+// rounds 2, 4, 8, 16, ...: about M entries a span (16 sequences of 32 beams, M =
+// 64: 103 us; cut after 4, 16, 64: 115; the same at M = 16). The first threshold comes from
 // the first round itself: the M-th largest of 128 maxima of 64 elements each. An
 // element is compared as a 64-bit word: its order as a number, then the lower
 // index first. Warps meet at the cuts only.
@@ -23,9 +24,16 @@
 // a fixed tree and merges the parts' sorted lists, then the block merges the
 // beams' lists by score.
 //
-// The scan is bound by instruction issue and the exponentials' unit about as
-// much as by memory: an element costs a load, its conversion, a maximum, a
-// fused multiply-add, an exponential, an addition and a comparison.
+// What bounds the scan is instruction issue and the latency of its chains, not
+// memory: 64 sequences of 8 beams x 128256 in bf16, n_out = 16, 131 MB: 46 us of
+// the call's 49.5 (2.65 TB/s), 62 % of the issue slots busy with 24 warps an SM,
+// about 440 instructions a tile of 1024: some 130 the exponentials' sum, 180 the
+// loads, maxima and the rest, 130 the entries and cuts. Without entries and cuts
+// it would take 31. Tried and slower: tiles of 512 with 32 to 48 warps an SM
+// (54 to 64 us: the instructions a tile that do not depend on its size), tiles
+// staged three ahead by asynchronous copies (54: more instructions, and loads are
+// not what is waited for), whole rows or equal parts of rows for blocks (73: the
+// last wave).
 #pragma once
 #include "quant_kernels.cuh"
 #include "score_kernels.cuh"
@@ -124,7 +132,7 @@ struct ScanTile {
   // (The loads stand alone, so that all are under way together.)
   __device__ __forceinline__ void load(const uint8_t* row, int at, int V, bool words) {
     const int lane = threadIdx.x & 31;
-    if (words && at + kScanTile <= V) {
+    if (words && at <= V - kScanTile) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + (FMT == QF_FP32 ? at : at / 2) + lane;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = __ldg(p + 32 * i);
@@ -137,7 +145,7 @@ struct ScanTile {
       }
     } else {
       const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-      if (at + kScanTile <= V) {           // (between words: element by element)
+      if (at <= V - kScanTile) {           // (between words: element by element)
         p += at + 2 * lane;
         uint16_t lo[kWords], hi[kWords];
 #pragma unroll
@@ -258,8 +266,8 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
     __syncthreads();
     const int rounds = (t1 - t0 + kScanWarps - 1) / kScanWarps;
     for (int done = 0; done < rounds;) {
-      // a span: rounds 0 to 3, 4 to 15, 16 to 63, ...
-      const int stop = min(rounds, max(4, 4 * done));
+      // a span: rounds 0 and 1, 2 and 3, 4 to 7, ...
+      const int stop = min(rounds, max(2, 2 * done));
       bool over = false;
       for (int k = done; k < stop; ++k) {
         const int t = t0 + k * kScanWarps + warp;

@@ -100,6 +100,7 @@ def test_masks_dead_beams_and_finished_ones(t, name):
     assert got.parent[2].tolist() == [-1] * 16
     assert sorted(got.parent[5].tolist())[-3:] == [0, 1, 2] and got.token[5, 0] == V - 1
     check(t, head, z, s, 64)
+    check(t, head, z, s, 9, finished=finished.to(t.uint8) * 200, end=3)
     assert head.check() == 0
 
 
@@ -271,6 +272,33 @@ def test_many_states_strided_ones_and_other_numbers_of_beams(t):
     big[1, 1, -5:] = 9
     BeamStates([big[:, :, -16:]]).reorder(t.tensor([[0, 1, 1, 0]], dtype=t.int32).cuda())
     assert big[2, 1, -5:].tolist() == [9] * 5 and int(big[3].max()) == 0
+
+
+def test_more_sequences_than_a_grid_has_rows(t):
+    from invariant_output_head_gb300 import BeamStates
+    n = 70001
+    x = t.arange(n * 2 * 3, dtype=t.int32, device="cuda").view(n * 2, 3)
+    parent = t.zeros(n, 2, dtype=t.int32, device="cuda")
+    parent[::2, 0] = 1
+    got = x.clone()
+    BeamStates([got]).reorder(parent)
+    row = (parent + 2 * t.arange(n, dtype=t.int32, device="cuda")[:, None]).view(-1).long()
+    assert t.equal(got, x[row])
+
+
+def test_selection_of_many_sequences_of_few_tokens(t):
+    V = 40
+    z, s = step_inputs(t, 3000, 2, V, "bf16", 2)
+    check(t, head_of(t, V), z, s, 5)
+
+
+@pytest.mark.parametrize("n_out", [1, 25, 33, 64])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_parts_of_every_size(t, rows, n_out):
+    """Rows of few tiles over many blocks: parts of one tile to a row's all."""
+    for V in (1023, 1024, 3100, 9000, 33000):
+        z, s = step_inputs(t, rows, 1, V, "fp16", V + rows)
+        check(t, head_of(t, V), z, s, n_out)
 
 
 # ------------------------------------------------------------------- together

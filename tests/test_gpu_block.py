@@ -216,3 +216,54 @@ def test_a_stalled_kernel_times_out_and_the_head_recovers(t, B):
     binding.detlm_head_debug(head.handle, 0, 0)
     assert t.equal(head.block_scaled_logits(q, xs, ws), want)
     assert head.check() == 0
+
+
+def test_a_weight_quantised_in_place_right_before_the_call(t):
+    """Each call uses the weight that the call before it on the stream wrote."""
+    from invariant_output_head_gb300 import Head, quantize_blocks
+    g = t.Generator(device="cuda").manual_seed(7)
+    V, d = 20000, 1024
+    Ws = [t.randn(V, d, generator=g, device="cuda", dtype=t.bfloat16) for _ in range(6)]
+    q, xs = quantize_blocks(t.randn(3, d, generator=g, device="cuda"))
+    want = []
+    for W in Ws:
+        Wq, ws = quantize_blocks(W, 128)
+        t.cuda.synchronize()
+        want.append(Head(Wq).block_scaled_logits(q, xs, ws))
+    weight = quantize_blocks(Ws[-1], 128)
+    head = Head(weight[0])
+    got = [t.empty_like(want[0]) for _ in Ws]
+    t.cuda.synchronize()
+    for W, z in zip(Ws, got):
+        quantize_blocks(W, 128, out=weight)
+        head.weights_changed()
+        head.block_scaled_logits(q, xs, weight[1], out=z)
+    assert all(t.equal(a, b) for a, b in zip(got, want))
+    assert head.check() == 0
+
+
+def test_two_heads_on_two_streams(t):
+    from invariant_output_head_gb300 import Head
+    cases = [head_inputs(t, B, 8000, 512, B) for B in (3, 300)]
+    heads = [Head(c[2]) for c in cases]
+    want = [h.block_scaled_logits(c[0], c[1], c[3]) for h, c in zip(heads, cases)]
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    got = [[h.block_scaled_logits(c[0], c[1], c[3], stream=s) for _ in range(8)]
+           for h, c, s in zip(heads, cases, streams)]
+    t.cuda.synchronize()
+    assert all(t.equal(z, w) for zs, w in zip(got, want) for z in zs)
+    assert [h.check() for h in heads] == [0, 0]
+
+
+def test_addresses_that_are_refused(t):
+    from invariant_output_head_gb300 import DetlmError, Head, quantize_blocks
+    q, xs, W, ws = head_inputs(t, 2, 300, 64, 1)
+    room = t.zeros(200, dtype=t.float32, device="cuda")
+    with pytest.raises(DetlmError):
+        quantize_blocks(room[1:129].view(2, 64))                # rows between 16 bytes
+    with pytest.raises(DetlmError):
+        quantize_blocks(room[:2 * 40].view(2, 40))              # d no multiple of 16
+    bytes_ = t.zeros(300, dtype=t.uint8, device="cuda")
+    with pytest.raises(DetlmError):
+        Head(W).block_scaled_logits(bytes_[8:136].view(t.float8_e4m3fn).view(2, 64), xs, ws)
