@@ -7,15 +7,15 @@ namespace {
 int beam_tiles(const detlm_head* h) { return static_cast<int>((h->V + kScanTile - 1) / kScanTile); }
 
 // The scan's blocks: as many as run at once, with four tiles each at least (a
-// block's cuts cost as much as a round), and so few that a row has at most
-// kBeamPartsMax parts: G / rows + 2 of G blocks.
+// block's cuts cost as much as a round) but one for each row, and so few that a
+// row has at most kBeamPartsMax parts: G / rows + 2 of G blocks.
 constexpr int64_t kScanLeast = 4;
 int scan_blocks(const detlm_head* h, int64_t rows, int fmt) {
-  int64_t g = static_cast<int64_t>(h->num_sms) * scan_resident(fmt);
-  const int64_t tiles = rows * beam_tiles(h);
-  if (g > tiles / kScanLeast) g = tiles / kScanLeast;
+  const int64_t tiles = rows * beam_tiles(h), slots = static_cast<int64_t>(h->num_sms) * scan_resident(fmt);
+  int64_t g = tiles / kScanLeast > rows ? tiles / kScanLeast : rows;
+  if (g > slots) g = slots;
   if (g > rows * (kBeamPartsMax - 2)) g = rows * (kBeamPartsMax - 2);
-  return static_cast<int>(g < 1 ? 1 : g);
+  return static_cast<int>(g);
 }
 // The tiles' sums and the parts' lists of up to `rows` rows: at most G + 2 rows
 // lists.

@@ -82,7 +82,10 @@ struct BeamMergeParams {
 // scan_block is the block that a tile falls to.
 __device__ __forceinline__ int64_t scan_first(int64_t tiles, int blocks, int b) { return tiles * b / blocks; }
 __device__ __forceinline__ int scan_block(int64_t tiles, int blocks, int64_t t) {
-  return static_cast<int>(((t + 1) * blocks - 1) / tiles);
+  const uint64_t n = static_cast<uint64_t>(t + 1) * static_cast<uint32_t>(blocks) - 1;
+  // (a division of 32 bits is much shorter, and mostly enough)
+  if ((n | static_cast<uint64_t>(tiles)) >> 32 == 0) return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(tiles));
+  return static_cast<int>(n / static_cast<uint64_t>(tiles));
 }
 
 // A beam that proposes continuations of its own.
@@ -416,7 +419,8 @@ __device__ __forceinline__ float2 tile_join(float2 a, float2 b, float c) {
 constexpr int kMergeBeamThreads = 256;
 
 // The block's shared memory: a warp's lists of a beam, for as many warps as have
-// one (later the merge's entries, 8 bytes each too); then every beam's candidates [beams][M]: scores, tokens, and their number.
+// one (later the merge's entries, 8 bytes each too); then every beam's candidates
+// [beams][M]: scores, tokens, and their number; a number of each warp; one more.
 __host__ __device__ inline size_t merge_lists(int beams, int parts, int M) {
   const int warps = beams < kMergeBeamThreads / 32 ? beams : kMergeBeamThreads / 32;
   return static_cast<size_t>(warps * parts > beams ? warps * parts : beams) * M;
@@ -429,6 +433,10 @@ __host__ __device__ inline size_t merge_smem(int beams, int parts, int M) {
 // Both merges place an entry by counting those before it, once a threshold has
 // taken most of the others out. (Taking the best head M times over, or counting
 // by bisection in each list, takes longer: every step waits for the one before.)
+// Bound by latency: 5 to 7 us for a few beams, of which a few loads and the
+// launch are half. As the last step of a sequence's last scan block (one launch,
+// a counter a sequence) it saved 1 us for one request and cost 3 to 7 for
+// hundreds of rows, whose scan it then holds up.
 __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const BeamMergeParams p) {
   grid_dep_launch();
   grid_dep_wait();
@@ -452,13 +460,18 @@ __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const Bea
       const int parts = scan_block(p.tiles, p.blocks, (r + 1) * p.n_tiles - 1) -
                         scan_block(p.tiles, p.blocks, r * p.n_tiles) + 1;
       const u64* best = p.best + static_cast<size_t>(r) * p.parts * M;
-      __syncwarp();                            // the beam before has been read
-#pragma unroll 8
-      for (int i = lane; i < parts * M; i += 32) list[i] = best[i];
-      float2 t = make_float2(-INFINITY, 0.0f);
       const float2* tiles = p.tile + static_cast<size_t>(r) * p.n_tiles;
+      const float2 none = make_float2(-INFINITY, 0.0f);
+      // (the first loads of both together)
+      const float2 first = lane < p.n_tiles ? tiles[lane] : none;
+      const u64 word = lane < parts * M ? best[lane] : 0;
+      __syncwarp();                            // the beam before has been read
+      if (lane < parts * M) list[lane] = word;
+#pragma unroll 8
+      for (int i = lane + 32; i < parts * M; i += 32) list[i] = best[i];
+      float2 t = tile_join(none, first, p.c);
 #pragma unroll 4
-      for (int i = lane; i < p.n_tiles; i += 32) t = tile_join(t, tiles[i], p.c);
+      for (int i = lane + 32; i < p.n_tiles; i += 32) t = tile_join(t, tiles[i], p.c);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         t = tile_join(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, o),
