@@ -396,7 +396,10 @@ int detlm_head_scaled_logits(detlm_head_t* head, const int8_t* q_dev,
  * from its own values.) The division is exact, so q has one right value. An
  * all-zero block has scale 1; a block with a NaN or an infinity has scale NaN
  * and q NaN. Requirements: d % 16 == 0; x_dev and q_dev 16-byte aligned,
- * scale_dev 4-byte aligned; fewer than 2^31 blocks. B == 0 is a no-op. */
+ * scale_dev 4-byte aligned; fewer than 2^31 blocks; outputs overlap neither the
+ * input nor each other. B == 0 is a no-op. A head's calls may follow at once on
+ * the same stream; a weight that a head already holds is announced with
+ * detlm_head_weights_changed when it is quantised again in place. */
 int detlm_quantize_blocks(const void* x_dev, int dtype, int64_t B, int64_t d,
                           int block_rows, void* q_dev, float* scale_dev,
                           cudaStream_t stream);
