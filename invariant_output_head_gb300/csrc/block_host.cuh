@@ -41,7 +41,7 @@ cudaError_t launch_block_pair(detlm_head* h, const CUtensorMap& x, const CUtenso
   int pairs = 0;
   e = op_pairs(h, &pairs);
   if (e != cudaSuccess) return e;
-  p.idesc = idesc_e4m3(kRowsM, kRowsN);
+  p.idesc = idesc_e4m3(kRowsM, 128);
   p.stages = kBlockPairMaxStages;
   while (p.stages > 4 && block_pair_layout(p.stages).total + 1024u > kSmemLimit) --p.stages;
   cudaLaunchConfig_t cfg;
@@ -154,8 +154,10 @@ int detlm_head_block_scaled_logits(detlm_head_t* h, const void* q_dev, const flo
   p.units = static_cast<int32_t>(units);
   CUtensorMap tmO = tmX;   // not read unless it is valid
   p.tma = encode_out(&tmO, type, out_dev, h->V, B) ? 1 : 0;
+  CUtensorMap tmV;         // half a vocabulary tile: what one of the pair's CTAs loads of it
+  if (!encode_2d(&tmV, DETLM_E4M3, h->W, h->d, h->V, 64)) return DETLM_EINVAL;
   time_start(h, stream);
-  e = launch_block_pair(h, tmX, h->tmW, tmO, p, stream);
+  e = launch_block_pair(h, tmX, tmV, tmO, p, stream);
   time_stop(h, stream);
   return status_from_cuda(e);
 }

@@ -392,14 +392,15 @@ constexpr int kBlockPairMaxStages = 6;
 struct BlockPairLayout {
   uint32_t stage_bytes, ctrl_off, xs_off, total;
 };
-// Stage s: this CTA's 128 hidden rows [128 x 128 B], its 128 vocabulary rows;
-// barriers (full[S], empty[S], slot_full[2], slot_empty[2], never, drain[2]), the
-// TMEM address holder and the abort flag; the epilogue warps' staging buffers.
+// Stage s: this CTA's 128 hidden rows [128 x 128 B], its 64 rows of either
+// vocabulary tile; barriers (full[S], empty[S], slot_full[4], slot_empty[4],
+// never, drain[2]), the TMEM address holder and the abort flag; the epilogue
+// warps' staging buffers.
 __host__ __device__ inline BlockPairLayout block_pair_layout(int stages) {
   BlockPairLayout L;
   L.stage_bytes = 2u * kRowsHalf * kRowBytes;
   L.ctrl_off = static_cast<uint32_t>(stages) * L.stage_bytes;
-  L.xs_off = (L.ctrl_off + (2u * stages + 7u) * 8u + 16u + 1023u) & ~1023u;
+  L.xs_off = (L.ctrl_off + (2u * stages + 11u) * 8u + 16u + 1023u) & ~1023u;
   L.total = L.xs_off + 8u * kOpXsBytes;
   return L;
 }
@@ -422,10 +423,10 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   auto accf_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
-  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
-  const uint32_t never_bar = bar0 + 8u * (2 * S + 4);
-  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);      // and the next
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 7) * 8);
+  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * S + 4 + b); };
+  const uint32_t never_bar = bar0 + 8u * (2 * S + 8);
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 9);      // and the next
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L.ctrl_off + (2 * S + 11) * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const uint32_t smem_base = smem_u32(smem);
   auto sX = [&](int s) { return smem_base + static_cast<uint32_t>(s) * L.stage_bytes; };
@@ -436,9 +437,9 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       mbar_init(full_bar(s), 1);       // the leader's arrival (+ both CTAs' loads)
       mbar_init(empty_bar(s), 1);      // the leader's MMA commit
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(accf_bar(b), 1);       // the leader's MMA commit
-      mbar_init(acce_bar(b), 16);      // eight epilogue warps of each CTA
+      mbar_init(acce_bar(b), 8);       // four epilogue warps of each CTA
     }
     mbar_init(never_bar, 1);
     mbar_init(drain_bar, 1);
@@ -473,7 +474,7 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
       bool ok = true;
       for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
-        const int n0 = w.r * 256 + half, v0 = w.q * 256 + half;
+        const int n0 = w.r * 256 + half, v0 = w.q * 256 + half / 2;
         // the peer's hidden rows may not exist: its box is not loaded then
         const uint32_t bytes = (2u + (w.r * 256 + kRowsHalf < p.B ? 2u : 1u)) * kRowsHalf * kRowBytes;
         for (int c = 0; c < p.nk; ++c) {
@@ -481,6 +482,7 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
           tma_load_2d_pair(sW(stage), &tmW, c * kBlockK, v0, fb, pol_w);
+          tma_load_2d_pair(sW(stage) + 64 * kRowBytes, &tmW, c * kBlockK, v0 + 128, fb, pol_w);
           if (n0 < p.B) tma_load_2d_pair(sX(stage), &tmX, c * kBlockK, n0, fb, pol_x);
           outstanding |= 1u << stage;
           out_par = (out_par & ~(1u << stage)) | (phase << stage);
@@ -522,14 +524,19 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
         for (; c < p.nk; c += 2) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
-          if (!mbar_wait(acce_bar(slot), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
-          tc_fence_after();
           const uint64_t da = sdesc_sw128(sX(stage));
-          const uint64_t db = sdesc_sw128(sW(stage));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)           // K = 32 per MMA
-            mma_f8_pair(tmem_base + slot * 256u, da + 2u * k, db + 2u * k, p.idesc, k != 0);
-          mma_commit_pair(accf_bar(slot), 3);
+          for (int v = 0; v < 2; ++v) {           // vocabulary tile
+            const uint32_t at = 2u * slot + v;
+            if (!mbar_wait(acce_bar(at), sph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t db = sdesc_sw128(sW(stage) + v * (64u * kRowBytes));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)           // K = 32 per MMA
+              mma_f8_pair(tmem_base + at * 128u, da + 2u * k, db + 2u * k, p.idesc, k != 0);
+            mma_commit_pair(accf_bar(at), 3);
+          }
+          if (!ok) break;
           mma_commit_pair(empty_bar(stage), 3);
           sph ^= 1u;
           stage += 2;
@@ -579,7 +586,7 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
           sx = __ldg(xs + c + 1);
           sw = __ldg(ws + c + 1);
         }
-        const uint32_t cur = slot, cph = sph;
+        const uint32_t cur = 2u * slot + g, cph = sph;
         if (++slot == 2u) { slot = 0; sph ^= 1u; }
         if (!failed && !mbar_wait(accf_bar(cur), cph, abort_flag, p.timeout_ns)) {
           failed = true;
@@ -597,7 +604,7 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             a[1] = y.y;
           }
         };
-        const uint32_t at = tmem_base + tlane + cur * 256u + static_cast<uint32_t>(g * 128);
+        const uint32_t at = tmem_base + tlane + cur * 128u;
         uint32_t ra[32], rb[32];
         if (live) {
           tmem_ld32(at, ra);
