@@ -563,15 +563,15 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const int q = warp & 3;                    // TMEM lane quarter
     const int g = (warp - 4) >> 2;             // vocabulary tile of the unit
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    Staging sg;
-    sg.xs = smem + L.xs_off + (warp - 4) * kOpXsBytes;
-    sg.xs_u32 = smem_u32(sg.xs);
     uint32_t slot = 0, sph = 0;
     bool failed = false;
-    for (UnitWalk walk = first; walk.u < p.units; walk.next()) {
-      const int nw0 = walk.r * 256 + half + q * 32;    // the warp's first row
+    // (registers are what these warps are short of: a unit's place is divided out
+    // again, not walked along)
+    for (int u = pair; u < p.units; u += n_pairs) {
+      const int vt = u / p.n1;
+      const int nw0 = (u - vt * p.n1) * 256 + half + q * 32;   // the warp's first row
       const int n = nw0 + lane;                        // this thread's row
-      const int vb = walk.q * 256 + g * 128;           // its first column
+      const int vb = vt * 256 + g * 128;               // its first column
       const bool live = nw0 < p.B && vb < p.V;
       // (rows and tiles that do not exist read another's scales)
       const float* xs = p.x_scale + static_cast<size_t>(min(n, p.B - 1)) * p.nk;
@@ -636,6 +636,9 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         break;
       }
       if (live) {
+        Staging sg;
+        sg.xs = smem + L.xs_off + (warp - 4) * kOpXsBytes;
+        sg.xs_u32 = smem_u32(sg.xs);
         const OutRows out{p.out, p.B, p.V, p.type, p.tma};
         store_rows(out, &tmO, sg, lane, n, nw0, vb, min(128, p.V - vb),
                    [&](int j, float (&y)[4]) {
