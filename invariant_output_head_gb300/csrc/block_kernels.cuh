@@ -21,11 +21,27 @@
 // vocabulary in groups of 32 rows (whole tiles of 128 would leave the last round
 // of V = 32000 a third full): tiles of four groups, the last of fewer, whose
 // missing groups are not loaded. A warp's 32 rows lie in one block of w_scale.
+// Bound by the stream of W from memory: 32 rows x 128256 x 4096 in 80 us, 6.66
+// TB/s of the 6.78 that a copy reaches, 1 row 79; one row of 32000 x 2048 in 14.2
+// us, of which some 4.5 are the launch, the first boxes' latency and the last
+// drain. W's first boxes are requested before the prologue (82.8 us without). Up
+// to 64 rows a row more costs nothing (84 us); at 96 and 128 (97 and 113) the
+// hidden rows' boxes, which every SM reads from L2, are as large as W's.
 //
 // block_pair_kernel: more rows, on CTA pairs (see pairop_kernels.cuh for the
 // pair protocol): 256 hidden rows x 256 vocabulary rows a unit, a thread holds
 // one hidden row's 128 logits of one vocabulary tile, so its scales are one
-// value of its row and one of the tile a block.
+// value of its row and one of the tile a block. Bound by the drains: 2048 rows x
+// 128256 x 4096 in 915 us, 2.35 PFLOP/s (a block of K every 0.54 us; the four
+// pairs of MMAs alone take 0.27 at 1.9 GHz, and without tensor-memory reads and
+// sums the kernel takes 609 us). A drain's sums are 64 packed multiply-adds of
+// each of two warps a scheduler, a quarter of a microsecond at full rate, and the
+// waits around them do not hide behind two warps. What it took: accumulator slots
+// by vocabulary tile, so that the two tiles' warps come one after the other (985
+// -> 975 us); no spilled registers (-> 936; 232 a thread -> 915); two threads
+// issuing (no change). Slower: sixteen warps of 64 columns with 104 registers
+// (2402: they spill), row scales loaded four at a time (999 to 1047), single
+// multiply-adds (979), the loop unrolled by the two slots (1690: spills).
 #pragma once
 #include "pairop_kernels.cuh"
 
@@ -461,11 +477,10 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int half = static_cast<int>(rank) * kRowsHalf;
-  const UnitWalk first(pair, n_pairs, p.n1);       // r: hidden-row tile, q: vocabulary tile of 256
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_normal();
       const uint64_t pol_x = policy_evict_last();
@@ -473,10 +488,11 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       grid_dep_wait();
       uint32_t stage = 0, phase = 0, outstanding = 0, out_par = 0;
       bool ok = true;
-      for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
-        const int n0 = w.r * 256 + half, v0 = w.q * 256 + half / 2;
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
+        const int vt = u / p.n1, rt = u - vt * p.n1;
+        const int n0 = rt * 256 + half, v0 = vt * 256 + half / 2;
         // the peer's hidden rows may not exist: its box is not loaded then
-        const uint32_t bytes = (2u + (w.r * 256 + kRowsHalf < p.B ? 2u : 1u)) * kRowsHalf * kRowBytes;
+        const uint32_t bytes = (2u + (rt * 256 + kRowsHalf < p.B ? 2u : 1u)) * kRowsHalf * kRowBytes;
         for (int c = 0; c < p.nk; ++c) {
           const uint32_t fb = cluster_addr(full_bar(stage), 0);
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
@@ -508,20 +524,20 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     __syncwarp();
   } else if (warp < 3) {
     // ------------------------------------------------------ MMA issuers
-    // One thread's waits, four MMAs and two commits take some 950 cycles a
-    // block of K, the MMAs themselves 512: warps 1 and 2 issue every second
-    // block, each into its own accumulator slot. A thread waits for its slot
-    // before it looks at the stage: the slot is free once the block before the
-    // last is drained, and so, as blocks are drained in order, is the one that
-    // was in the stage before; the stage's parity then means this block.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
+    // One thread's waits, MMAs and commits take about 950 cycles a block of K, the
+    // MMAs themselves 512: warps 1 and 2 issue every second block, each into its
+    // own accumulator slots, one of each vocabulary tile. When a thread comes to
+    // block c it has issued c - 2, whose slots were free once c - 4 was drained:
+    // blocks are drained in order, so with four stages or more (the host makes no
+    // fewer) what was in c's stage before is done, and the stage's parity means c.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
     if (lane == 0 && rank == 0) {
       const uint32_t slot = static_cast<uint32_t>(warp - 1);
       uint32_t stage = slot, phase = 0, sph = 0;
       bool ok = true;
       if (p.stall) ok = mbar_wait(never_bar, 0, abort_flag, p.timeout_ns);
       int c = static_cast<int>(slot);            // this thread's block in the unit
-      for (UnitWalk w = first; w.u < p.units && ok; w.next()) {
+      for (int u = pair; u < p.units && ok; u += n_pairs) {
         for (; c < p.nk; c += 2) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
           const uint64_t da = sdesc_sw128(sX(stage));
@@ -555,18 +571,16 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     __syncwarp();
   } else if (warp < 4) {
     // warp 3: no role, fewer registers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOpRegsWg0));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsWg0Wide));
   } else {
     // --------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kOpRegsEpi));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsEpiWide));
     grid_dep_wait();
     const int q = warp & 3;                    // TMEM lane quarter
     const int g = (warp - 4) >> 2;             // vocabulary tile of the unit
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
     uint32_t slot = 0, sph = 0;
     bool failed = false;
-    // (registers are what these warps are short of: a unit's place is divided out
-    // again, not walked along)
     for (int u = pair; u < p.units; u += n_pairs) {
       const int vt = u / p.n1;
       const int nw0 = (u - vt * p.n1) * 256 + half + q * 32;   // the warp's first row

