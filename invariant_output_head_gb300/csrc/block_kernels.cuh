@@ -305,6 +305,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     const int n_first = (warp - 2) / 4 * NW;   // first column: a hidden row
     const int et = threadIdx.x - 64;
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
+    grid_dep_wait();                           // the scales are the previous kernels' outputs
     for (int i = et; i < p.nk * N; i += ET) {
       const int c = i / N, n = i - (i / N) * N;
       sx[i] = n < p.B ? p.x_scale[static_cast<size_t>(n) * p.nk + c] : 0.0f;
@@ -321,13 +322,13 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
       for (int i = 0; i < NW / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       float sw[KPS];
 #pragma unroll
-      for (int b = 0; b < KPS; ++b) sw[b] = b < p.nk ? __ldg(ws + b) : 0.0f;
+      for (int b = 0; b < KPS; ++b) sw[b] = b < p.nk ? ws[b] : 0.0f;
       for (int st = 0; st < steps; ++st) {
         float sw_next[KPS];
 #pragma unroll
         for (int b = 0; b < KPS; ++b) {
           const int c = (st + 1) * KPS + b;
-          sw_next[b] = c < p.nk ? __ldg(ws + c) : 0.0f;
+          sw_next[b] = c < p.nk ? ws[c] : 0.0f;
         }
         const uint32_t cur = slot, cph = sph;
         if (++slot == static_cast<uint32_t>(SL)) { slot = 0; sph ^= 1u; }
@@ -593,12 +594,12 @@ block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       float acc[8][16];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i >> 4][i & 15] = 0.0f;
-      float sx = __ldg(xs), sw = __ldg(ws);
+      float sx = xs[0], sw = ws[0];
       for (int c = 0; c < p.nk; ++c) {
         const float s = __fmul_rn(sx, sw);
         if (c + 1 < p.nk) {
-          sx = __ldg(xs + c + 1);
-          sw = __ldg(ws + c + 1);
+          sx = xs[c + 1];
+          sw = ws[c + 1];
         }
         const uint32_t cur = 2u * slot + g, cph = sph;
         if (++slot == 2u) { slot = 0; sph ^= 1u; }

@@ -267,3 +267,28 @@ def test_addresses_that_are_refused(t):
     bytes_ = t.zeros(300, dtype=t.uint8, device="cuda")
     with pytest.raises(DetlmError):
         Head(W).block_scaled_logits(bytes_[8:136].view(t.float8_e4m3fn).view(2, 64), xs, ws)
+
+
+@pytest.mark.parametrize("B", [5, 100, 200])
+def test_rows_quantised_right_before_the_call(t, B):
+    """The quantisation of many rows is still under way when the product of the
+    last of them is launched: it reads the rows and scales of this quantisation,
+    not of the one before."""
+    from invariant_output_head_gb300 import Head, block_buffers, quantize_blocks
+    n, d, V = 6000, 8192, 1000
+    g = t.Generator(device="cuda").manual_seed(B)
+    W = t.randn(V, d, device="cuda", generator=g).mul_(60).clamp_(-448, 448).to(t.float8_e4m3fn)
+    head = Head(W)
+    ws = t.rand(8, 64, device="cuda", generator=g) + 0.5
+    xs = [t.randn(n, d, device="cuda", generator=g) * 10.0 ** (4 * i) for i in range(2)]
+    want = []
+    for x in xs:
+        q, s = quantize_blocks(x)
+        t.cuda.synchronize()
+        want.append(head.block_scaled_logits(q[-B:], s[-B:], ws))
+        t.cuda.synchronize()
+    out = block_buffers(n, d, device="cuda")
+    for i in range(20):
+        quantize_blocks(xs[i % 2], out=out)
+        got = head.block_scaled_logits(out[0][-B:], out[1][-B:], ws)
+        assert t.equal(got, want[i % 2])
