@@ -21,7 +21,7 @@ cudaError_t launch_block_gemm(const CUtensorMap& w, const CUtensorMap& g, const 
   while (p.stages > 2 && block_layout(N, p.stages, p.nk).total + 1024u > kSmemLimit) --p.stages;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  const int64_t groups = (p.V + kBlockGroup - 1) / kBlockGroup;
+  const int64_t groups = (static_cast<int64_t>(p.V) + kBlockGroup - 1) / kBlockGroup;
   cfg.gridDim = dim3(static_cast<unsigned>(groups < sms ? groups : sms));
   cfg.blockDim = dim3(block_threads(N));
   cfg.dynamicSmemBytes = block_layout(N, p.stages, p.nk).total + 1024u;

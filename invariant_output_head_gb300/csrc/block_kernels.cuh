@@ -173,7 +173,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     return sW(s, KPS) + static_cast<uint32_t>(b) * (N * kRowBytes);
   };
 
-  const int64_t groups = (p.V + kBlockGroup - 1) / kBlockGroup;
+  const int64_t groups = (static_cast<int64_t>(p.V) + kBlockGroup - 1) / kBlockGroup;
   const int g0 = static_cast<int>(groups * blockIdx.x / gridDim.x);
   const int g1 = static_cast<int>(groups * (blockIdx.x + 1) / gridDim.x);
   const int steps = (p.nk + KPS - 1) / KPS;
@@ -315,7 +315,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     bool failed = false;
     for (int g = g0; g < g1; g += 4) {
       const bool mine = g + q < g1;            // this warp's group exists
-      const int v = (g + q) * kBlockGroup + lane;
+      const int v = mine ? (g + q) * kBlockGroup + lane : 0;
       const float* ws = p.w_scale + static_cast<size_t>(mine ? (g + q) / (kBM / kBlockGroup) : 0) * p.nk;
       float2 acc[NW / 2];
 #pragma unroll

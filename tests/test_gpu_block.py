@@ -292,3 +292,24 @@ def test_rows_quantised_right_before_the_call(t, B):
         quantize_blocks(xs[i % 2], out=out)
         got = head.block_scaled_logits(out[0][-B:], out[1][-B:], ws)
         assert t.equal(got, want[i % 2])
+
+
+def test_a_vocabulary_of_the_largest_size(t):
+    """V = 2^31 - 1: the last group of rows ends one short of 2^31."""
+    from invariant_output_head_gb300 import Head
+    if t.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough free memory")
+    V, d = 2 ** 31 - 1, 16
+    W = t.zeros(V, d, dtype=t.uint8, device="cuda")
+    at = [0, 31, 2 ** 30 + 5, V - 40, V - 1]
+    for i, v in enumerate(at):
+        W[v] = 0x38 + 8 * i                       # 2^i
+    ws = t.ones(2 ** 24, 1, device="cuda")
+    ws[-1] = 0.5
+    q = t.full((1, d), 0x38, dtype=t.uint8, device="cuda").view(t.float8_e4m3fn)
+    out = t.full((1, V), 7.0, dtype=t.bfloat16, device="cuda")
+    Head(W.view(t.float8_e4m3fn)).block_scaled_logits(q, t.ones(1, 1, device="cuda"), ws, out=out)
+    assert [float(out[0, v]) for v in at] == [16.0, 32.0, 64.0, 64.0, 128.0]
+    for v in at:
+        out[0, v] = 0.0
+    assert not bool(out.view(t.int16).any())
