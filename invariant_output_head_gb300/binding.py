@@ -724,6 +724,9 @@ class Head:
             _matrix(out.parent, "out.parent", (n_seq, n_out), torch.int32, device)
             _matrix(out.token, "out.token", (n_seq, n_out), torch.int32, device)
             _matrix(out.score, "out.score", (n_seq, n_out), torch.float32, device)
+            gap = out.score.data_ptr() - scores.data_ptr()
+            if -4 * out.score.numel() < gap < 4 * scores.numel() and (gap or n_out != beams):
+                raise ValueError("out.score must be scores, or apart from it")
         _on_device(scores, lambda: detlm_head_beam_select(
             self.handle, logits.data_ptr(), code, scores.data_ptr(), _ptr(finished), end_token,
             n_seq, beams, n_out, temperature, out.parent.data_ptr(), out.token.data_ptr(),
@@ -733,7 +736,7 @@ class Head:
     def reserve_beams(self, max_rows: int, n_out: int) -> None:
         """Workspace for selections of up to max_rows = n_seq * beams rows and
         n_out continuations."""
-        detlm_head_reserve_beams(self.handle, int(max_rows), int(n_out))
+        _on_device(self.W, lambda: detlm_head_reserve_beams(self.handle, int(max_rows), int(n_out)))
 
     @_on_its_stream
     def greedy_gated(self, h, tau: float = 0.001, with_logits: bool = False, stream=None):
@@ -875,10 +878,45 @@ def _pieces(t, axis):
     return dims[0][1], step or 0, n_seg, each, positions
 
 
-def _range(t):
-    """First and last byte of a tensor's elements, plus one."""
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _shared(a, b=None):
+    """Whether two states' rows (address, row step, rows, piece step, pieces,
+    bytes of a piece) share a byte; of one state: whether two of its pieces do.
+    Exact for states of one layout and for rows that lie apart; other states
+    whose memory interleaves count as sharing it."""
+    own, b = b is None, a if b is None else b
+    extent = [(n - 1) * seg + size for _, _, _, seg, n, size in (a, b)]   # of a row
+    at = b[0] - a[0]
+    if not own and (at >= (a[2] - 1) * a[1] + extent[0] or -at >= (b[2] - 1) * b[1] + extent[1]):
+        return False
+    step, seg, size = a[1], a[3], a[5]
+    if b[1] != step and a[2] > 1 and b[2] > 1:
+        return True
+    if b[2] > 1:
+        step = b[1]
+    if a[2] == b[2] == 1:
+        step = sum(extent)                       # (any)
+    if step == 0:
+        return True
+    # rows of b that lie `first` to `last` rows from one of a and reach into it
+    first = max(1 - a[2], -((at + extent[1] - 1) // step))
+    last = min(b[2] - 1, (extent[0] - 1 - at) // step)
+    for d in range(first, last + 1):
+        off = at + d * step
+        if b[3:] != a[3:]:
+            return True
+        if a[4] == 1:
+            if not (own and d == 0):
+                return True
+            continue
+        # pieces of b that lie k pieces from one of a
+        near = -off // seg if seg else 0
+        for k in (near, near + 1):
+            k = max(1 - a[4], min(a[4] - 1, k))
+            if abs(off + k * seg) < size and not (own and d == 0 and k == 0):
+                return True
+        if own and d == 0 and seg < size:
+            return True
+    return False
 
 
 class BeamStates:
@@ -890,8 +928,8 @@ class BeamStates:
     beams). token_dim names the axis of positions of each state (one number, or
     one a state, None for a state without), of which reorder(used=n) moves the
     first n. A row has to be equal contiguous pieces (any one axis, or several
-    that make one, strided). The tensors are kept; their addresses and strides
-    are read once, here.
+    that make one, strided), and no two states share memory, nor out any with the
+    states. The tensors are kept; their addresses and strides are read once, here.
     """
 
     def __init__(self, states, out=None, token_dim=None):
@@ -932,16 +970,20 @@ class BeamStates:
         self._check_overlap(out is None)
 
     def _check_overlap(self, in_place):
-        outs = [o for o in self.out if o.numel()]
-        if len({o.data_ptr() for o in outs}) < len(outs):
-            raise ValueError("the same tensor twice")
-        if any(n > 1 and s == 0 for o in outs for n, s in zip(o.shape, o.stride())):
-            raise ValueError("an output has more than one element at one place")
+        rows = [(e.dst, e.dst_row, self.rows_out, e.dst_seg, e.n_seg, e.seg_bytes)
+                for e in self._table if e.n_seg and self.rows_out]
+        for i, a in enumerate(rows):
+            if _shared(a):
+                raise ValueError("an output has more than one element at one place")
+            for b in rows[:i]:
+                if _shared(a, b):
+                    raise ValueError("two states share memory")
         if in_place:
             return
-        for a, b in map(_range, outs):
-            for c, d in (_range(s) for s in self.states if s.numel()):
-                if a < d and c < b:
+        for a in rows:
+            for e in self._table:
+                if e.n_seg and _shared(a, (e.src, e.src_row, self.rows_in, e.src_seg, e.n_seg,
+                                           e.seg_bytes)):
                     raise ValueError("out overlaps a state")
 
     def reorder(self, parent, used: int | None = None, stream=None) -> None:

@@ -2,6 +2,7 @@
 the layout of states."""
 import ctypes
 import math
+import random
 
 import pytest
 
@@ -257,6 +258,57 @@ def test_states_layouts_and_refusals(calls):
         b.BeamStates([cache[:, :, :5, ::2]])             # pieces at two strides
     with pytest.raises(ValueError):
         b.BeamStates([cache], out=[fake(1, 3, 20, 16, dtype=torch.bfloat16).expand(8, 3, 20, 16)])
+
+
+def test_selection_over_part_of_its_scores_is_refused(calls):
+    head = head_of(fake(50, 16, dtype=torch.bfloat16), "bf16")
+    z, pool = fake(12, 50), fake(40)
+    i32 = [fake(3, n, dtype=torch.int32) for n in (4, 4, 8, 8)]
+    s = pool[8:20].view(3, 4)
+    head.beam_select(z, s, 4, out=b.Beams(*i32[:2], s))
+    head.beam_select(z, s, 4, out=b.Beams(*i32[:2], pool[20:32].view(3, 4)))
+    assert len(calls) == 2
+    for n, score in ((4, pool[9:21]), (4, pool[:12]), (8, pool[8:32]), (8, pool[:24])):
+        with pytest.raises(ValueError):
+            head.beam_select(z, s, n, out=b.Beams(*i32[n // 2 - 2:][:2], score.view(3, n)))
+    assert len(calls) == 2
+
+
+def test_states_that_share_memory_are_refused(calls):
+    both = fake(8, 2, 3, 20, 16)
+    flat = both.view(-1)
+    kv = fake(8, 3, 32)
+    turned = fake(3, 8, 40).transpose(0, 1)              # pieces of all rows between a row's
+    b.BeamStates([turned, kv[..., :16], kv[..., 16:]])
+    b.BeamStates([both[:, 0]], out=[both[:, 1]])
+    b.BeamStates([flat[:640].view(8, 80), flat[640:1280].view(8, 80)])
+    for states in ([both[:, 0], both], [both[:, 0], both[:, 0, 1:]], [both[:, 0], both[:, :, 2]],
+                   [flat[:640].view(8, 80), flat[639:1279].view(8, 80)], [flat.unfold(0, 80, 40)],
+                   [kv[..., :17], kv[..., 16:]], [turned, turned[:, 1:]],
+                   [turned[:, :, :20], turned[:, :, 19:]]):
+        with pytest.raises(ValueError):
+            b.BeamStates(states)
+    with pytest.raises(ValueError):
+        b.BeamStates([both[:4, 0]], out=[both[3:7, 0]])
+    # every layout of a few bytes against the bytes themselves
+    def places(p, step, rows, seg, n, size):
+        return [p + r * step + k * seg + i for r in range(rows) for k in range(n) for i in range(size)]
+    rng = random.Random(5)
+    found = [0, 0]
+    for _ in range(4000):
+        n = rng.randint(1, 3)
+        layout = (rng.choice([1, 2, 4, 6, 8, 12]), rng.randint(1, 4),
+                  rng.choice([2, 3, 6, 12]) if n > 1 else 0, n, rng.randint(1, 3))
+        one = (100, *layout)
+        two = (100 + rng.randint(-30, 30), layout[0], rng.randint(1, 4), *layout[2:])
+        mine = places(*one)
+        assert b._shared(one) == (len(set(mine)) < len(mine))
+        if b._shared(one) or b._shared(two):
+            continue
+        shared = b._shared(one, two)
+        assert shared == bool(set(mine) & set(places(*two)))
+        found[shared] += 1
+    assert min(found) > 200
 
 
 # ------------------------------------------------------------------- reference
