@@ -49,6 +49,7 @@ constexpr int kScanTile = 1024;           // logits of a tile: 32 a lane
 constexpr int kScanPer = kScanTile / 32;
 constexpr int kScanRound = kScanWarps * kScanTile;
 constexpr int kScanCap = 1024;            // entries of the list
+constexpr float kFusedMost = 16777216.0f; // largest |maximum| log2(e) / T of a tile summed in fused form
 // blocks of an SM (their registers: a tile and the next)
 __host__ __device__ constexpr int scan_resident(int fmt) { return fmt == QF_FP32 ? 2 : 3; }
 
@@ -341,12 +342,16 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
             }
           }
         }
-        // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf
+        // the tile's sum: 0 where it holds nothing but -inf, NaN with a NaN or +inf.
+        // The rounding of base c is at most half a step of it, so up to 2^24 the
+        // factor that puts it back is between 2^-1/2 and 2^1/2; from 2^32 on it can
+        // be 0 or infinite (a tile masked with -1e10, or with the type's lowest
+        // value at T = 2), so large maxima take the difference first.
         m = score_unkey(__reduce_max_sync(0xffffffffu, score_key(m)));
         const float base = m == -INFINITY ? 0.0f : m;
         const float e0 = __fmul_rn(base, p.c);
         float sum;
-        if (fabsf(e0) < INFINITY) {
+        if (fabsf(e0) < kFusedMost) {
           // x c - e0 in one rounding; e0 is off base c by what the factor puts back
           sum = scan_sum(x, [&](float2 v) {
             return fma2_rn(v, make_float2(p.c, p.c), make_float2(-e0, -e0));

@@ -1,0 +1,158 @@
+"""Beam selection's sums and scores at logits of every magnitude: whole tiles
+masked with large negative numbers, temperatures from tiny to huge."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+TILE = 1024                                   # logits that the call sums at a time
+
+
+@pytest.fixture(scope="module")
+def t():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch
+
+
+def head_of(t, V):
+    from invariant_output_head_gb300 import Head
+    return Head(t.zeros(V, 16, dtype=t.bfloat16, device="cuda"))
+
+
+def sum_bound(V, E):
+    """Bound on the relative error of a row's sum S of 2^x, x = (z - m) log2(e) /
+    T, in half-steps u = 2^-24. Every x is made of parts of one sign (to a tile's
+    maximum, then from join to join to the row's), each a difference (1), times
+    a rounded log2(e) / T (3: 1 / T, log2(e), their product), rounded (1): 5 u of
+    |x| ln 2, which over the sum is 5 E with E the mean of |z - m| / T under the
+    softmax. In the fused form a tile's exponents are off by up to 1/2 from that,
+    u / 2 more, and a factor puts it back: one 2^x (4: it is good to 2^-22) and a
+    product (1). 2^x of an element: 4. Additions in a tile: 3 + 3 + 5. A join: 2^x
+    (4), product, addition; as many as a lane has tiles, and 5."""
+    joins = -(-(-(-V // TILE)) // 32) + 5
+    return 0.5 + 5 + 4 + 11 + 6 * joins + 5 * E
+
+
+def check_each(t, head, z, s, n_out, T=1.0):
+    """The call against 64 bits, every candidate within its own bound: its score
+    from its own distance to its row's maximum; each beam's candidates the first
+    of its own by (logit falling, token); all of them in order, and none that
+    is better left out."""
+    n_seq, beams = s.shape
+    V = z.shape[1]
+    got = head.beam_select(z.cuda(), s.cuda(), n_out, temperature=T)
+    assert head.check() == 0
+    parent, token, score = (x.cpu() for x in got)
+    u, T = 2.0 ** -24, float(t.tensor(T, dtype=t.float32))
+    for q in range(n_seq):
+        total, bound, order = [], [], []
+        for b in range(beams):
+            row, own = z[q * beams + b].double(), float(s[q, b])
+            m = float(row.max())
+            if not math.isfinite(own) or math.isnan(m) or math.isinf(m):
+                total.append(t.full((V,), -math.inf, dtype=t.float64))
+                bound.append(t.zeros(V, dtype=t.float64))
+            else:
+                far = (row - m) / T
+                p = t.softmax(far, dim=0)
+                L = float(t.logsumexp(far, dim=0))
+                E = float((p * -far.clamp_min(-1e300)).sum())
+                x = far - L + own
+                D = -far
+                total.append(x)
+                # difference, 1 / T and product; logf (an ulp) of S; the two sums;
+                # products of u left out: 1 %
+                bound.append(1.01 * u * (3 * D + sum_bound(V, E) + 2 * L + (D + L) + x.abs()) + 2.0 ** -148)
+            order.append(t.sort(row, descending=True, stable=True).indices)
+        total, bound = t.stack(total), t.stack(bound)
+        total[total.float() == -math.inf] = -math.inf        # no number in 32 bits
+        want = total.view(-1).sort(descending=True).values[:n_out]
+        real = int((want > -math.inf).sum())
+        assert parent[q, real:].tolist() == [-1] * (n_out - real), q
+        assert token[q, real:].tolist() == [-1] * (n_out - real), q
+        assert score[q, real:].tolist() == [-math.inf] * (n_out - real), q
+        assert bool((parent[q, :real] >= 0).all()) and bool((score[q, :real] > -math.inf).all()), q
+        p, v, x = parent[q, :real].long(), token[q, :real].long(), score[q, :real]
+        tol = bound[p, v]
+        assert bool(((x.double() - total[p, v]).abs() <= tol).all()), \
+            (q, float(((x.double() - total[p, v]).abs() / tol).max()))
+        assert bool((x[:-1] >= x[1:]).all())
+        assert bool(((total[p, v] - want[:real]).abs() <= 2 * tol.maximum(bound.view(-1)[
+            total.view(-1).sort(descending=True).indices[:real]])).all()), q
+        for b in range(beams):
+            mine = v[p == b]
+            assert t.equal(mine, order[b][:len(mine)]), (q, b)
+    return got
+
+
+def rows(t, n, V, dtype, seed):
+    g = t.Generator().manual_seed(seed)
+    return (t.randn(n, V, generator=g) * 2.5).to(dtype)
+
+
+FILLS = ["low", -1e9, -1e10, -1e12, -1e30, -math.inf]
+
+
+@pytest.mark.parametrize("T", [0.1, 0.3, 1.0, 1.5, 2.0, 30.0])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("name", ["float32", "bfloat16", "float16"])
+def test_whole_tiles_masked(t, name, fill, T):
+    """The first tile, some in the middle, the last (of one logit and of
+    many), all but one, in the rows of one sequence; more rows so that tiles
+    fall to parts of every length."""
+    dtype = getattr(t, name)
+    fill = max(t.finfo(dtype).min if fill == "low" else fill,
+               -math.inf if fill == -math.inf else t.finfo(dtype).min)
+    for V in (8 * TILE + 1, 5 * TILE + 700, TILE + 1):
+        z = rows(t, 6, V, dtype, V)
+        z[0, :TILE] = fill
+        z[1, 2 * TILE:4 * TILE] = fill
+        z[2, V // TILE * TILE:] = fill
+        z[3, TILE:] = fill
+        z[4, :V // TILE * TILE] = fill
+        s = -t.rand(1, 6, generator=t.Generator().manual_seed(V)) * 4
+        head = head_of(t, V)
+        # a sequence of its own for each (a beam that is lost shows), and together
+        check_each(t, head, z, s.view(6, 1), 12, T)
+        check_each(t, head, z, s, 40, T)
+
+
+@pytest.mark.parametrize("T", [5e-39, 1e-20, 1e-8, 1e-5, 1e-3, 1e8])
+@pytest.mark.parametrize("name", ["float32", "bfloat16", "float16"])
+def test_extreme_temperatures(t, name, T):
+    """Logits of ordinary size, whose distances to the maximum do not stay so."""
+    for V in (3000, 9000):
+        z = rows(t, 4, V, getattr(t, name), 3) + 20
+        check_each(t, head_of(t, V), z, t.tensor([[-0.5], [-1.0], [-2.0], [0.0]]), 16, T)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.7, 3.0])
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+@pytest.mark.parametrize("at", [1e4, 1e7, 3e8, -3e8, 1e10, -1e10, 1e20, -1e30])
+def test_logits_far_from_zero(t, name, at, T):
+    """Whole rows about one large number, on its steps: exponents on both sides
+    of where the form of a tile's sum changes."""
+    dtype = getattr(t, name)
+    V = 4 * TILE + 3
+    base = t.tensor(at, dtype=dtype)
+    step = abs(float(base.double())) * 2.0 ** (-23 if dtype == t.float32 else -7)
+    k = t.randint(-3, 4, (3, V), generator=t.Generator().manual_seed(7))
+    z = (base.double() + k * step).to(dtype)
+    check_each(t, head_of(t, V), z, t.tensor([[-0.5], [-1.0], [-2.0]]), 10, T)
+
+
+def test_one_masked_tile_leaves_other_rows_bits(t):
+    """A row's bits are its own: masked tiles beside it change nothing."""
+    V = 6 * TILE
+    z = rows(t, 8, V, t.bfloat16, 1)
+    s = t.zeros(8, 1)
+    head = head_of(t, V)
+    before = head.beam_select(z.cuda(), s.cuda(), 8)
+    z[3, TILE:3 * TILE] = -1e30
+    after = head.beam_select(z.cuda(), s.cuda(), 8)
+    keep = [0, 1, 2, 4, 5, 6, 7]
+    assert all(t.equal(a[keep], b[keep]) for a, b in zip(before, after))
+    assert (after.parent[3] == 0).all()
