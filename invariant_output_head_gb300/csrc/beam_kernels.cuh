@@ -413,11 +413,18 @@ __global__ void __launch_bounds__(kScanThreads, scan_resident(FMT)) beam_scan_ke
   grid_dep_launch();
 }
 
+// (x - m) f for a finite m, by halves: the difference of two numbers may be past
+// fp32 where its product is not (+-3e38 at T = 1e38). Otherwise the same bits.
+__device__ __forceinline__ float far_times(float x, float m, float f) {
+  const float y = __fmul_rn(__fmaf_rn(0.5f, x, __fmul_rn(-0.5f, m)), f);
+  return __fadd_rn(y, y);
+}
+
 // Two tiles' maximum and sum as one (the same bits in either order).
 __device__ __forceinline__ float2 tile_join(float2 a, float2 b, float c) {
   const float m = fmaxf(a.x, b.x);
-  const float fa = a.x == m ? 1.0f : exp2_approx((a.x - m) * c);
-  const float fb = b.x == m ? 1.0f : exp2_approx((b.x - m) * c);
+  const float fa = a.x == m ? 1.0f : exp2_approx(far_times(a.x, m, c));
+  const float fb = b.x == m ? 1.0f : exp2_approx(far_times(b.x, m, c));
   return make_float2(m, __fadd_rn(__fmul_rn(a.y, fa), __fmul_rn(b.y, fb)));
 }
 
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kMergeBeamThreads) beam_merge_kernel(const Bea
         for (int k = 0; k < n; ++k) rank += list[k] > word;
         if (rank >= M) continue;
         const float z = score_unkey(static_cast<uint32_t>(word >> 32));
-        const float s = __fadd_rn(own, __fsub_rn(__fmul_rn(__fsub_rn(z, t.x), p.inv_t), log_s));
+        const float s = __fadd_rn(own, __fsub_rn(far_times(z, t.x, p.inv_t), log_s));
         if (!(s > -INFINITY)) continue;        // (and those behind it score no more)
         score[b * M + rank] = s;
         token[b * M + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(word));

@@ -22,18 +22,18 @@ def head_of(t, V):
     return Head(t.zeros(V, 16, dtype=t.bfloat16, device="cuda"))
 
 
-def sum_bound(V, E):
+def sum_bound(V, E, f):
     """Bound on the relative error of a row's sum S of 2^x, x = (z - m) log2(e) /
     T, in half-steps u = 2^-24. Every x is made of parts of one sign (to a tile's
     maximum, then from join to join to the row's), each a difference (1), times
-    a rounded log2(e) / T (3: 1 / T, log2(e), their product), rounded (1): 5 u of
-    |x| ln 2, which over the sum is 5 E with E the mean of |z - m| / T under the
-    softmax. In the fused form a tile's exponents are off by up to 1/2 from that,
+    a rounded log2(e) / T (1 / T is off by f, log2(e) by 1, their product by f
+    again), rounded (1): (3 + 2 f) u of |x| ln 2, which over the sum is (3 + 2 f) E
+    with E the mean of |z - m| / T under the softmax. In the fused form a tile's exponents are off by up to 1/2 from that,
     u / 2 more, and a factor puts it back: one 2^x (4: it is good to 2^-22) and a
     product (1). 2^x of an element: 4. Additions in a tile: 3 + 3 + 5. A join: 2^x
     (4), product, addition; as many as a lane has tiles, and 5."""
     joins = -(-(-(-V // TILE)) // 32) + 5
-    return 0.5 + 5 + 4 + 11 + 6 * joins + 5 * E
+    return 0.5 + 5 + 4 + 11 + 6 * joins + (3 + 2 * f) * E
 
 
 def check_each(t, head, z, s, n_out, T=1.0):
@@ -47,6 +47,7 @@ def check_each(t, head, z, s, n_out, T=1.0):
     assert head.check() == 0
     parent, token, score = (x.cpu() for x in got)
     u, T = 2.0 ** -24, float(t.tensor(T, dtype=t.float32))
+    f = max(1.0, T * 2.0 ** -126)             # 1 / T in 32 bits: half-steps of it (more below 2^-126)
     for q in range(n_seq):
         total, bound, order = [], [], []
         for b in range(beams):
@@ -65,7 +66,7 @@ def check_each(t, head, z, s, n_out, T=1.0):
                 total.append(x)
                 # difference, 1 / T and product; logf (an ulp) of S; the two sums;
                 # products of u left out: 1 %
-                bound.append(1.01 * u * (3 * D + sum_bound(V, E) + 2 * L + (D + L) + x.abs()) + 2.0 ** -148)
+                bound.append(1.01 * u * ((2 + f) * D + sum_bound(V, E, f) + 2 * L + (D + L) + x.abs()) + 2.0 ** -148)
             order.append(t.sort(row, descending=True, stable=True).indices)
         total, bound = t.stack(total), t.stack(bound)
         total[total.float() == -math.inf] = -math.inf        # no number in 32 bits
@@ -156,3 +157,17 @@ def test_one_masked_tile_leaves_other_rows_bits(t):
     keep = [0, 1, 2, 4, 5, 6, 7]
     assert all(t.equal(a[keep], b[keep]) for a, b in zip(before, after))
     assert (after.parent[3] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1.0, 2.0, 8.0, 1e30, 1e37, 1e38, 3e38])
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+def test_logits_farther_apart_than_32_bits_hold(t, name, T):
+    """Logits of both ends of the type's range: their difference overflows, the
+    scores and the weights in the sum need not."""
+    V = 5 * TILE + 9
+    z = t.rand(4, V, generator=t.Generator().manual_seed(2)) * 6e38 - 3e38
+    z[1, :3 * TILE] = -3.3e38               # tiles at the two ends
+    z[1, 3 * TILE:] = 3.3e38
+    z[2, :-1], z[2, -1] = t.finfo(getattr(t, name)).min, 1e38
+    z[3, 5:] = -math.inf
+    check_each(t, head_of(t, V), z.to(getattr(t, name)), t.tensor([[-0.5], [-1.0], [-2.0], [0.0]]), 16, T)
