@@ -718,6 +718,11 @@ class Head:
             if finished.dtype not in (torch.bool, torch.uint8):
                 raise ValueError("finished must be a bool or uint8 tensor")
             _matrix(finished, "finished", (n_seq, beams), finished.dtype, device)
+            # (C integers would take the low bits of larger numbers, here and below)
+            if not 0 <= end_token < self.V:
+                raise DetlmError(DETLM_EINVAL, "beam_select: end_token")
+        if not 1 <= n_out <= DETLM_MAX_BEAM_OUT:
+            raise DetlmError(DETLM_EINVAL, "beam_select: n_out")
         if out is None:
             out = beam_buffers(n_seq, n_out, device)
         else:
@@ -736,6 +741,8 @@ class Head:
     def reserve_beams(self, max_rows: int, n_out: int) -> None:
         """Workspace for selections of up to max_rows = n_seq * beams rows and
         n_out continuations."""
+        if not 0 <= max_rows < 1 << 31 or not 1 <= n_out <= DETLM_MAX_BEAM_OUT:
+            raise DetlmError(DETLM_EINVAL, "reserve_beams")
         _on_device(self.W, lambda: detlm_head_reserve_beams(self.handle, int(max_rows), int(n_out)))
 
     @_on_its_stream
