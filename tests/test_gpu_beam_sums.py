@@ -36,14 +36,15 @@ def sum_bound(V, E, f):
     return 0.5 + 5 + 4 + 11 + 6 * joins + (3 + 2 * f) * E
 
 
-def check_each(t, head, z, s, n_out, T=1.0):
+def check_each(t, head, z, s, n_out, T=1.0, finished=None, end=0):
     """The call against 64 bits, every candidate within its own bound: its score
     from its own distance to its row's maximum; each beam's candidates the first
     of its own by (logit falling, token); all of them in order, and none that
     is better left out."""
     n_seq, beams = s.shape
     V = z.shape[1]
-    got = head.beam_select(z.cuda(), s.cuda(), n_out, temperature=T)
+    got = head.beam_select(z.cuda(), s.cuda(), n_out, temperature=T, end_token=end,
+                           finished=None if finished is None else finished.cuda())
     assert head.check() == 0
     parent, token, score = (x.cpu() for x in got)
     u, T = 2.0 ** -24, float(t.tensor(T, dtype=t.float32))
@@ -53,6 +54,13 @@ def check_each(t, head, z, s, n_out, T=1.0):
         for b in range(beams):
             row, own = z[q * beams + b].double(), float(s[q, b])
             m = float(row.max())
+            if finished is not None and bool(finished[q, b]) and math.isfinite(own):
+                # its own score, as it is, for the end token alone
+                total.append(t.full((V,), -math.inf, dtype=t.float64))
+                total[-1][end] = own
+                bound.append(t.zeros(V, dtype=t.float64))
+                order.append(t.tensor([end]))
+                continue
             if not math.isfinite(own) or math.isnan(m) or math.isinf(m):
                 total.append(t.full((V,), -math.inf, dtype=t.float64))
                 bound.append(t.zeros(V, dtype=t.float64))
@@ -171,3 +179,65 @@ def test_logits_farther_apart_than_32_bits_hold(t, name, T):
     z[2, :-1], z[2, -1] = t.finfo(getattr(t, name)).min, 1e38
     z[3, 5:] = -math.inf
     check_each(t, head_of(t, V), z.to(getattr(t, name)), t.tensor([[-0.5], [-1.0], [-2.0], [0.0]]), 16, T)
+
+
+@pytest.mark.parametrize("T", [0.7, 1.0, 2.5])
+@pytest.mark.parametrize("name", ["float32", "bfloat16", "float16"])
+def test_masked_finished_and_dead_beams_together(t, name, T):
+    dtype = getattr(t, name)
+    V = 9 * TILE + 77
+    z = rows(t, 24, V, dtype, 5)
+    low = t.finfo(dtype).min
+    z[0] = -math.inf                        # a row with nothing
+    z[1, 1:] = -math.inf                    # one token
+    z[2, :8 * TILE] = low
+    z[3, 100:] = max(-1e10, low)
+    z[4, 17], z[5, V - 1] = math.nan, math.inf
+    z[6] = low                              # every token alike
+    z[9, TILE:] = max(-1e30, low)
+    z[13, 5] = math.nan                     # of a finished beam: not read
+    s = -t.rand(6, 4, generator=t.Generator().manual_seed(6)) * 4 - 3
+    s[1, 1], s[1, 3], s[2, 0] = -math.inf, math.nan, math.inf
+    finished = t.zeros(6, 4, dtype=t.bool)
+    finished[2, 1] = finished[3, 1] = finished[5, 0] = finished[5, 1] = finished[5, 2] = True
+    finished[1, 1] = True                   # finished and dead: nothing
+    head = head_of(t, V)
+    for n_out, end in ((4, 0), (16, V - 1), (64, 3)):
+        check_each(t, head, z, s, n_out, T, finished, end)
+    check_each(t, head, z, s, 16, T, finished.to(t.uint8) * 128, 9)
+
+
+def test_outputs_in_page_locked_host_memory(t):
+    """As of the other calls: a device address of page-locked memory will do."""
+    from invariant_output_head_gb300 import binding as b
+    from invariant_output_head_gb300 import Head, quantize_blocks
+    g = t.Generator(device="cuda").manual_seed(4)
+    V, d, n, beams = 1000, 256, 50, 4
+    W, ws = quantize_blocks(t.randn(V, d, generator=g, device="cuda"), 128)
+    head = Head(W)
+    x = t.randn(n * beams, d, generator=g, device="cuda")
+    scores = -t.rand(n, beams, generator=g, device="cuda")
+    stream = t.cuda.current_stream().cuda_stream
+    for B in (3 * beams, n * beams):
+        q, xs = quantize_blocks(x[:B].contiguous())
+        z = head.block_scaled_logits(q, xs, ws)
+        r = head.beam_select(z, scores[:B // beams], beams)
+        rows_ = x[:B].clone()
+        b.BeamStates([rows_]).reorder(r.parent)
+        pin = [t.empty(v.shape, dtype=v.dtype).pin_memory() for v in (q, xs, z, *r, rows_)]
+        b.detlm_quantize_blocks(x.data_ptr(), b.DETLM_FP32, B, d, 1, pin[0].data_ptr(),
+                                pin[1].data_ptr(), stream)
+        b.detlm_head_block_scaled_logits(head.handle, q.data_ptr(), xs.data_ptr(), ws.data_ptr(), B,
+                                         b.DETLM_FP32, pin[2].data_ptr(), stream)
+        b.detlm_head_beam_select(head.handle, z.data_ptr(), b.DETLM_FP32, scores.data_ptr(), None, 0,
+                                 B // beams, beams, beams, 1.0, *(v.data_ptr() for v in pin[3:6]), stream)
+        state = (b._State * 1)()
+        e = state[0]
+        e.src, e.dst, e.src_row, e.dst_row = x.data_ptr(), pin[6].data_ptr(), 4 * d, 4 * d
+        e.n_seg, e.seg_bytes = 1, 4 * d
+        b.detlm_beam_reorder(b.ctypes.addressof(state), 1, r.parent.data_ptr(), B // beams, beams,
+                             beams, -1, stream)
+        t.cuda.synchronize()
+        assert head.check() == 0
+        for got, want in zip(pin, (q, xs, z, *r, rows_)):
+            assert t.equal(got.view(-1).view(t.uint8), want.cpu().view(-1).view(t.uint8))
