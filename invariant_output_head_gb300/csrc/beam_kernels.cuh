@@ -15,7 +15,7 @@
 // logits collect in shared memory: an element is kept if it is above the
 // smallest of the M = n_out best at the last cut, and the list is cut to M after
 // rounds 2, 4, 8, 16, ...: about M entries a span (16 sequences of 32 beams, M =
-// 64: 103 us; cut after 4, 16, 64: 115; the same at M = 16). The first threshold comes from
+// 64: 104 us; cut after 4, 16, 64: 115; the same at M = 16). The first threshold comes from
 // the first round itself: the M-th largest of 128 maxima of 64 elements each. An
 // element is compared as a 64-bit word: its order as a number, then the lower
 // index first. Warps meet at the cuts only.
@@ -24,12 +24,12 @@
 // a fixed tree and merges the parts' sorted lists, then the block merges the
 // beams' lists by score.
 //
-// What bounds the scan is instruction issue and the latency of its chains, not
-// memory: 64 sequences of 8 beams x 128256 in bf16, n_out = 16, 131 MB: 46 us of
-// the call's 49.5 (2.65 TB/s), 62 % of the issue slots busy with 24 warps an SM,
-// about 440 instructions a tile of 1024: some 130 the exponentials' sum, 180 the
-// loads, maxima and the rest, 130 the entries and cuts. Without entries and cuts
-// it would take 31. Tried and slower: tiles of 512 with 32 to 48 warps an SM
+// What the scan waits for is the latency of its chains, not memory: 64 sequences
+// of 8 beams x 128256 in bf16, n_out = 16, 131 MB: 49 us a call (2.7 TB/s), 55 %
+// of the issue slots busy with 24 warps an SM, about 440 instructions a tile of
+// 1024: some 130 the exponentials' sum, 180 the loads, maxima and the rest, 130
+// the entries and cuts (a lane with an entry takes its warp through the appends).
+// Without entries and cuts it would take 31. Tried and slower: tiles of 512 with 32 to 48 warps an SM
 // (54 to 64 us: the instructions a tile that do not depend on its size), tiles
 // staged three ahead by asynchronous copies (54: more instructions, and loads are
 // not what is waited for), whole rows or equal parts of rows for blocks (73: the

@@ -21,27 +21,30 @@
 // vocabulary in groups of 32 rows (whole tiles of 128 would leave the last round
 // of V = 32000 a third full): tiles of four groups, the last of fewer, whose
 // missing groups are not loaded. A warp's 32 rows lie in one block of w_scale.
-// Bound by the stream of W from memory: 32 rows x 128256 x 4096 in 80 us, 6.66
-// TB/s of the 6.78 that a copy reaches, 1 row 79; one row of 32000 x 2048 in 14.2
-// us, of which some 4.5 are the launch, the first boxes' latency and the last
-// drain. W's first boxes are requested before the prologue (82.8 us without). Up
-// to 64 rows a row more costs nothing (84 us); at 96 and 128 (97 and 113) the
-// hidden rows' boxes, which every SM reads from L2, are as large as W's.
+// Bound by the stream of W from memory: 32 rows x 128256 x 4096 in 82 us, 6.48
+// TB/s of the 6.78 that a copy reaches; one row of 32000 x 2048 in 14.2 us, of
+// which some 4.5 are the launch, the first boxes' latency and the last drain. W's
+// first boxes are requested before the prologue (2 us more without). Up to 64
+// rows a row more costs nothing (86 us); at 96 and 128 (98 and 114) the hidden
+// rows' boxes, which every SM reads from L2, are as large as W's.
 //
 // block_pair_kernel: more rows, on CTA pairs (see pairop_kernels.cuh for the
 // pair protocol): 256 hidden rows x 256 vocabulary rows a unit, a thread holds
 // one hidden row's 128 logits of one vocabulary tile, so its scales are one
-// value of its row and one of the tile a block. Bound by the drains: 2048 rows x
-// 128256 x 4096 in 915 us, 2.35 PFLOP/s (a block of K every 0.54 us; the four
-// pairs of MMAs alone take 0.27 at 1.9 GHz, and without tensor-memory reads and
-// sums the kernel takes 609 us). A drain's sums are 64 packed multiply-adds of
-// each of two warps a scheduler, a quarter of a microsecond at full rate, and the
-// waits around them do not hide behind two warps. What it took: accumulator slots
-// by vocabulary tile, so that the two tiles' warps come one after the other (985
-// -> 975 us); no spilled registers (-> 936; 232 a thread -> 915); two threads
-// issuing (no change). Slower: sixteen warps of 64 columns with 104 registers
-// (2402: they spill), row scales loaded four at a time (999 to 1047), single
-// multiply-adds (979), the loop unrolled by the two slots (1690: spills).
+// value of its row and one of the tile a block. Bound by the drains, which run
+// nearly after the MMAs instead of beside them: 2048 rows x 128256 x 4096 in 915
+// to 925 us, 2.33 PFLOP/s, a block of K every 0.54 us, tensor pipe 45 %, issue
+// slots 40 %. The four pairs of MMAs alone take 0.27 us at 1.9 GHz (without
+// tensor-memory reads and sums the kernel takes 609 us), a drain's sums, 64 packed
+// multiply-adds of each of two warps a scheduler, 256 cycles or 0.135 us: both
+// would fit beside each other, but the reads and waits before the sums do not
+// hide behind two warps a scheduler. What it took: accumulator slots by vocabulary
+// tile, so that the two tiles' warps come one after the other (985 -> 975 us); no
+// spilled registers (-> 936; 232 a thread -> 915); two threads issuing (no change).
+// Slower: sixteen warps of 64 columns with 104 registers, read 32 at a time (2402:
+// they spill; 16 at a time is not tried), row scales loaded four at a time (999 to
+// 1047), single multiply-adds (974), the loop unrolled by the two slots (1690:
+// spills).
 #pragma once
 #include "pairop_kernels.cuh"
 
